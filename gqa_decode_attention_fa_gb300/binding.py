@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libgqa_decode.so (include/gqa_decode.h, gqa_prefill.h, gqa_q4.h).
+"""Thin ctypes binding over libgqa_decode.so (include/gqa_decode.h, gqa_prefill.h, gqa_q4.h,
+gqa_rope.h, gqa_tree.h, gqa_pages.h).
 
 Argument marshalling only: every step of the decode path runs in the library's CUDA
 kernels.  Device tensors are torch tensors (device memory and streams come from torch);
@@ -21,6 +22,8 @@ from . import build as _build
  GQA_ERR_SCRATCH_LIMIT) = range(6)
 STATIC_SCRATCH_BYTES = 32 << 20
 DEVERR_POSITION, DEVERR_SEQLEN, DEVERR_PAGE, DEVERR_TIMEOUT, DEVERR_LAUNCH = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_NOPAGE, DEVERR_CONFLICT = 0x20, 0x40
+MAX_TREE, MAX_POOLS, MAX_PAGE_PAIRS = 256, 256, 4096
 HEADER = os.path.join(_build.ROOT, "include", "gqa_decode.h")
 HEADERS = _build.HEADERS
 
@@ -44,6 +47,64 @@ class PrefillDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in (
         "batch", "num_q_heads", "num_kv_heads", "head_dim", "chunk_len", "block_size", "max_seq_len",
         "num_cache_blocks", "device")]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "num_tokens", "block_size", "max_seq_len",
+        "num_cache_blocks", "device", "q_stride", "k_stride", "v_stride")]
+
+
+class TreeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "tree_len", "block_size", "max_seq_len",
+        "num_cache_blocks", "device")]
+
+
+class PagesDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "max_blocks", "num_blocks", "device")]
+
+
+class KeepDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "max_keep", "max_seq_len", "block_size", "num_blocks", "device")]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("row_bytes", ctypes.c_longlong)]
+
+
+class Rope(ctypes.Structure):
+    """A rotary embedding (gqa_rope_t, include/gqa_rope.h): layout "half" or "interleaved",
+    scaling None, "linear", "banded", "yarn" or "custom" (with ``freqs``, one per pair)."""
+
+    _fields_ = [("layout", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("original_max_len", ctypes.c_int), ("theta", ctypes.c_float), ("factor", ctypes.c_float),
+                ("low_freq_factor", ctypes.c_float), ("high_freq_factor", ctypes.c_float),
+                ("beta_fast", ctypes.c_float), ("beta_slow", ctypes.c_float), ("magnitude", ctypes.c_float),
+                ("freqs", ctypes.c_void_p)]
+    LAYOUTS = {"half": 0, "interleaved": 1}
+    SCALINGS = {None: 0, "linear": 1, "banded": 2, "yarn": 3, "custom": 4}
+
+    def __init__(self, theta: float = 1e6, rotary_dim: int = 128, layout: str = "half", scaling: Optional[str] = None,
+                 factor: float = 1.0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, original_max_len: int = 0, magnitude: float = 0.0,
+                 freqs=None):
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise ValueError(f"rope layout {layout!r} or scaling {scaling!r} is not known")
+        self._freqs = None if freqs is None else np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+        if self._freqs is not None and self._freqs.shape != (int(rotary_dim) // 2,):
+            raise ValueError("freqs: one frequency per pair, [rotary_dim / 2]")
+        super().__init__(self.LAYOUTS[layout], int(rotary_dim), self.SCALINGS[scaling], int(original_max_len),
+                         float(theta), float(factor), float(low_freq_factor), float(high_freq_factor),
+                         float(beta_fast), float(beta_slow), float(magnitude),
+                         None if self._freqs is None else self._freqs.ctypes.data)
+
+    def frequencies(self):
+        """([rotary_dim / 2] float64 frequencies after scaling, magnitude): gqa_rope_freqs."""
+        out, mag = np.zeros(max(0, self.rotary_dim // 2)), ctypes.c_double()
+        _check(load().gqa_rope_freqs(ctypes.byref(self), out.ctypes.data, ctypes.byref(mag)), "gqa_rope_freqs")
+        return out, mag.value
 
 
 def header_functions() -> list:
@@ -94,12 +155,23 @@ def load(build: bool = True):
         lib.gqa_prefill_attn.argtypes = [ctypes.POINTER(PrefillDesc)] + [P] * 9 + [F, F, P, P, P]
         lib.gqa_q4_codebook.argtypes = [P]
         lib.gqa_decode_attn_q4.argtypes = [P] * 15 + [F, F, P, P]
+        lib.gqa_rope_freqs.argtypes = [P, P, P]
+        lib.gqa_rope_append.argtypes = [P] * 13 + [F, P, P, P]
+        lib.gqa_tree_prepare.argtypes = [I, I, P, P, P, P, P, I, P, P]
+        lib.gqa_tree_workspace_bytes.argtypes = [P, P]
+        lib.gqa_tree_attn.argtypes = [P] * 12
+        lib.gqa_pages_fork.argtypes = [P] * 6 + [I, P, P]
+        lib.gqa_pages_resize.argtypes = [P] * 9
+        lib.gqa_pages_copy.argtypes = [P, I, I, P, P, I, I, P, P]
+        lib.gqa_cache_keep_rows.argtypes = [P, P, I] + [P] * 6
         lib.gqa_status_string.argtypes = [I]
         lib.gqa_status_string.restype = ctypes.c_char_p
         for name in ("gqa_plan_create", "gqa_plan_destroy", "gqa_decode_attn", "gqa_decode_attn_host",
                      "gqa_attention_splitkv", "gqa_combine", "gqa_plan_read_q_rot",
                      "gqa_plan_device_errors", "gqa_decode_attn_static", "gqa_prefill_attn", "gqa_q4_codebook",
-                     "gqa_decode_attn_q4"):
+                     "gqa_decode_attn_q4", "gqa_rope_freqs", "gqa_rope_append", "gqa_tree_prepare",
+                     "gqa_tree_workspace_bytes", "gqa_tree_attn", "gqa_pages_fork", "gqa_pages_resize",
+                     "gqa_pages_copy", "gqa_cache_keep_rows"):
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -227,6 +299,243 @@ def prefill_attn_workload(w, out, *, device: int = 0, device_errors=None, stream
     prefill_attn(w.B, w.Hq, w.Hkv, w.T, w.max_seq, w.q_new, w.k_new, w.v_new, w.k_cache, w.v_cache, w.page_table,
                  w.q_start, w.q_norm_w, w.k_norm_w, w.rope_theta, w.eps, out, block_size=w.block_size,
                  num_cache_blocks=w.num_blocks, device=device, device_errors=device_errors, stream=stream)
+
+
+# ------------------------------------------------------- rotary append, draft trees, cache pages
+
+def _on(device: int, stream) -> int:
+    """The stream a call on `device` is queued on: the caller's, else torch's current one there."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _dev(t, name: str, dtype, shape, device: int, optional: bool = False) -> Optional[int]:
+    """Device pointer of a dense tensor of the dtype and shape the call needs (`dtype` a torch
+    dtype or a tuple of them; a None in `shape` takes any size)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {t.device}")
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape and (
+            t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape))):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _cache_shape(name: str, t, rows: int, num_kv_heads: int, device: int) -> int:
+    import torch
+    p = _dev(t, name, torch.bfloat16, None, device)
+    if t.numel() != rows * num_kv_heads * 128:
+        raise ValueError(f"{name}: expected {rows} rows of {num_kv_heads} x 128, got shape {tuple(t.shape)}")
+    return p
+
+
+def _tokens(t, name: str, batch: int, tokens: int, heads: int, device: int):
+    """(pointer, stride in elements between tokens) of a [B, T, H, 128] tensor whose heads are
+    dense and whose tokens are evenly spaced -- dense, or a slice of a wider projection."""
+    import torch
+    if t is None or not t.is_cuda or t.device.index != device or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: expected a bfloat16 tensor on cuda:{device}")
+    if tuple(t.shape) != (batch, tokens, heads, 128):
+        raise ValueError(f"{name}: expected shape {(batch, tokens, heads, 128)}, got {tuple(t.shape)}")
+    sb, st, sh, sd = t.stride()
+    if tokens == 1:
+        st = sb
+    step = heads * 128 if batch == 1 and tokens == 1 else st
+    if sd != 1 or (heads > 1 and sh != 128) or (batch > 1 and sb != step * tokens) or step < heads * 128:
+        raise ValueError(f"{name}: heads must be dense and tokens evenly spaced, got strides {t.stride()}")
+    return t.data_ptr(), step
+
+
+def rope_append(batch: int, num_q_heads: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, q, k, v, k_cache,
+                v_cache, page_table, slot_start, positions, counts, q_norm_w, k_norm_w, rope: Rope, eps: float, q_out,
+                *, block_size: int = 0, num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0,
+                device_errors=None, stream=None):
+    """QK-norm, rotation and append of [B, T] tokens (gqa_rope_append, include/gqa_rope.h).  q, k
+    and v may be slices of one projection (token strides are taken from the tensors)."""
+    import torch
+    i32 = torch.int32
+    qp, qs = _tokens(q, "q", batch, num_tokens, num_q_heads, device)
+    kp, ks = _tokens(k, "k", batch, num_tokens, num_kv_heads, device)
+    vp, vs = _tokens(v, "v", batch, num_tokens, num_kv_heads, device)
+    rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
+    desc = RopeDesc(batch, num_q_heads, num_kv_heads, head_dim, num_tokens, block_size, max_seq_len, num_cache_blocks,
+                    device, qs, ks, vs)
+    _check(load().gqa_rope_append(
+        ctypes.byref(desc), qp, kp, vp, _cache_shape("k_cache", k_cache, rows, num_kv_heads, device),
+        _cache_shape("v_cache", v_cache, rows, num_kv_heads, device),
+        _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+        _dev(slot_start, "slot_start", i32, (batch,), device),
+        _dev(positions, "positions", i32, (batch, num_tokens), device, True),
+        _dev(counts, "counts", i32, (batch,), device, True),
+        _dev(q_norm_w, "q_norm_w", torch.bfloat16, (128,), device, True),
+        _dev(k_norm_w, "k_norm_w", torch.bfloat16, (128,), device, True), ctypes.byref(rope), float(eps),
+        _dev(q_out, "q_out", torch.bfloat16, (batch, num_tokens, num_q_heads, 128), device),
+        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_rope_append")
+
+
+def tree_prepare(parents, ctx_lens, counts, mask, positions, *, device: int = 0, device_errors=None, stream=None):
+    """The masks (int64 words) and positions of draft trees from their parents [B, T]
+    (gqa_tree_prepare, include/gqa_tree.h)."""
+    import torch
+    i32 = torch.int32
+    pp = _dev(parents, "parents", i32, (None, None), device)
+    batch, tree_len = parents.shape
+    _check(load().gqa_tree_prepare(
+        batch, tree_len, pp, _dev(ctx_lens, "ctx_lens", i32, (batch,), device),
+        _dev(counts, "counts", i32, (batch,), device, True),
+        _dev(mask, "mask", (torch.int64, torch.uint64), (batch, tree_len, (tree_len + 63) // 64), device),
+        _dev(positions, "positions", i32, (batch, tree_len), device), device,
+        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_tree_prepare")
+
+
+def tree_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, *,
+                         block_size: int = 0, num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0) -> int:
+    desc = TreeDesc(batch, num_q_heads, num_kv_heads, head_dim, tree_len, block_size, max_seq_len, num_cache_blocks,
+                    device)
+    n = ctypes.c_size_t(0)
+    _check(load().gqa_tree_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)), "gqa_tree_workspace_bytes")
+    return int(n.value)
+
+
+def tree_workspace(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, *,
+                   device: int = 0):
+    """A workspace for gqa_tree_attn calls of this geometry (any cache layout) that do not overlap."""
+    import torch
+    return torch.empty(tree_workspace_bytes(batch, num_q_heads, num_kv_heads, tree_len, max_seq_len, device=device),
+                       dtype=torch.uint8, device=f"cuda:{device}")
+
+
+def tree_attn(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, q, k_cache, v_cache,
+              page_table, ctx_lens, counts, mask, out, *, block_size: int = 0, num_cache_blocks: int = 0,
+              head_dim: int = 128, workspace=None, device: int = 0, device_errors=None, stream=None):
+    """Attention of draft-tree nodes over the cache (gqa_tree_attn, include/gqa_tree.h).
+    ``workspace``: a uint8 tensor of tree_workspace_bytes; None takes one from torch's allocator
+    for this call (which knows the current stream only: give one with an explicit ``stream``)."""
+    import torch
+    i32 = torch.int32
+    rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
+    desc = TreeDesc(batch, num_q_heads, num_kv_heads, head_dim, tree_len, block_size, max_seq_len, num_cache_blocks,
+                    device)
+    lib = load()
+    need = ctypes.c_size_t(0)
+    _check(lib.gqa_tree_workspace_bytes(ctypes.byref(desc), ctypes.byref(need)), "gqa_tree_workspace_bytes")
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("a call on an explicit stream needs a workspace")
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=f"cuda:{device}")
+    ws = _dev(workspace, "workspace", torch.uint8, (None,), device)
+    if workspace.numel() < need.value:
+        raise ValueError(f"workspace: {need.value} bytes needed, got {workspace.numel()}")
+    shape = (batch, tree_len, num_q_heads, 128)
+    _check(lib.gqa_tree_attn(
+        ctypes.byref(desc), _dev(q, "q", torch.bfloat16, shape, device),
+        _cache_shape("k_cache", k_cache, rows, num_kv_heads, device),
+        _cache_shape("v_cache", v_cache, rows, num_kv_heads, device),
+        _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+        _dev(ctx_lens, "ctx_lens", i32, (batch,), device), _dev(counts, "counts", i32, (batch,), device, True),
+        _dev(mask, "mask", (torch.int64, torch.uint64), (batch, tree_len, (tree_len + 63) // 64), device),
+        _dev(out, "out", torch.bfloat16, shape, device), ws,
+        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_tree_attn")
+
+
+class CachePools:
+    """The pools of a cache that share a page table (K and V of every layer; the index and scale
+    tensors of a 4-bit cache): tensors of `rows` rows, paged with num_blocks * 64 rows, else
+    contiguous.  Keeps the tensors alive."""
+
+    def __init__(self, tensors, num_blocks: int = 0, rows: int = 0):
+        tensors = list(tensors)
+        self.num_blocks, self.rows = int(num_blocks), int(rows) or int(num_blocks) * 64
+        if not 1 <= len(tensors) <= MAX_POOLS or self.rows < 1 or (num_blocks and self.rows != num_blocks * 64):
+            raise ValueError(f"1 to {MAX_POOLS} pools, of num_blocks pages or of rows rows")
+        self.device = tensors[0].device.index
+        self.array = (Pool * len(tensors))()
+        for i, t in enumerate(tensors):
+            if not t.is_cuda or t.device.index != self.device or not t.is_contiguous():
+                raise ValueError("pools: contiguous tensors on one CUDA device")
+            size = t.numel() * t.element_size()
+            if size == 0 or size % self.rows:
+                raise ValueError(f"pool {i}: {size} bytes are not {self.rows} rows")
+            self.array[i] = Pool(t.data_ptr(), size // self.rows)
+        self.tensors = tensors
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _page_state(ref_counts, page_table, seq_lens, device: int):
+    import torch
+    i32 = torch.int32
+    ptrs = (_dev(ref_counts, "ref_counts", i32, (None,), device), _dev(page_table, "page_table", i32, (None, None), device),
+            _dev(seq_lens, "seq_lens", i32, (page_table.shape[0],), device))
+    return PagesDesc(page_table.shape[0], page_table.shape[1], ref_counts.shape[0], device), ptrs
+
+
+def pages_fork(ref_counts, page_table, seq_lens, src, dst, *, device: int = 0, device_errors=None, stream=None):
+    """Sequences dst[i] share the pages of sequences src[i] (gqa_pages_fork, include/gqa_pages.h)."""
+    import torch
+    desc, ptrs = _page_state(ref_counts, page_table, seq_lens, device)
+    n = src.shape[0]
+    _check(load().gqa_pages_fork(
+        ctypes.byref(desc), *ptrs, _dev(src, "src", torch.int32, (n,), device), _dev(dst, "dst", torch.int32, (n,), device),
+        n, _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_pages_fork")
+
+
+def pages_resize(ref_counts, page_table, seq_lens, new_lens, cow_src, cow_dst, *, device: int = 0, device_errors=None,
+                 stream=None):
+    """Grow, shrink or free sequences (gqa_pages_resize); cow_src / cow_dst [B] receive the pages to
+    copy before the sequences are written to (pages_copy), or -1."""
+    import torch
+    desc, ptrs = _page_state(ref_counts, page_table, seq_lens, device)
+    shape = (desc.batch,)
+    _check(load().gqa_pages_resize(
+        ctypes.byref(desc), *ptrs, _dev(new_lens, "new_lens", torch.int32, shape, device),
+        _dev(cow_src, "cow_src", torch.int32, shape, device), _dev(cow_dst, "cow_dst", torch.int32, shape, device),
+        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_pages_resize")
+
+
+def pages_copy(pools: CachePools, src, dst, *, device_errors=None, stream=None):
+    """Page dst[i] := page src[i] in every pool; src[i] < 0 is skipped (gqa_pages_copy)."""
+    import torch
+    n, device = src.shape[0], pools.device
+    _check(load().gqa_pages_copy(
+        pools.array, len(pools), pools.num_blocks, _dev(src, "src", torch.int32, (n,), device),
+        _dev(dst, "dst", torch.int32, (n,), device), n, device,
+        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_pages_copy")
+
+
+def cache_keep_rows(pools: CachePools, page_table, start, keep, counts, *, max_seq_len: int, device_errors=None,
+                    stream=None):
+    """Rows start[b] + keep[b][i] move to start[b] + i in every pool (gqa_cache_keep_rows)."""
+    import torch
+    i32, device = torch.int32, pools.device
+    kp = _dev(keep, "keep", i32, (None, None), device)
+    batch, width = keep.shape
+    paged = page_table is not None
+    if paged != (pools.num_blocks > 0) or (not paged and pools.rows != batch * max_seq_len):
+        raise ValueError("a page table goes with paged pools; contiguous ones have batch * max_seq_len rows")
+    desc = KeepDesc(batch, width, max_seq_len, 64 if paged else 0, pools.num_blocks, device)
+    _check(load().gqa_cache_keep_rows(
+        ctypes.byref(desc), pools.array, len(pools),
+        _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+        _dev(start, "start", i32, (batch,), device), kp, _dev(counts, "counts", i32, (batch,), device),
+        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        "gqa_cache_keep_rows")
 
 
 def q4_codebook() -> np.ndarray:
