@@ -1,12 +1,24 @@
 // QK RMSNorm + rotary embedding + KV append of any number of tokens (include/gqa_rope.h).
 //
-// One CTA per token.  The token's cos/sin (binary64, kept as double-word hi + lo) go through
-// shared memory; then a warp takes a head row at a time, lane l holding dims 4l .. 4l + 3 (one
-// 8-byte access).  In the interleaved layout both pairs of a lane are in the lane; in the half
-// layout the partners are r/8 lanes apart and come by a shuffle (r is a multiple of 8, so that a
-// lane's four dims are on one side).  Query rows are computed in binary32 and rounded
-// once; key rows, which stay in the cache, in double-word arithmetic, so that they round as
-// the exact value does (rowmath.cuh).
+// One CTA of four warps per token.  Half a warp takes a head row, a lane 8 of its dims (one
+// 16-byte access; four rows' loads in flight): two chunks of 4, since r / 2 is a multiple of 4 and
+// so a chunk's partners are one chunk of one lane.  In the interleaved layout they are in the
+// chunk itself; in the half layout they come by a shuffle of the packed bf16 words.
+//
+// The work is bound by HBM (a token is read once and written once, 28 KB at 40/8 heads) only if
+// the instructions stay few beside it, about 50 a row:
+//   * the norm weights are folded into the lane's cosines and sines, z = r (x_i (w_i c) + x_j
+//     (-+ w_j s)), in pairs (fma.rn.f32x2);
+//   * the angle p f modulo a turn.  f / 2 pi is kept as a 64-bit fraction of a turn, so p times
+//     it modulo 2^64 is the angle's place in the turn, exact but for 2^-65 p turns -- an integer
+//     product instead of binary64's (1/64 of the binary32 rate here); sine and cosine of the rest
+//     (at most 1/8 turn) are Taylor sums, the large terms in double-word binary32;
+//   * the key rows, which stay in the cache and round as the exact value does (rowmath.cuh).
+//     A row is first computed in binary32 with a bound on its error; where both ends of every
+//     interval round to the same bf16 (about 11 rows of 12) that is the exact value's rounding
+//     too, else the warp repeats the row in double-word (the method of Ziv, "Fast evaluation of
+//     elementary mathematical functions with correctly rounded last bit", ACM TOMS 17(3), 1991).
+// Query rows are computed in binary32 and rounded once.
 #include <math.h>
 #include <string.h>
 
@@ -27,13 +39,14 @@ struct RopeAppendParams {
   int paged, max_seq, max_blocks, num_blocks;
   int rotary;                    // r
   float eps;
-  double magnitude;
-  double freq[kHeadDim / 2];
+  float mag_hi, mag_lo;          // magnitude as a double-word
+  uint64_t turns[kHeadDim / 2];  // f_i / (2 pi) modulo 1, in units of 2^-64
 };
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kRopeWarps = kRopeThreads / 32;
 
 // Cache row of slot `slot` of sequence b, or -1 when its page id is out of range.
 __device__ __forceinline__ long long append_row(const RopeAppendParams &p, int b, int slot) {
@@ -45,18 +58,177 @@ __device__ __forceinline__ long long append_row(const RopeAppendParams &p, int b
 
 }  // namespace
 
+namespace {
+
+// c + v for |c| >= 2 |v|, both double-words (no cancellation): relative error about 2^-46.
+__device__ __forceinline__ dw dw_add_big(dw c, dw v) {
+  const dw s = fast_two_sum(c.hi, v.hi);
+  return fast_two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(c.lo, v.lo)));
+}
+
+// cos and sin of frac 2^-64 turns as double-words (relative error about 2^-44).
+__device__ __forceinline__ void cos_sin_turn(uint64_t frac, dw *c, dw *s) {
+  const uint64_t quarter = (frac + (1ull << 61)) >> 62;                // nearest quarter turn
+  const int64_t rest = static_cast<int64_t>(frac - (quarter << 62));   // within an eighth of a turn
+  const float hi = static_cast<float>(rest);
+  const float lo = static_cast<float>(rest - static_cast<int64_t>(hi));
+  const dw x = dw_mul(dw{hi, lo}, dw{0x1.921fb6p-62f, -0x1.777a5cp-87f});  // 2 pi / 2^64
+  const dw z = dw_mul(x, x);
+  // sin x = x + x z (-1/3! + z (1/5! + z (-1/7! + z (1/9! - z/11! + z^2/13! - z^3/15!))))
+  float t = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, -0x1.ae7f3ep-41f, 0x1.612462p-33f), -0x1.ae6456p-26f), 0x1.71de3ap-19f);
+  dw p = dw_add_big(dw{-0x1.a01a02p-13f, 0x1.7f97fap-39f}, dw{z.hi * t, 0.f});
+  p = dw_add_big(dw{0x1.111112p-7f, -0x1.ddddep-32f}, dw_mul(z, p));
+  p = dw_add_big(dw{-0x1.555556p-3f, 0x1.555556p-28f}, dw_mul(z, p));
+  const dw sx = dw_add_big(x, dw_mul(x, dw_mul(z, p)));
+  // cos x = 1 + z (-1/2! + z (1/4! + z (-1/6! + z (1/8! - z/10! + z^2/12! - z^3/14!))))
+  t = fmaf(z.hi, fmaf(z.hi, -0x1.93974ap-37f, 0x1.1eed8ep-29f), -0x1.27e4fcp-22f);
+  p = dw_add_big(dw{0x1.a01a02p-16f, -0x1.7f97fap-42f}, dw{z.hi * t, 0.f});
+  p = dw_add_big(dw{-0x1.6c16c2p-10f, 0x1.27d27ep-35f}, dw_mul(z, p));
+  p = dw_add_big(dw{0x1.555556p-5f, -0x1.555556p-30f}, dw_mul(z, p));
+  p = dw_add_big(dw{-0.5f, 0.f}, dw_mul(z, p));
+  const dw cx = dw_add_big(dw{1.f, 0.f}, dw_mul(z, p));
+  const dw a = quarter & 1 ? sx : cx, b = quarter & 1 ? cx : sx;  // of the angle, but for their signs
+  *c = (quarter + 1) & 2 ? dw_neg(a) : a;
+  *s = quarter & 2 ? dw_neg(b) : b;
+}
+
+// Two binary32 values in a register pair.
+struct f2 {
+  uint64_t v;
+};
+__device__ __forceinline__ f2 make_f2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_f2(f2 x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ f2 fma_f2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ f2 mul_f2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 unpack_f2(uint32_t w) { return make_f2(bf16_lo_to_float(w), bf16_hi_to_float(w)); }
+__device__ __forceinline__ f2 abs_f2(f2 x) {
+  f2 r;
+  r.v = x.v & 0x7fffffff7fffffffull;
+  return r;
+}
+
+// A lane's place in a row: dims 8 l .. 8 l + 7, as two chunks of 4.
+template <bool kInterleaved>
+struct RopeLane {
+  // the half layout's partners of chunk h: words of lane from[h], its other chunk when `odd`
+  bool odd;
+  int from[2];
+  bool turns[2], first[2];
+  int pair[2];  // the chunk's first pair
+
+  __device__ __forceinline__ void init(int rotary, int l, int base) {
+    const int m = rotary / 8;  // chunks of the first elements
+    odd = m & 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 2 * l + h;
+      turns[h] = c < 2 * m;
+      first[h] = c < m;
+      from[h] = base + ((first[h] ? c + m : c >= m ? c - m : c) >> 1 & 15);
+      pair[h] = kInterleaved ? 2 * c : 4 * (first[h] ? c : c - m);
+    }
+  }
+  // The partners of the row's words x (bf16 pairs); zeros in chunks that do not turn, which have
+  // no sine term (and must not meet 0 x inf).
+  __device__ __forceinline__ void partners(const uint32_t (&x)[4], uint32_t (&y)[4]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (kInterleaved) {
+          y[2 * h + e] = turns[h] ? __funnelshift_l(x[2 * h + e], x[2 * h + e], 16) : 0u;
+        } else {
+          const uint32_t o = __shfl_sync(0xffffffffu, odd ? x[2 * (1 - h) + e] : x[2 * h + e], from[h]);
+          y[2 * h + e] = turns[h] ? o : 0u;
+        }
+      }
+  }
+  __device__ __forceinline__ bool negative(int h, int e) const {  // the sign of dim 4 h + e's sine term
+    return kInterleaved ? (e & 1) == 0 : first[h];
+  }
+  __device__ __forceinline__ int pair_of(int h, int e) const { return pair[h] + (kInterleaved ? e >> 1 : e); }
+};
+
+// Key rows in double-word arithmetic: the rounding of the exact value.
+template <bool kInterleaved>
+__device__ __noinline__ uint4 key_row_exact(const float4 *cs, const RopeLane<kInterleaved> l, uint4 xv, uint4 wv,
+                                            bool norm, float eps) {
+  const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, w[4] = {wv.x, wv.y, wv.z, wv.w};
+  uint32_t xp[4], wp[4];
+  l.partners(x, xp);
+  l.partners(w, wp);
+  dw rn = {1.f, 0.f};
+  if (norm) {
+    dw ss = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = bf16_lo_to_float(x[e]), b = bf16_hi_to_float(x[e]);
+      ss = dw_add(ss, two_sum(__fmul_rn(a, a), __fmul_rn(b, b)));  // the squares are exact
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+      ss = dw_add(ss, dw{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+    const dw m = dw_add(dw{__fmul_rn(ss.hi, 1.0f / 128.0f), __fmul_rn(ss.lo, 1.0f / 128.0f)}, dw{eps, 0.f});
+    const float r0 = __frcp_rn(__fsqrt_rn(m.hi));
+    const dw e1 = dw_add(dw{1.f, 0.f}, dw_neg(dw_mul(m, two_prod(r0, r0))));  // 1 - m r0^2
+    rn = fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e1.hi));
+  }
+  uint32_t z[4];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int h = e >> 2;
+    // exact products: 8-bit significands
+    const float y = e & 1 ? bf16_hi_to_float(x[e >> 1]) * bf16_hi_to_float(w[e >> 1])
+                          : bf16_lo_to_float(x[e >> 1]) * bf16_lo_to_float(w[e >> 1]);
+    dw turned = {y, 0.f};
+    if (l.turns[h]) {
+      const float yp = e & 1 ? bf16_hi_to_float(xp[e >> 1]) * bf16_hi_to_float(wp[e >> 1])
+                             : bf16_lo_to_float(xp[e >> 1]) * bf16_lo_to_float(wp[e >> 1]);
+      const float4 c = cs[l.pair_of(h, e & 3)];
+      turned = dw_add(dw_mul_f(dw{c.x, c.z}, y), dw_mul_f(dw{c.y, c.w}, l.negative(h, e & 3) ? -yp : yp));
+    }
+    const uint32_t out = round_dw_bf16(norm ? dw_mul(turned, rn) : turned);
+    z[e >> 1] = e & 1 ? z[e >> 1] | (out << 16) : out;
+  }
+  return make_uint4(z[0], z[1], z[2], z[3]);
+}
+
+constexpr int kRopeAhead = 4;  // row pairs of a warp whose loads are in flight together
+// Error of a key element computed in binary32, relative to r (|x_i w_i cos| + |x_j w_j sin|), in
+// units of 2^-24: the sum of 128 squares 11 roundings (7 in the lane, 4 between lanes), halved by
+// the root; eps 1/2; the reciprocal root 4 (2 ulp); cos or sin, its product with w, the product
+// with x, the fma, the product with r 1 each -- 15 in all.  20 leaves room for the rounding of
+// the interval's own ends.
+constexpr float kKeyWindow = 20.f * 0x1p-24f;
+
+}  // namespace
+
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
   __shared__ float4 cs[kHeadDim / 2];  // m (cos_hi, sin_hi, cos_lo, sin_lo) of pair i
   griddep_wait();  // everything below may come from the preceding kernel
   const int b = static_cast<int>(blockIdx.x) / p.T, t = static_cast<int>(blockIdx.x) - b * p.T;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, hl = lane & 15;
   const long long tok = static_cast<long long>(blockIdx.x);
   const int n = p.counts ? p.counts[b] : p.T;
   const int s0 = p.slot_start[b];
+  int pos = p.positions ? p.positions[tok] : s0 + t;
   const bool seq_ok = n >= 0 && n <= p.T && s0 >= 0 && static_cast<long long>(s0) + n <= p.max_seq;
   if (seq_ok && t >= n) return;
-  const int pos = !seq_ok ? 0 : p.positions ? p.positions[tok] : s0 + t;
   if (!seq_ok || pos < 0) {
     if (tid == 0 && (seq_ok || t == 0))
       flag_error(p.err, (seq_ok || s0 < 0) ? GQA_DEVERR_POSITION : GQA_DEVERR_SEQLEN);
@@ -64,100 +236,149 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     for (int c = tid; c < p.Hq * kHeadDim / 8; c += kRopeThreads) dst[c] = make_uint4(0, 0, 0, 0);
     return;
   }
+
+  // Row pairs: rows 2 i + half of the queries, then of the keys, then of the values.
+  const uint4 *qsrc = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride) + hl;
+  uint4 x[kRopeAhead];
+  auto load = [&](const uint4 *src, int heads, int i0) {
+#pragma unroll
+    for (int e = 0; e < kRopeAhead; ++e) {
+      const int r = 2 * (i0 + e * kRopeWarps) + half;
+      x[e] = r < heads ? src[r * (kHeadDim / 8)] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load(qsrc, p.Hq, warp);
   if (tid < p.rotary / 2) {
-    double sv, cv;
-    sincos(static_cast<double>(pos) * p.freq[tid], &sv, &cv);
-    sv *= p.magnitude;
-    cv *= p.magnitude;
-    const float ch = static_cast<float>(cv), sh = static_cast<float>(sv);
-    cs[tid] = make_float4(ch, sh, static_cast<float>(cv - ch), static_cast<float>(sv - sh));
+    dw c, s;
+    cos_sin_turn(static_cast<uint64_t>(pos) * p.turns[tid], &c, &s);
+    if (p.mag_hi != 1.f || p.mag_lo != 0.f) {
+      c = dw_mul(c, dw{p.mag_hi, p.mag_lo});
+      s = dw_mul(s, dw{p.mag_hi, p.mag_lo});
+    }
+    cs[tid] = make_float4(c.hi, s.hi, c.lo, s.lo);
   }
   const long long crow = append_row(p, b, s0 + t);
   if (crow < 0 && tid == 0) flag_error(p.err, GQA_DEVERR_PAGE);
+  RopeLane<kInterleaved> l;
+  l.init(p.rotary, hl, 16 * half);
   __syncthreads();
 
-  // This lane's place in the rotation: dims 4l .. 4l + 3.
-  const bool turns = 4 * lane < p.rotary;
-  const int span = p.rotary / 8;  // half layout: lanes between partners
-  const bool first = lane < span;
-  const int partner = (kInterleaved || !turns) ? lane : first ? lane + span : lane - span;
-  float4 c4[kInterleaved ? 2 : 4];
+  // The lane's cosines and sines with the norm weights folded in.
+  f2 A[4], S[4];
+  auto fold = [&](const uint16_t *weights) {
+    const uint4 wv = weights ? reinterpret_cast<const uint4 *>(weights)[hl]
+                             : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // ones
+    const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
+    uint32_t wp[4];
+    l.partners(w, wp);
 #pragma unroll
-  for (int e = 0; e < (kInterleaved ? 2 : 4); ++e) {
-    const int i = kInterleaved ? 2 * lane + e : 4 * (first ? lane : lane - span) + e;
-    c4[e] = turns ? cs[i] : make_float4(1.f, 0.f, 0.f, 0.f);
-  }
-  const uint2 none = make_uint2(0x3f803f80u, 0x3f803f80u);  // ones
-  const uint2 qw = p.q_norm_w ? reinterpret_cast<const uint2 *>(p.q_norm_w)[lane] : none;
-  const uint2 kw = p.k_norm_w ? reinterpret_cast<const uint2 *>(p.k_norm_w)[lane] : none;
+    for (int e = 0; e < 4; ++e) {
+      float c[2], s[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = e >> 1, d = 2 * (e & 1) + k;
+        const float4 v = l.turns[h] ? cs[l.pair_of(h, d)] : make_float4(1.f, 0.f, 0.f, 0.f);
+        c[k] = v.x * (k ? bf16_hi_to_float(w[e]) : bf16_lo_to_float(w[e]));
+        s[k] = v.y * (k ? bf16_hi_to_float(wp[e]) : bf16_lo_to_float(wp[e]));
+        if (l.negative(h, d)) s[k] = -s[k];
+      }
+      A[e] = make_f2(c[0], c[1]);
+      S[e] = make_f2(s[0], s[1]);
+    }
+    return wv;
+  };
+  // r of a row (1 where there is no norm), from its values
+  auto inv_rms = [&](const f2 (&v)[4]) {
+    f2 q = mul_f2(v[0], v[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) q = fma_f2(v[e], v[e], q);
+    float a, c;
+    split_f2(q, a, c);
+    float ss = a + c;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    return rsqrtf(ss * (1.0f / 128.0f) + p.eps);
+  };
 
-  const int rows = p.Hq + (crow >= 0 ? 2 * p.Hkv : 0);
-  for (int r = warp; r < rows; r += kRopeThreads / 32) {
-    if (r >= p.Hq + p.Hkv) {  // value row: stored as it is
-      const int h = r - p.Hq - p.Hkv;
-      reinterpret_cast<uint2 *>(p.v_cache + (crow * p.Hkv + h) * kHeadDim)[lane] =
-          reinterpret_cast<const uint2 *>(p.v + tok * p.v_stride + h * kHeadDim)[lane];
-      continue;
+  // queries
+  (void)fold(p.q_norm_w);
+  uint4 *qdst = reinterpret_cast<uint4 *>(p.q_out + tok * p.Hq * kHeadDim) + hl;
+  for (int i0 = warp; 2 * i0 < p.Hq; i0 += kRopeAhead * kRopeWarps) {
+    if (i0 != warp) load(qsrc, p.Hq, i0);
+#pragma unroll
+    for (int k = 0; k < kRopeAhead; ++k) {
+      const int i = i0 + k * kRopeWarps;
+      if (2 * i >= p.Hq) break;
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      uint32_t wp[4];
+      l.partners(w, wp);
+      f2 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = unpack_f2(w[e]);
+      const float rn = p.q_norm_w ? inv_rms(v) : 1.f;
+      const f2 rn2 = make_f2(rn, rn);
+      uint32_t out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, c;
+        split_f2(mul_f2(rn2, fma_f2(v[e], A[e], mul_f2(unpack_f2(wp[e]), S[e]))), a, c);
+        out[e] = pack_bf16(a, c);
+      }
+      if (2 * i + half < p.Hq) qdst[(2 * i + half) * (kHeadDim / 8)] = make_uint4(out[0], out[1], out[2], out[3]);
     }
-    const bool isq = r < p.Hq;
-    const int h = isq ? r : r - p.Hq;
-    const uint2 xw = isq ? reinterpret_cast<const uint2 *>(p.q + tok * p.q_stride + h * kHeadDim)[lane]
-                         : reinterpret_cast<const uint2 *>(p.k + tok * p.k_stride + h * kHeadDim)[lane];
-    const uint2 ww = isq ? qw : kw;
-    const bool norm = isq ? p.q_norm_w != nullptr : p.k_norm_w != nullptr;
-    const float x[4] = {bf16_lo_to_float(xw.x), bf16_hi_to_float(xw.x), bf16_lo_to_float(xw.y),
-                        bf16_hi_to_float(xw.y)};
-    float y[4] = {x[0] * bf16_lo_to_float(ww.x), x[1] * bf16_hi_to_float(ww.x), x[2] * bf16_lo_to_float(ww.y),
-                  x[3] * bf16_hi_to_float(ww.y)};  // exact: 8-bit significands
-    float yp[4];                                   // the partners, with the sign of their term
-    if (kInterleaved) {
-      yp[0] = -y[1], yp[1] = y[0], yp[2] = -y[3], yp[3] = y[2];
-    } else {
+  }
+  if (crow < 0) return;
+
+  // keys
+  const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride) + hl;
+  const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride) + hl;
+  uint4 *kdst = reinterpret_cast<uint4 *>(p.k_cache + crow * p.Hkv * kHeadDim) + hl;
+  uint4 *vdst = reinterpret_cast<uint4 *>(p.v_cache + crow * p.Hkv * kHeadDim) + hl;
+  load(ksrc, p.Hkv, warp);
+  const uint4 kw = fold(p.k_norm_w);
+  for (int i0 = warp; 2 * i0 < p.Hkv; i0 += kRopeAhead * kRopeWarps) {
+    if (i0 != warp) load(ksrc, p.Hkv, i0);
+#pragma unroll
+    for (int k = 0; k < kRopeAhead; ++k) {
+      const int i = i0 + k * kRopeWarps;
+      if (2 * i >= p.Hkv) break;
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      uint32_t wp[4];
+      l.partners(w, wp);
+      f2 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = unpack_f2(w[e]);
+      const float rn = p.k_norm_w ? inv_rms(v) : 1.f;
+      const f2 rn2 = make_f2(rn, rn), up = make_f2(kKeyWindow, kKeyWindow), down = make_f2(-kKeyWindow, -kKeyWindow);
+      uint32_t out[4];
+      bool sure = true;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float o = __shfl_sync(0xffffffffu, y[e], partner);
-        yp[e] = first ? -o : o;
+        const f2 vp = unpack_f2(wp[e]);
+        const f2 z = mul_f2(rn2, fma_f2(v[e], A[e], mul_f2(vp, S[e])));
+        const f2 size = mul_f2(rn2, fma_f2(abs_f2(v[e]), abs_f2(A[e]), abs_f2(mul_f2(vp, S[e]))));
+        float a, c;
+        split_f2(fma_f2(size, down, z), a, c);
+        out[e] = pack_bf16(a, c);
+        split_f2(fma_f2(size, up, z), a, c);
+        sure = sure && out[e] == pack_bf16(a, c);
+        // tiny values, whose binary32 steps are not relative, take the exact path, and so does
+        // what is not finite
+        split_f2(size, a, c);
+        sure = sure && (a == 0.f || (a > 0x1p-80f && a < 0x1p100f)) && (c == 0.f || (c > 0x1p-80f && c < 0x1p100f));
       }
+      uint4 row = make_uint4(out[0], out[1], out[2], out[3]);
+      if (!__all_sync(0xffffffffu, sure)) row = key_row_exact<kInterleaved>(cs, l, x[k], kw, p.k_norm_w != nullptr, p.eps);
+      if (2 * i + half < p.Hkv) kdst[(2 * i + half) * (kHeadDim / 8)] = row;
     }
-    if (isq) {
-      float ss = 0.f;
+  }
+  // values: stored as they are
+  for (int i0 = warp; 2 * i0 < p.Hkv; i0 += kRopeAhead * kRopeWarps) {
+    load(vsrc, p.Hkv, i0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float rn = norm ? 1.0f / sqrtf(ss * (1.0f / 128.0f) + p.eps) : 1.0f;
-      float z[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 c = c4[kInterleaved ? e >> 1 : e];
-        z[e] = rn * (turns ? fmaf(y[e], c.x, yp[e] * c.y) : y[e]);
-      }
-      reinterpret_cast<uint2 *>(p.q_out + (tok * p.Hq + h) * kHeadDim)[lane] =
-          make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
-    } else {
-      dw rn = {1.f, 0.f};
-      if (norm) {
-        dw ss = {0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ss = dw_add(ss, dw{__fmul_rn(x[e], x[e]), 0.f});
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          ss = dw_add(ss, dw{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
-        const dw m = dw_add(dw{__fmul_rn(ss.hi, 1.0f / 128.0f), __fmul_rn(ss.lo, 1.0f / 128.0f)}, dw{p.eps, 0.f});
-        const float r0 = __frcp_rn(__fsqrt_rn(m.hi));
-        const dw e1 = dw_add(dw{1.f, 0.f}, dw_neg(dw_mul(m, two_prod(r0, r0))));  // 1 - m r0^2
-        rn = fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e1.hi));
-      }
-      uint16_t z[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 c = c4[kInterleaved ? e >> 1 : e];
-        const dw turned = turns ? dw_add(dw_mul_f(dw{c.x, c.z}, y[e]), dw_mul_f(dw{c.y, c.w}, yp[e])) : dw{y[e], 0.f};
-        z[e] = round_dw_bf16(norm ? dw_mul(turned, rn) : turned);
-      }
-      reinterpret_cast<uint2 *>(p.k_cache + (crow * p.Hkv + h) * kHeadDim)[lane] =
-          make_uint2(static_cast<uint32_t>(z[0]) | (static_cast<uint32_t>(z[1]) << 16),
-                     static_cast<uint32_t>(z[2]) | (static_cast<uint32_t>(z[3]) << 16));
+    for (int k = 0; k < kRopeAhead; ++k) {
+      const int r = 2 * (i0 + k * kRopeWarps) + half;
+      if (r < p.Hkv) vdst[r * (kHeadDim / 8)] = x[k];
     }
   }
 }
@@ -165,6 +386,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 }  // namespace gqa
 
 using namespace gqa;
+
+namespace {
+
+// f / (2 pi) modulo 1 in units of 2^-64, rounded: the 53-bit significand of f times the first 128
+// bits of 1 / (2 pi), shifted into place.  |f| <= 2^16.
+uint64_t turns_of(double f) {
+  int e = 0;
+  const double a = frexp(fabs(f), &e);  // |f| = a 2^e, a in [1/2, 1) or 0
+  const uint64_t m = static_cast<uint64_t>(ldexp(a, 53));
+  const int shift = 117 - e;            // |f| / (2 pi) 2^64 = m c 2^-shift, c = 2^128 / (2 pi)
+  if (m == 0 || shift >= 191) return 0;
+  const unsigned __int128 lo = static_cast<unsigned __int128>(m) * 0x7f09d5f47d4d3770ull;
+  const unsigned __int128 hi = static_cast<unsigned __int128>(m) * 0x28be60db9391054aull + (lo >> 64);
+  // m c = hi 2^64 + (lo mod 2^64); shift is above 64, so the low word only rounds
+  const int s = shift - 64;             // 37 .. 126
+  const uint64_t t = static_cast<uint64_t>(hi >> s) + static_cast<uint64_t>((hi >> (s - 1)) & 1);
+  return f < 0 ? 0 - t : t;
+}
+
+}  // namespace
 
 extern "C" gqa_status_t gqa_rope_freqs(const gqa_rope_t *rope, double *freqs, double *magnitude) {
   if (!rope) return GQA_ERR_INVALID_ARG;
@@ -217,6 +458,8 @@ extern "C" gqa_status_t gqa_rope_freqs(const gqa_rope_t *rope, double *freqs, do
       m = 0.1 * log(factor) + 1.0;
     }
   }
+  for (int i = 0; i < r / 2; ++i)
+    if (!(fabs(f[i]) <= 65536.0)) return GQA_ERR_INVALID_ARG;
   if (s.magnitude > 0.f) m = s.magnitude;
   if (freqs) memcpy(freqs, f, sizeof(double) * (r / 2));
   if (magnitude) *magnitude = m;
@@ -249,8 +492,12 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   if (q_out == q && d.q_stride != 0 && d.q_stride != qd) return GQA_ERR_INVALID_ARG;
   RopeAppendParams p;
   memset(&p, 0, sizeof p);
-  st = gqa_rope_freqs(rope, p.freq, &p.magnitude);
+  double freqs[kHeadDim / 2], magnitude;
+  st = gqa_rope_freqs(rope, freqs, &magnitude);
   if (st != GQA_OK) return st;
+  for (int i = 0; i < rope->rotary_dim / 2; ++i) p.turns[i] = turns_of(freqs[i]);
+  p.mag_hi = static_cast<float>(magnitude);
+  p.mag_lo = static_cast<float>(magnitude - p.mag_hi);
   st = check_device(d.device);
   if (st != GQA_OK) return st;
   DeviceGuard guard(d.device);

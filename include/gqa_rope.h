@@ -73,7 +73,8 @@ typedef struct gqa_rope {
  * gqa_rope_freqs -- the frequencies and the magnitude a gqa_rope_t stands for (host,
  * synchronous, no device work).
  *   freqs [r/2] receives f_i after scaling; magnitude receives m; either may be NULL.
- * Errors: GQA_ERR_INVALID_ARG (NULL rope, a field outside the ranges above).
+ * Errors: GQA_ERR_INVALID_ARG (NULL rope, a field outside the ranges above, a frequency beyond
+ * 65536 in size).
  */
 gqa_status_t gqa_rope_freqs(const gqa_rope_t *rope, double *freqs, double *magnitude);
 

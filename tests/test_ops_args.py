@@ -77,7 +77,8 @@ def test_custom_frequencies_are_the_callers():
     dict(scaling="banded", factor=2.0, original_max_len=0), dict(scaling="banded", factor=2.0, original_max_len=64, low_freq_factor=4.0),
     dict(scaling="yarn", factor=0.5, original_max_len=64), dict(scaling="yarn", factor=2.0, original_max_len=64, beta_fast=1.0),
     dict(scaling="yarn", factor=2.0, original_max_len=64, theta=1.0), dict(scaling="custom"),
-    dict(scaling="custom", freqs=[float("inf")] * 64),
+    dict(scaling="custom", freqs=[float("inf")] * 64), dict(scaling="custom", freqs=[65537.0] * 64),
+    dict(scaling="linear", factor=1e-6),
 ])
 def test_bad_rotary_embeddings_are_refused(over):
     with pytest.raises(binding.GqaError) as e:
