@@ -24,6 +24,7 @@
 
 #include "../../include/gqa_rope.h"
 #include "op_args.h"
+#include "pairmath.cuh"
 #include "rowmath.cuh"
 
 namespace gqa {
@@ -92,28 +93,6 @@ __device__ __forceinline__ void cos_sin_turn(uint64_t frac, dw *c, dw *s) {
   *s = quarter & 2 ? dw_neg(b) : b;
 }
 
-// Two binary32 values in a register pair.
-struct f2 {
-  uint64_t v;
-};
-__device__ __forceinline__ f2 make_f2(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void split_f2(f2 x, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
-}
-__device__ __forceinline__ f2 fma_f2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ f2 mul_f2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 __device__ __forceinline__ f2 unpack_f2(uint32_t w) { return make_f2(bf16_lo_to_float(w), bf16_hi_to_float(w)); }
 __device__ __forceinline__ f2 abs_f2(f2 x) {
   f2 r;

@@ -6,19 +6,28 @@
 // row sees the whole context, so the work is one pass over K and V per row tile; only the last
 // tiles, which hold the nodes' own slots, are masked, by the bits of the node's mask.
 //
-// Work.  The batch's KV tiles (sequence-major, then KV head, then 64 tokens) are cut into W
+// Work.  The batch's tokens, in tiles of 64 (one page) sequence after sequence, are cut into W
 // equal contiguous ranges whatever the sequence boundaries, so ragged batches and single long
-// sequences both fill the GPU; the lengths are read on the device.  CTA (w, r) streams range w
-// for row tile r; the row tiles of one range run side by side and share its tiles in L2.  A piece
-// of a range that is a whole (sequence, KV head) segment writes its output rows; one that is
-// cut leaves (O, m, l) in the workspace and tree_merge_kernel joins the parts in order.
+// sequences both fill the GPU; the lengths are read on the device.  CTA (w, kv, r) streams KV
+// head kv of range w for row tile r.  The CTAs of a range run side by side: the heads of a token
+// lie next to each other in the cache, and streamed together they read HBM in whole rows
+// (with the heads of a tile read at different times, 8 heads x 8 sequences of 32k took 182 us
+// instead of XXX), and the row tiles share their tiles in L2.  A piece of a range that is a
+// whole sequence writes its output rows; one that is cut leaves (O, m, l) in the workspace and
+// tree_merge_kernel joins the parts in order.
 //
-// Attention CTA: as in prefill.cu.  A TMA warp streams K (2 stages) and V (3 stages) tiles; an
-// MMA warp issues S = Q K^T into one of two tensor-memory buffers and O += P V, P read from
-// tensor memory as bf16 hi + lo (rounding P to one bf16 would double the output's error: its
-// 2^-9 relative error a weight is as large as the output's own rounding); four softmax warps
-// hold a row a thread.  The maximum is raised lazily (by more than 2^8), so most tiles rescale
-// nothing.  The pipeline runs on across the pieces of a range.
+// Attention CTA, one per SM: a TMA warp streams the K and V tiles through deep rings (a tile takes
+// longer to come from HBM than to be used; with two CTAs an SM and 2 + 3 stages each, the loads in
+// flight did not cover that); two streams of an MMA warp and four softmax warps each work on
+// them, so that one stream's softmax overlaps the other's products.  Where the CTA has two row
+// tiles (R >= 2) each stream takes one and both use every tile: a tile's way through TMA, whose
+// rows of 128 bytes an SM takes at about 50 GB/s, is paid once for 256 rows.  Where it has one, the
+// streams take the even and the odd tiles and join their O at the end (a softmax thread finds
+// both in its own tensor-memory lane).
+//   A stream's MMA warp issues S = Q K^T into one of two tensor-memory buffers and O += P V, P
+// read from tensor memory as bf16 hi + lo (rounding P to one bf16 would add an error as large as
+// the output's own rounding); a softmax thread holds a row.  The maximum is raised lazily (by more
+// than 2^8), so most tiles rescale nothing.  The pipeline runs on across the pieces of a range.
 #include <math.h>
 #include <string.h>
 
@@ -26,6 +35,7 @@
 
 #include "../../include/gqa_tree.h"
 #include "op_args.h"
+#include "pairmath.cuh"
 #include "tc05.cuh"
 
 namespace gqa {
@@ -35,7 +45,7 @@ struct TreeParams {
   const uint64_t *mask;
   const uint16_t *v_cache;
   uint16_t *out;
-  float *part;                  // [W * R * 2][130][128]: O columns, m, l of a cut piece
+  float *part;                  // [W * Hkv * R * 2][130][128]: O columns, m, l of a cut piece
   uint32_t *err;
   int B, T, Hq, Hkv, G, Tt, R;  // R row tiles of Tt nodes
   int words;                    // 64-bit words of a mask row
@@ -46,53 +56,58 @@ struct TreeParams {
 
 namespace {
 
-constexpr int kTrKStages = 2;
-constexpr int kTrVStages = 3;
-constexpr int kTrSoftmaxWarps = 4;
-constexpr int kTrThreads = 32 * (kTrSoftmaxWarps + 2);
-constexpr int kTrProducerWarp = kTrSoftmaxWarps;
-constexpr int kTrMmaWarp = kTrSoftmaxWarps + 1;
-constexpr int kTrCtasPerSm = 2;
-constexpr int kTrRows = 128;
-// Tensor memory per CTA: two S buffers (64 fp32 columns each; P overwrites S as bf16 pairs, hi
-// in the first 32 columns, lo in the next) and O (128 columns); two CTAs fill the SM's 512.
-constexpr uint32_t kTrTmemCols = 256;
+constexpr int kTrRows = 128;                 // M of every MMA
+constexpr int kTrStreams = 2;
+constexpr int kTrMmaWarp = 8;                // and 9: a stream's each
+constexpr int kTrProducerWarp = 10;
+constexpr int kTrThreads = 32 * 11;
+// Tensor memory: a stream's two S buffers (64 fp32 columns each; P overwrites S as bf16 pairs, hi in
+// the first 32 columns, lo in the next) and its O (128 columns).
+constexpr uint32_t kTrTmemStream = 256;
+constexpr uint32_t kTrTmemCols = kTrStreams * kTrTmemStream;
 constexpr uint32_t kTrTmemO = 128;
 constexpr float kTrRescaleLog2 = 8.f;
 
 constexpr int kTrQBytes = 2 * kTrRows * kHalfRowBytes;  // 32 KiB: two 64-dim panels
 constexpr int kTrTileBytes = 2 * kHalfTileBytes;         // 16 KiB: a K or V tile's two halves
-constexpr int kTrOffK = kTrQBytes;
-constexpr int kTrOffV = kTrOffK + kTrKStages * kTrTileBytes;
-constexpr int kTrOffBar = kTrOffV + kTrVStages * kTrTileBytes;
-// barriers: k_full[2], k_empty[2], v_full[3], v_empty[3], s_full[2], p_full[2], q_full, q_empty,
-// pv_done, o_full, o_free, drain
-constexpr int kTrNumBars = 2 * kTrKStages + 2 * kTrVStages + 2 + 2 + 6;
-constexpr int kTrSmemBytes = kTrOffBar + 8 * kTrNumBars + 16;
 constexpr int kTrPartFloats = (kHeadDim + 2) * kTrRows;
-static_assert(kTrCtasPerSm * (kTrSmemBytes + 1024) <= 228 * 1024, "two CTAs must share an SM");
-static_assert(kTrOffK % 1024 == 0 && kTrOffV % 1024 == 0 && kTrTileBytes % 1024 == 0, "swizzled tiles 1024-aligned");
+
+// Shared memory of the kernel with NQ query tiles: what they leave is the K and V rings.
+template <int NQ>
+struct TreeSmem {
+  static constexpr int kStages = NQ == 1 ? 6 : 5;  // of K and of V
+  static constexpr int kOffK = NQ * kTrQBytes;
+  static constexpr int kOffV = kOffK + kStages * kTrTileBytes;
+  static constexpr int kOffMl = kOffV + kStages * kTrTileBytes;  // [2 streams][128] (m, l)
+  // barriers: k_full, k_empty, v_full, v_empty [kStages], s_full, p_full [2 streams][2],
+  // pv_done, o_full, o_free, drain [2 streams], q_full, q_empty, meet
+  static constexpr int kNumBars = 4 * kStages + 2 * 4 + 4 * 2 + 3;
+  static constexpr int kOffBar = kOffMl + kTrStreams * kTrRows * 8;
+  static constexpr int kBytes = kOffBar + 8 * kNumBars + 4 * 5 + 12;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0, "swizzled tiles 1024-aligned");
+};
 
 // Nodes of sequence b, or -1 when its lengths are invalid.
 __device__ __forceinline__ int tree_nodes(const TreeParams &p, int b, int ctx) {
   const int n = p.counts ? p.counts[b] : p.T;
   return (ctx >= 0 && n >= 0 && n <= p.T && static_cast<long long>(ctx) + n <= p.max_seq) ? n : -1;
 }
-// KV tiles of each segment of sequence b: those up to its last node's slot, none when it has no node.
+// KV tiles of sequence b: those up to its last node's slot, none when it has no node.
 __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
   const int ctx = p.ctx_lens[b], n = tree_nodes(p, b, ctx);
   return n > 0 ? (ctx + n + kTile - 1) / kTile : 0;
 }
 
-// Walks the segments a range [pos, end) of KV tiles covers.  Every warp of the CTA runs its own
+// Walks the sequences a range [pos, end) of KV tiles covers.  Every warp of the CTA runs its own
 // copy, all lanes alike.
 struct TreeWalk {
   long long pos, end;  // tiles still to do
   long long seq0;      // first tile of sequence b
-  int b, nt;           // sequence, its tiles a segment
+  int b, nt;           // sequence, its tiles
   // of the piece at hand
-  int kv, j0, j1;
-  bool whole;          // the piece is its whole segment
+  int j0, j1;
+  bool whole;          // the piece is its whole sequence
 
   __device__ __forceinline__ void start(const TreeParams &p, long long begin, long long stop, int b0, long long s0) {
     pos = begin;
@@ -104,14 +119,12 @@ struct TreeWalk {
   // The next piece; false when the range is done.
   __device__ __forceinline__ bool next(const TreeParams &p) {
     if (pos >= end) return false;
-    while (pos >= seq0 + static_cast<long long>(nt) * p.Hkv) {
-      seq0 += static_cast<long long>(nt) * p.Hkv;
+    while (pos >= seq0 + nt) {
+      seq0 += nt;
       ++b;
       nt = tree_tiles(p, b);
     }
-    const long long off = pos - seq0;
-    kv = static_cast<int>(off / nt);
-    j0 = static_cast<int>(off - static_cast<long long>(kv) * nt);
+    j0 = static_cast<int>(pos - seq0);
     const long long left = end - pos;
     j1 = left < nt - j0 ? j0 + static_cast<int>(left) : nt;
     whole = j0 == 0 && j1 == nt;
@@ -125,7 +138,7 @@ struct TreeWalk {
 __device__ __forceinline__ long long tree_total(const TreeParams &p, int lane, long long *lane_first) {
   const int per = (p.B + 31) / 32, b0 = lane * per, b1 = min(p.B, b0 + per);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += static_cast<long long>(tree_tiles(p, b)) * p.Hkv;
+  for (int b = b0; b < b1; ++b) sum += tree_tiles(p, b);
   long long x = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +157,7 @@ __device__ __forceinline__ void tree_find(const TreeParams &p, int lane, long lo
   long long s = __shfl_sync(0xffffffffu, lane_first, owner);
   int x = owner * per;
   while (x + 1 < p.B) {
-    const long long nxt = s + static_cast<long long>(tree_tiles(p, x)) * p.Hkv;
+    const long long nxt = s + tree_tiles(p, x);
     if (nxt > at) break;
     s = nxt;
     ++x;
@@ -153,8 +166,17 @@ __device__ __forceinline__ void tree_find(const TreeParams &p, int lane, long lo
   *seq0 = s;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Ranges in use: at least kTrMinTiles tiles each, so that small batches leave few partials.
-constexpr int kTrMinTiles = 2;
+constexpr int kTrMinTiles = 4;
 __device__ __forceinline__ int tree_ranges(const TreeParams &p, long long total) {
   const long long most = (total + kTrMinTiles - 1) / kTrMinTiles;
   return static_cast<int>(most < p.W ? most : p.W);
@@ -211,40 +233,55 @@ __global__ void __launch_bounds__(GQA_MAX_TREE) tree_prepare_kernel(const int32_
 }
 
 // ------------------------------------------------------------------------------- attention
-__global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
+template <int NQ>
+__global__ void __launch_bounds__(kTrThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeParams p) {
+  using Smem = TreeSmem<NQ>;
+  constexpr int kStages = Smem::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_addr(smem_raw) & 1023u) != 0u) {  // a launch assumption broken: no work at all
     if (threadIdx.x == 0) flag_error(p.err, GQA_DEVERR_LAUNCH);
     return;
   }
   uint8_t *smem = smem_raw;
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kTrOffBar);
-  uint64_t *k_empty = k_full + kTrKStages;
-  uint64_t *v_full = k_empty + kTrKStages;
-  uint64_t *v_empty = v_full + kTrVStages;
-  uint64_t *s_full = v_empty + kTrVStages;
-  uint64_t *p_full = s_full + 2;
-  uint64_t *q_full = p_full + 2;
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + Smem::kOffBar);
+  uint64_t *k_empty = k_full + kStages;
+  uint64_t *v_full = k_empty + kStages;
+  uint64_t *v_empty = v_full + kStages;
+  uint64_t *s_full = v_empty + kStages;  // [stream][buffer]
+  uint64_t *p_full = s_full + 4;
+  uint64_t *pv_done = p_full + 4;  // [stream]
+  uint64_t *o_full = pv_done + 2;
+  uint64_t *o_free = o_full + 2;
+  uint64_t *drain = o_free + 2;
+  uint64_t *q_full = drain + 2;
   uint64_t *q_empty = q_full + 1;
-  uint64_t *pv_done = q_full + 2;
-  uint64_t *o_full = q_full + 3;
-  uint64_t *o_free = q_full + 4;
-  uint64_t *drain = q_full + 5;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(k_full + kTrNumBars);
-  uint32_t *v_bad = tmem_slot + 1;  // a non-finite value in a node's V row of the piece at hand
+  uint64_t *meet = q_full + 2;  // all eight softmax warps
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(k_full + Smem::kNumBars);
+  // the last piece (from 1) of those with piece % 4 = i that had a non-finite value in a node's V
+  // row (a stream is at most two pieces ahead of the other: the queries are given back by both)
+  uint32_t *v_bad = tmem_slot + 1;
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + Smem::kOffMl);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = static_cast<int>(blockIdx.x) % p.R, w = static_cast<int>(blockIdx.x) / p.R;
+  const int units = (p.R + NQ - 1) / NQ;  // row tiles, NQ at a time
+  const int r0 = static_cast<int>(blockIdx.x) % units * NQ, kv = static_cast<int>(blockIdx.x) / units % p.Hkv,
+            w = static_cast<int>(blockIdx.x) / units / p.Hkv;
 
   if (tid == 0) {
-    for (int i = 0; i < kTrNumBars; ++i) {
+    for (int i = 0; i < Smem::kNumBars; ++i) {
       uint64_t *bar = k_full + i;
-      const bool from_softmax = bar == &p_full[0] || bar == &p_full[1] || bar == o_free;
-      mbar_init(smem_addr(bar), from_softmax ? kTrSoftmaxWarps : 1);
+      // the queries, and tiles that both streams use, are given back by both; P comes from a stream's
+      // four softmax warps; O is read by all eight
+      int count = 1;
+      if ((bar >= k_empty && bar < v_full) || (bar >= v_empty && bar < s_full)) count = NQ;
+      if (bar == q_empty) count = 2;
+      if (bar >= p_full && bar < pv_done) count = 4;
+      if ((bar >= o_free && bar < drain) || bar == meet) count = 8;
+      mbar_init(smem_addr(bar), count);
     }
-    *v_bad = 0;
+    for (int i = 0; i < 4; ++i) v_bad[i] = 0;
     fence_barrier_init();
   }
   if (warp == kTrProducerWarp && lane == 0) {
@@ -261,7 +298,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // everything below may come from the preceding kernel
-  griddep_launch_dependents();  // only tree_merge_kernel follows, and it waits
+  griddep_launch_dependents();  // only tree_merge_kernel follows early, and it waits
 
   // Sequences with invalid lengths: flagged, zeros in all their rows.
   for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x)) {
@@ -287,135 +324,204 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
     }
     walk.start(p, begin, stop, b, seq0);
   }
-  uint8_t *const qs = smem;
-  auto k_ptr = [&](int s) { return smem + kTrOffK + s * kTrTileBytes; };
-  auto v_ptr = [&](int s) { return smem + kTrOffV + s * kTrTileBytes; };
-  // Does row tile r have a node in sequence b?
-  auto has_rows = [&](int b) { return r * p.Tt < tree_nodes(p, b, p.ctx_lens[b]); };
+  auto k_ptr = [&](int s) { return smem + Smem::kOffK + s * kTrTileBytes; };
+  auto v_ptr = [&](int s) { return smem + Smem::kOffV + s * kTrTileBytes; };
+  // A piece's streams: 0 if the CTA's row tiles have no node in the sequence, 1 if only the first
+  // has (the streams share its tiles), 2 if both have (each stream takes all tiles for its own).
+  auto row_tiles = [&](int b) {
+    const int n = tree_nodes(p, b, p.ctx_lens[b]);
+    return r0 * p.Tt >= n ? 0 : (NQ == 2 && (r0 + 1) * p.Tt < n) ? 2 : 1;
+  };
 
   if (warp == kTrProducerWarp) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int it = 0, piece = 0;  // KV tiles and pieces so far: their stages and phases
-      bool ok = true;
-      while (ok && walk.next(p)) {
-        if (!has_rows(walk.b)) continue;
-        const int b = walk.b, kv = walk.kv;
-        auto row_of = [&](int j) {
-          if (!p.paged) return b * p.max_seq + j * kTile;
-          const int pg = p.page_table[static_cast<long long>(b) * p.max_blocks + j];
-          if (pg < 0 || pg >= p.num_blocks) {
-            flag_error(p.err, GQA_DEVERR_PAGE);
-            return -kTile;  // the whole box out of bounds: TMA fills zeros
+    // The whole warp walks (a lane holds the cache row of one of the next 32 tiles, the 32 after
+    // them are fetched ahead); lane 0 issues the loads.
+    int it = 0, piece = 0, queries = 0;  // KV tiles, pieces, loads of queries so far: stages and phases
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int b = walk.b, j0 = walk.j0, j1 = walk.j1, nr = row_tiles(b);
+      if (nr == 0) continue;
+      auto row_of = [&](int j) -> int {  // -kTile where there is none: TMA fills zeros
+        if (j >= j1) return -kTile;
+        if (!p.paged) return b * p.max_seq + j * kTile;
+        const int pg = p.page_table[static_cast<long long>(b) * p.max_blocks + j];
+        if (pg < 0 || pg >= p.num_blocks) {
+          flag_error(p.err, GQA_DEVERR_PAGE);
+          return -kTile;
+        }
+        return pg * kTile;
+      };
+      int rows = row_of(j0 + lane), rows_next = row_of(j0 + 32 + lane), base = j0;
+      // The queries, once the last S of the piece before has read its own; until then the piece's
+      // first tiles, as far as the rings take them without an S of this piece.
+      bool q_sent = false;
+      auto send_q = [&](bool wait) {
+        bool free = piece == 0;
+        if (!free) {
+          const uint32_t bar = smem_addr(q_empty), phase = static_cast<uint32_t>((piece - 1) & 1);
+          free = __all_sync(0xffffffffu, wait ? mbar_wait(bar, phase) : mbar_try_wait(bar, phase));
+        }
+        if (!free) return !wait;
+        q_sent = true;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_addr(q_full), 2u * 64u * 2u * static_cast<uint32_t>(p.G * p.Tt * nr));
+          for (int x = 0; x < nr; ++x) {
+            const uint32_t qd = smem_addr(smem) + x * kTrQBytes;
+            tma_load_4d(qd, &tmQ, smem_addr(q_full), 0, kv * p.G, (r0 + x) * p.Tt, b);
+            tma_load_4d(qd + kTrRows * kHalfRowBytes, &tmQ, smem_addr(q_full), 64, kv * p.G, (r0 + x) * p.Tt, b);
           }
-          return pg * kTile;
-        };
-        // the queries, once the last S of the piece before has read its own
-        if (piece > 0) ok = mbar_wait(smem_addr(q_empty), static_cast<uint32_t>((piece - 1) & 1));
+        }
+        return true;
+      };
+      for (int j = j0; j < j1; ++j, ++it) {
+        if (!q_sent) ok = send_q(j - j0 == kStages - 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(smem_addr(q_full), 2u * 64u * 2u * static_cast<uint32_t>(p.G * p.Tt));
-        tma_load_4d(smem_addr(qs), &tmQ, smem_addr(q_full), 0, kv * p.G, r * p.Tt, b);
-        tma_load_4d(smem_addr(qs + kTrRows * kHalfRowBytes), &tmQ, smem_addr(q_full), 64, kv * p.G, r * p.Tt, b);
-        ++piece;
-        for (int j = walk.j0; j < walk.j1; ++j, ++it) {
-          const int row = row_of(j);
-          const int ks = it % kTrKStages, vs = it % kTrVStages;
-          if (it >= kTrKStages) ok = mbar_wait(smem_addr(&k_empty[ks]), static_cast<uint32_t>((it / kTrKStages - 1) & 1));
-          if (!ok) break;
-          const uint32_t kb = smem_addr(&k_full[ks]), kd = smem_addr(k_ptr(ks));
+        if (j - base == 32) {
+          base += 32;
+          rows = rows_next;
+          rows_next = row_of(base + 32 + lane);
+        }
+        const int row = __shfl_sync(0xffffffffu, rows, j - base);
+        const int st = it % kStages;
+        const uint32_t free_phase = static_cast<uint32_t>((it / kStages - 1) & 1);
+        if (it >= kStages) ok = mbar_wait(smem_addr(&k_empty[st]), free_phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t kb = smem_addr(&k_full[st]), kd = smem_addr(k_ptr(st));
           mbar_arrive_expect_tx(kb, kTrTileBytes);
           tma_load_3d(kd, &tmK, kb, 0, kv, row);
           tma_load_3d(kd + kHalfTileBytes, &tmK, kb, 64, kv, row);
-          if (it >= kTrVStages) ok = mbar_wait(smem_addr(&v_empty[vs]), static_cast<uint32_t>((it / kTrVStages - 1) & 1));
-          if (!ok) break;
-          const uint32_t vb = smem_addr(&v_full[vs]), vd = smem_addr(v_ptr(vs));
+        }
+        if (it >= kStages) ok = mbar_wait(smem_addr(&v_empty[st]), free_phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t vb = smem_addr(&v_full[st]), vd = smem_addr(v_ptr(st));
           mbar_arrive_expect_tx(vb, kTrTileBytes);
           tma_load_3d(vd, &tmV, vb, 0, kv, row);
           tma_load_3d(vd + kHalfTileBytes, &tmV, vb, 64, kv, row);
         }
       }
-      if (!ok) {
-        flag_error(p.err, GQA_DEVERR_TIMEOUT);
-        // Do not leave while copies into this CTA's shared memory may still be in flight: wait out
-        // every phase that a load was issued for (tile `it` may have its K loads alone).
-        if (piece > 0) (void)mbar_wait(smem_addr(q_full), static_cast<uint32_t>((piece - 1) & 1));
-        for (int i = (it + 1 > kTrKStages ? it + 1 - kTrKStages : 0); i <= it; ++i)
-          (void)mbar_wait(smem_addr(&k_full[i % kTrKStages]), static_cast<uint32_t>((i / kTrKStages) & 1));
-        for (int i = (it > kTrVStages ? it - kTrVStages : 0); i < it; ++i)
-          (void)mbar_wait(smem_addr(&v_full[i % kTrVStages]), static_cast<uint32_t>((i / kTrVStages) & 1));
-      }
+      if (ok && !q_sent) ok = send_q(true);
+      queries += q_sent;
+      ++piece;
     }
-  } else if (warp == kTrMmaWarp) {
-    // ------------------------------------------------------------------ MMA issuer
-    // Issue order within a piece: S_0, S_1, PV_0, S_2, PV_1, ..., PV_last.  S overwrites the buffer
-    // that held the P of two tiles before; that P V was issued before it and the tensor pipe runs
-    // them in order.
+    if (!ok && lane == 0) {
+      flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      // Do not leave while copies into this CTA's shared memory may still be in flight: wait out
+      // every phase that a load was issued for (tile `it` may have its K loads alone).
+      if (queries > 0) (void)mbar_wait(smem_addr(q_full), static_cast<uint32_t>((queries - 1) & 1));
+      for (int i = (it + 1 > kStages ? it + 1 - kStages : 0); i <= it; ++i)
+        (void)mbar_wait(smem_addr(&k_full[i % kStages]), static_cast<uint32_t>((i / kStages) & 1));
+      for (int i = (it > kStages ? it - kStages : 0); i < it; ++i)
+        (void)mbar_wait(smem_addr(&v_full[i % kStages]), static_cast<uint32_t>((i / kStages) & 1));
+    }
+  } else if (warp >= kTrMmaWarp) {
+    // ------------------------------------------------------------------ MMA issuer of a stream
+    // Issue order within a piece: S_0, S_1, PV_0, S_2, PV_1, ..., PV_last (of the stream's tiles).
+    // S overwrites the buffer that held the P of two tiles before; that P V was issued before it
+    // and the tensor pipe runs them in order.  With one row tile the tiles are given back by
+    // commits, at once: HBM is the bound.  With two the products are, and a commit holds the pipe up
+    // for about 100 cycles: there is one a tile, after S, which also says that every P V before is
+    // done, and the softmax warps that see it give the tiles back (64 nodes on 128k: 338 -> 291 us;
+    // done so with one row tile, 8 x 32k single tokens take 186 us instead of 176).
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_bf16_f32(kTrRows, kTile, false, false);
       constexpr uint32_t kIdO = idesc_bf16_f32(kTrRows, kHeadDim, false, true);
-      const uint32_t qa = smem_addr(qs);
-      int it = 0, piece = 0;
+      const int st = warp - kTrMmaWarp;
+      const uint32_t tm = tmem + st * kTrTmemStream;
+      uint64_t *const sf = s_full + 2 * st, *const pf = p_full + 2 * st;
+      // descriptors of the first tiles; the others differ in the start address alone (16-byte units,
+      // below 2^14 anywhere in shared memory), so one addition gives each: the issue must keep up
+      const uint64_t qd0 = sdesc_sw128(smem_addr(smem), 16, 1024), kd0 = sdesc_sw128(smem_addr(k_ptr(0)), 16, 1024),
+                     vd0 = sdesc_sw128(smem_addr(v_ptr(0)), kHalfTileBytes, 1024);
+      int it0 = 0, is = 0, piece = 0;  // the CTA's tiles before the piece, the stream's own, pieces
       bool ok = true;
-      auto issue_pv = [&](int t, bool first) -> bool {
-        const int pb = t & 1, s = t % kTrVStages;
-        if (!mbar_wait(smem_addr(&v_full[s]), static_cast<uint32_t>((t / kTrVStages) & 1))) return false;
-        if (!mbar_wait(smem_addr(&p_full[pb]), static_cast<uint32_t>((t >> 1) & 1))) return false;
+      // O += P V for the stream's tile number x, the CTA's tile number t
+      auto issue_pv = [&](int x, int t, bool first) -> bool {
+        const int pb = x & 1, sv = t % kStages;
+        if (!mbar_wait(smem_addr(&v_full[sv]), static_cast<uint32_t>((t / kStages) & 1))) return false;
+        if (!mbar_wait(smem_addr(&pf[pb]), static_cast<uint32_t>((x >> 1) & 1))) return false;
         tc_fence_after();
-        const uint32_t va = smem_addr(v_ptr(s));
+        const uint64_t vd = vd0 + static_cast<uint64_t>(sv * (kTrTileBytes / 16));
+        const uint32_t pt = tm + 64 * pb;
+        umma_bf16_ts(tm + kTrTmemO, pt, vd, kIdO, first ? 0u : 1u);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_bf16_ts(tmem + kTrTmemO, tmem + 64 * pb + 8 * k, sdesc_sw128(va + 2048 * k, kHalfTileBytes, 1024), kIdO,
-                       (!first || k > 0) ? 1u : 0u);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_bf16_ts(tmem + kTrTmemO, tmem + 64 * pb + 32 + 8 * k, sdesc_sw128(va + 2048 * k, kHalfTileBytes, 1024),
-                       kIdO, 1u);
-        umma_commit(smem_addr(&v_empty[s]));
-        umma_commit(smem_addr(pv_done));
+        for (int k = 1; k < 2 * kTile / 16; ++k)  // hi, then lo
+          umma_bf16_ts(tm + kTrTmemO, pt + 8 * k, vd + 128 * (k % (kTile / 16)), kIdO, 1u);
+        if (NQ == 1) umma_commit(smem_addr(&v_empty[sv]));
         return true;
       };
       while (ok && walk.next(p)) {
-        if (!has_rows(walk.b)) continue;
+        const int nr = row_tiles(walk.b);
+        if (nr == 0) continue;
+        const int nt = walk.j1 - walk.j0, step = nr == 1 ? 2 : 1, first = nr == 1 ? st : 0;
+        const uint64_t qd = qd0 + (nr == 2 ? st * (kTrQBytes / 16) : 0);
         ok = mbar_wait(smem_addr(q_full), static_cast<uint32_t>(piece & 1));
-        for (int j = walk.j0; j < walk.j1 && ok; ++j, ++it) {
-          const int s = it % kTrKStages, sb = it & 1;
-          ok = mbar_wait(smem_addr(&k_full[s]), static_cast<uint32_t>((it / kTrKStages) & 1));
+        for (int i = first; i < nt && ok; i += step, ++is) {
+          const int t = it0 + i, sk = t % kStages, sb = is & 1;
+          ok = mbar_wait(smem_addr(&k_full[sk]), static_cast<uint32_t>((t / kStages) & 1));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ka = smem_addr(k_ptr(s));
+          const uint64_t kd = kd0 + static_cast<uint64_t>(sk * (kTrTileBytes / 16));
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k)
-            umma_bf16(tmem + 64 * sb, sdesc_sw128(qa + (k >> 2) * (kTrRows * kHalfRowBytes) + 32 * (k & 3), 16, 1024),
-                      sdesc_sw128(ka + (k >> 2) * kHalfTileBytes + 32 * (k & 3), 16, 1024), kIdS, k > 0 ? 1u : 0u);
-          umma_commit(smem_addr(&k_empty[s]));
-          umma_commit(smem_addr(&s_full[sb]));
-          if (j == walk.j1 - 1) umma_commit(smem_addr(q_empty));
-          if (j > walk.j0) ok = issue_pv(it - 1, j - 1 == walk.j0);
-          // O of the piece before must have been read before this piece's first P V
-          if (j == walk.j0 && piece > 0 && ok) ok = mbar_wait(smem_addr(o_free), static_cast<uint32_t>((piece - 1) & 1));
+            umma_bf16(tm + 64 * sb, qd + (k >> 2) * (kTrRows * kHalfRowBytes / 16) + 2 * (k & 3),
+                      kd + (k >> 2) * (kHalfTileBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
+          umma_commit(smem_addr(&sf[sb]));
+          if (NQ == 1) umma_commit(smem_addr(&k_empty[sk]));
+          if (i > first) {
+            ok = issue_pv(is - 1, t - step, i - step == first);
+            if (i + step >= nt && ok) umma_commit(smem_addr(&pv_done[st]));  // all but the last P V
+          } else if (piece > 0) {
+            // O of the piece before must have been read before this piece's first P V
+            ok = mbar_wait(smem_addr(&o_free[st]), static_cast<uint32_t>((piece - 1) & 1));
+          }
         }
-        if (ok) ok = issue_pv(it - 1, walk.j1 - walk.j0 == 1);
-        if (ok) umma_commit(smem_addr(o_full));
+        if (first < nt) {
+          if (ok) {
+            const int last = first + (nt - 1 - first) / step * step;
+            ok = issue_pv(is - 1, it0 + last, last == first);
+          }
+          if (ok) umma_commit(smem_addr(&o_full[st]));
+        } else if (ok) {  // one tile, the other stream's
+          if (piece > 0) ok = mbar_wait(smem_addr(&o_free[st]), static_cast<uint32_t>((piece - 1) & 1));
+          mbar_arrive(smem_addr(&o_full[st]));
+        }
+        it0 += nt;
         ++piece;
       }
       if (!ok) flag_error(p.err, GQA_DEVERR_TIMEOUT);
-      if (it > 0) {  // nothing is deallocated while an MMA runs
-        umma_commit(smem_addr(drain));
-        if (!mbar_wait(smem_addr(drain), 0)) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      if (is > 0) {  // nothing is deallocated while an MMA runs
+        umma_commit(smem_addr(&drain[st]));
+        if (!mbar_wait(smem_addr(&drain[st]), 0)) flag_error(p.err, GQA_DEVERR_TIMEOUT);
       }
     }
   } else {
-    // ------------------------------------------------------------------ softmax warps
-    const int row = warp * 32 + lane;
+    // ------------------------------------------------------------------ softmax warps of a stream
+    const int st = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
     const int tl = row / p.G, g = row - tl * p.G;
-    const int t = r * p.Tt + tl;  // this row's node
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    int it = 0, piece = 0;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm = tmem + lane_base + st * kTrTmemStream;
+    uint64_t *const sf = s_full + 2 * st, *const pf = p_full + 2 * st;
+    int it0 = 0, is = 0, piece = 0, met = 0, pv = 0;  // (pv: pieces with more than one tile of the stream's)
     bool ok = true;
+    // A barrier of the eight softmax warps, with a limit to the wait (a warp that gave up on
+    // another wait does not come).
+    auto softmax_barrier = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(meet));
+      return mbar_wait(smem_addr(meet), static_cast<uint32_t>(met++ & 1));
+    };
     while (ok && walk.next(p)) {
       const int b = walk.b, j0 = walk.j0, j1 = walk.j1;
-      const int ctx = p.ctx_lens[b], n = tree_nodes(p, b, ctx);
-      if (r * p.Tt >= n) continue;
+      const int ctx = p.ctx_lens[b], n = tree_nodes(p, b, ctx), nr = row_tiles(b);
+      if (nr == 0) continue;
+      const int r = r0 + (nr == 2 ? st : 0), step = nr == 1 ? 2 : 1, first = nr == 1 ? st : 0;
+      const int t = r * p.Tt + tl;  // this row's node
       const bool valid = tl < p.Tt && t < n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const uint64_t *mrow = p.mask + (static_cast<long long>(b) * p.T + t) * p.words;
@@ -427,8 +533,9 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
         return left >= 64 ? m : m & ((1ull << left) - 1ull);
       };
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = j0; j < j1; ++j, ++it) {
-        const int sb = it & 1;
+      const uint32_t shares = nr == 1 ? 2 : 1;  // of the tiles' two users, those this stream stands for
+      for (int j = j0 + first; j < j1; j += step, ++is) {
+        const int sb = is & 1;
         const int o0 = j * kTile - ctx;  // the node at the tile's first slot; negative: context
         const bool tail = o0 > -kTile;   // the tile holds slots of nodes
         uint64_t see = ~0ull;
@@ -445,16 +552,18 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
           }
           // This tile's V: rows that no node owns (nothing has written them) are cleared, and
           // so is a non-finite value in a node's row, which would reach the rows that do not see the
-          // node as 0 x inf; the epilogue gives it to those that do.
-          const int vs = it % kTrVStages;
-          ok = mbar_wait(smem_addr(&v_full[vs]), static_cast<uint32_t>((it / kTrVStages) & 1));
+          // node as 0 x inf; the epilogue gives it to those that do.  When both streams use the
+          // tile, each looks at half of it.
+          const int tt = it0 + (j - j0), vs = tt % kStages;
+          ok = mbar_wait(smem_addr(&v_full[vs]), static_cast<uint32_t>((tt / kStages) & 1));
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           bool bad = false;
-          for (int c = row; c < 2 * kTile * 8; c += kTrRows) {  // 16-byte chunks: half, row, chunk
-            const int slot = (c >> 3) & (kTile - 1), node = o0 + slot;
+          const int share = nr == 2 ? 2 : 1;
+          for (int c = row + (nr == 2 ? st * kTrRows : 0); c < 2 * kTile * 8; c += share * kTrRows) {
+            const int slot = (c >> 3) & (kTile - 1), node = o0 + slot;  // 16-byte chunks: half, row, chunk
             if (node < 0) continue;
             uint4 *at = reinterpret_cast<uint4 *>(v_ptr(vs)) + c;
             if (node >= n) {
@@ -474,25 +583,36 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
               bad = true;
             }
           }
-          if (bad) atomicMax(v_bad, static_cast<uint32_t>(piece + 1));
+          if (bad) atomicMax(&v_bad[piece & 3], static_cast<uint32_t>(piece + 1));
           fence_proxy_async_smem();
+          if (nr == 2) ok = softmax_barrier();
         }
-        ok = mbar_wait(smem_addr(&s_full[sb]), static_cast<uint32_t>((it >> 1) & 1));
+        ok = ok && mbar_wait(smem_addr(&sf[sb]), static_cast<uint32_t>((is >> 1) & 1));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
+        if ((warp & 3) == 0 && lane == 0) {
+          // S is done with the K tile, the P V of two tiles before with its V tile, and the last S
+          // of the piece with the queries
+          const int i = j - j0;
+          if (NQ == 2) {
+            mbar_arrive_n(smem_addr(&k_empty[(it0 + i) % kStages]), shares);
+            if (i >= first + 2 * step) mbar_arrive_n(smem_addr(&v_empty[(it0 + i - 2 * step) % kStages]), shares);
+          }
+          if (j + step >= j1) mbar_arrive(smem_addr(q_empty));
+        }
         if (!warp_valid) {  // no node in this warp's rows: what P holds there reaches no output
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&p_full[sb]));
+          if (lane == 0) mbar_arrive(smem_addr(&pf[sb]));
           continue;
         }
         tc_fence_after();
         float sv[64];
         {
           float a[32], c[32];
-          tmem_ld32(tmem + lane_base + 64 * sb, a);
-          tmem_ld32(tmem + lane_base + 64 * sb + 32, c);
+          tmem_ld32(tm + 64 * sb, a);
+          tmem_ld32(tm + 64 * sb + 32, c);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -508,15 +628,14 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
             sv[32 + c] = (s1 >> c) & 1u ? sv[32 + c] : -INFINITY;
           }
         }
-        float m8[8];
+        float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sv[e], sv[e + 8]);
+        for (int c = 4; c < 60; c += 8)
 #pragma unroll
-        for (int c = 16; c < 64; c += 8)
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], sv[c + e], sv[c + 4 + e]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], sv[c + e]);
-        const float mx =
-            fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], sv[60 + e]);
+        const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
         const float m_new = fmaxf(m_run, mx * p.scale_log2);
         float corr = 1.f;
         bool resc = false;
@@ -524,12 +643,15 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
           corr = fast_exp2(m_run - m_new);  // 0 before the row's first seen key
           m_run = m_new;
           l_run *= corr;
-          resc = j > j0;
+          resc = j > j0 + first;
         }
         if (__any_sync(0xffffffffu, resc)) {
-          // O must hold every P V before this tile's when it is scaled.  (S was issued after the P V
-          // of two tiles before, so the parity wait is never more than one phase ahead.)
-          ok = mbar_wait(smem_addr(pv_done), static_cast<uint32_t>((it - 1) & 1));
+          // O must hold every P V before this tile's when it is scaled: the next S comes after them,
+          // or, behind the piece's last S, a commit of their own.
+          if (j + step < j1)
+            ok = mbar_wait(smem_addr(&sf[sb ^ 1]), static_cast<uint32_t>(((is + 1) >> 1) & 1));
+          else
+            ok = mbar_wait(smem_addr(&pv_done[st]), static_cast<uint32_t>(pv & 1));
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -538,57 +660,103 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
 #pragma unroll
           for (int c4 = 0; c4 < 4; ++c4) {
             float o[32];
-            tmem_ld32(tmem + lane_base + kTrTmemO + 32 * c4, o);
+            tmem_ld32(tm + kTrTmemO + 32 * c4, o);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= corr;
-            tmem_st32(tmem + lane_base + kTrTmemO + 32 * c4, o);
+            tmem_st32(tm + kTrTmemO + 32 * c4, o);
           }
         }
-        // P = 2^(s - m) as bf16 hi + lo pairs into the S buffer's columns
+        // P = 2^(s - m) as bf16 hi + lo pairs into the S buffer's columns: hi the leading 8 bits of the
+        // significand as they are, lo the rest rounded (to 2^-16 of the weight in all)
         uint32_t ph[32], pl[32];
-        float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen no key yet: P = 0
+        const f2 scale2 = make_f2(p.scale_log2, p.scale_log2), neg2 = make_f2(neg_m, neg_m), minus = make_f2(-1.f, -1.f);
+        f2 rs[4] = {{0}, {0}, {0}, {0}};
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          const float v0 = fast_exp2(fmaf(sv[2 * c], p.scale_log2, neg_m));
-          const float v1 = fast_exp2(fmaf(sv[2 * c + 1], p.scale_log2, neg_m));
-          rs8[c & 7] += v0 + v1;
-          ph[c] = pack_bf16(v0, v1);
-          pl[c] = pack_bf16(v0 - bf16_lo_to_float(ph[c]), v1 - bf16_hi_to_float(ph[c]));
+          float v0, v1, e0, e1;
+          split_f2(fma_f2(make_f2(sv[2 * c], sv[2 * c + 1]), scale2, neg2), v0, v1);
+          v0 = fast_exp2(v0);
+          v1 = fast_exp2(v1);
+          const f2 v = make_f2(v0, v1);
+          rs[c & 3] = add_f2(rs[c & 3], v);
+          const uint32_t h0 = __float_as_uint(v0) & 0xffff0000u, h1 = __float_as_uint(v1) & 0xffff0000u;
+          ph[c] = __byte_perm(h0, h1, 0x7632);
+          split_f2(fma_f2(make_f2(__uint_as_float(h0), __uint_as_float(h1)), minus, v), e0, e1);
+          pl[c] = pack_bf16(e0, e1);
         }
-        tmem_st32(tmem + lane_base + 64 * sb, ph);
-        tmem_st32(tmem + lane_base + 64 * sb + 32, pl);
-        l_run += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+        tmem_st32(tm + 64 * sb, ph);
+        tmem_st32(tm + 64 * sb + 32, pl);
+        float l0, l1;
+        split_f2(add_f2(add_f2(rs[0], rs[1]), add_f2(rs[2], rs[3])), l0, l1);
+        l_run += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&p_full[sb]));
+        if (lane == 0) mbar_arrive(smem_addr(&pf[sb]));
       }
-      if (!ok) break;
-
-      // The piece's O: to the output if the piece is its whole segment, else to its slot of the
-      // workspace (a range has at most two cut pieces, its first and its last).
-      ok = mbar_wait(smem_addr(o_full), static_cast<uint32_t>(piece & 1));
+      float f_own = 1.f, f_other = 0.f;
+      if (ok) ok = mbar_wait(smem_addr(&o_full[st]), static_cast<uint32_t>(piece & 1));
+      if (j0 + first + step < j1) ++pv;
+      if ((warp & 3) == 0 && lane == 0 && ok) {  // every P V is done: the last two V tiles
+        const int nt = j1 - j0, last = first + (nt - 1 - first) / step * step;
+        if (NQ == 2 && first < nt) mbar_arrive_n(smem_addr(&v_empty[(it0 + last) % kStages]), shares);
+        if (NQ == 2 && first + step < nt) mbar_arrive_n(smem_addr(&v_empty[(it0 + last - step) % kStages]), shares);
+        if (first >= nt) mbar_arrive(smem_addr(q_empty));  // this stream had no tile
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && nr == 1) {
+        // Join the streams: each thread learns its row's (m, l) in the other one.  (Both threads of a
+        // row have read the last joined piece's before this stream's O was free for this one.)
+        s_ml[st * kTrRows + row] = make_float2(m_run, l_run);
+        ok = softmax_barrier();
+        const float2 x = s_ml[(st ^ 1) * kTrRows + row];
+        if (x.y != 0.f) {
+          const float M = l_run != 0.f ? fmaxf(m_run, x.x) : x.x;
+          f_own = l_run != 0.f ? fast_exp2(m_run - M) : 0.f;
+          f_other = fast_exp2(x.x - M);
+          l_run = st == 0 ? fmaf(x.y, f_other, l_run * f_own) : fmaf(l_run, f_own, x.y * f_other);
+          m_run = M;
+        }
+        if (ok) ok = mbar_wait(smem_addr(&o_full[st ^ 1]), static_cast<uint32_t>(piece & 1));
+      }
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
+      // The piece's O: to the output if the piece is its whole sequence, else to its slot of the
+      // workspace (a range has at most two cut pieces, its first and its last).  Streams that
+      // share the row tile write half of the dims each.
       tc_fence_after();
       if (warp_valid) {
         bool bad = false;
-        if (j1 * kTile > ctx) {
-          // every softmax warp's look at V came before its P, which came before this O
-          bad = *reinterpret_cast<volatile uint32_t *>(v_bad) == static_cast<uint32_t>(piece + 1);
-        }
+        if (j1 * kTile > ctx)  // every softmax warp's look at V came before its P, which came before this O
+          bad = *reinterpret_cast<volatile uint32_t *>(&v_bad[piece & 3]) == static_cast<uint32_t>(piece + 1);
         const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // (NaN stays NaN)
-        uint16_t *dst = p.out + ((static_cast<long long>(b) * p.T + t) * p.Hq + walk.kv * p.G + g) * kHeadDim;
-        float *mine = p.part + (static_cast<long long>(blockIdx.x) * 2 + (j0 > 0 ? 0 : 1)) * kTrPartFloats;
+        uint16_t *dst = p.out + ((static_cast<long long>(b) * p.T + t) * p.Hq + kv * p.G + g) * kHeadDim;
+        float *mine = p.part + (((static_cast<long long>(w) * p.Hkv + kv) * p.R + r) * 2 + (j0 > 0 ? 0 : 1)) * kTrPartFloats;
+        const int c0 = nr == 1 ? 2 * st : 0, c1 = nr == 1 ? c0 + 2 : 4;
+        const bool two = nr == 1 && j1 - j0 > 1;  // both streams have an O
 #pragma unroll 1
-        for (int c4 = 0; c4 < 4; ++c4) {
+        for (int c4 = c0; c4 < c1; ++c4) {
           float o[32];
-          tmem_ld32(tmem + lane_base + kTrTmemO + 32 * c4, o);
-          tmem_wait_ld();
+          if (nr == 1) {
+            const uint32_t t0 = tmem + lane_base + kTrTmemO + 32 * c4;
+            tmem_ld32(t0, o);
+            tmem_wait_ld();
+            const float f0 = st == 0 ? f_own : f_other, f1 = st == 0 ? f_other : f_own;
+            if (two) {
+              float o1[32];
+              tmem_ld32(t0 + kTrTmemStream, o1);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e] * f0);
+            }
+          } else {
+            tmem_ld32(tm + kTrTmemO + 32 * c4, o);
+            tmem_wait_ld();
+          }
           if (bad && valid) {
             // values of seen nodes that are not finite: p x inf for some p > 0
 #pragma unroll 1
@@ -601,7 +769,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
                 if (pg < 0 || pg >= p.num_blocks) continue;
                 crow = static_cast<long long>(pg) * kTile + (slot & (kTile - 1));
               }
-              const uint32_t *v = reinterpret_cast<const uint32_t *>(p.v_cache + (crow * p.Hkv + walk.kv) * kHeadDim) + 16 * c4;
+              const uint32_t *v = reinterpret_cast<const uint32_t *>(p.v_cache + (crow * p.Hkv + kv) * kHeadDim) + 16 * c4;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const uint32_t y = v[e];
@@ -623,21 +791,25 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
                                  pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
           }
         }
-        if (!walk.whole) {
+        if (!walk.whole && (nr == 2 || st == 0)) {
           mine[kHeadDim * kTrRows + row] = m_run;
           mine[(kHeadDim + 1) * kTrRows + row] = l_run;
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(o_free));
+      if (lane == 0) {  // both streams' O have been read by a warp of each, or one by its own alone
+        mbar_arrive(smem_addr(&o_free[st]));
+        mbar_arrive(smem_addr(&o_free[nr == 1 ? st ^ 1 : st]));
+      }
+      it0 += j1 - j0;
       ++piece;
     }
     if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
   }
 
   // ------------------------------------------------------------------ teardown
-  __syncwarp();  // the producer and MMA warps ran their loops on lane 0 alone
+  __syncwarp();  // the MMA warps ran their loops on lane 0 alone
   tc_fence_before();
   __syncthreads();
   if (warp == kTrMmaWarp) {
@@ -647,68 +819,89 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtasPerSm)
 }
 
 // ----------------------------------------------------------------------------------- merge
-// One CTA per (segment, row tile, 16 dims); a thread takes four rows and a dim.  A segment that
-// one range held whole is already written.  The parts are joined in the order of the ranges:
-// out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, kept as a running (M, sum, sum) pair.
-constexpr int kTrMergeDims = 16;
-constexpr int kTrMergeThreads = 32 * kTrMergeDims;
-constexpr int kTrMergeAhead = 4;
-__global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-  griddep_wait();  // the attention kernel's partials
+// One CTA per (boundary between two ranges, KV head and row tile, 32 dims): it joins the parts of
+// the sequence that the boundary cuts, if it is the first to cut it.  A warp takes four dims, a lane
+// four rows (of column-major partials: 512 contiguous bytes a load).  The parts come in the order of
+// the ranges: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, kept as a running (M, sum, sum).
+// What to join follows from the lengths, which the attention kernel has waited for before it let
+// this one start, so it is found before the wait.
+constexpr int kTrMergeDims = 32;
+constexpr int kTrMergeThreads = 256;
+constexpr int kTrMergePer = kTrMergeDims / (kTrMergeThreads / 32);  // dims of a warp
+constexpr int kTrMergePitch = kTrMergeDims + 8;                     // of the output staged in shared memory
+__global__ void __launch_bounds__(kTrMergeThreads, 3) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ __align__(16) uint16_t s_out[kTrRows][kTrMergePitch];
   const int lane = threadIdx.x & 31;
-  const int seg = static_cast<int>(blockIdx.x) / p.R, r = static_cast<int>(blockIdx.x) % p.R;
-  const int b = seg / p.Hkv, kv = seg - b * p.Hkv;
-  const int ctx = p.ctx_lens[b], n = tree_nodes(p, b, ctx);
-  if (r * p.Tt >= n) return;
+  const int unit = static_cast<int>(blockIdx.x) % (p.Hkv * p.R), cut = static_cast<int>(blockIdx.x) / (p.Hkv * p.R) + 1;
+  const int r = unit % p.R, kv = unit / p.R;
   long long lane_first = 0;
   const long long total = tree_total(p, lane, &lane_first);
   const int ranges = tree_ranges(p, total);
-  const int per = (p.B + 31) / 32;
-  long long first = __shfl_sync(0xffffffffu, lane_first, b / per);
-  for (int x = b / per * per; x < b; ++x) first += static_cast<long long>(tree_tiles(p, x)) * p.Hkv;
-  const int nt = tree_tiles(p, b);
-  first += static_cast<long long>(kv) * nt;
-  const int w0 = worker_of(total, ranges, first), w1 = worker_of(total, ranges, first + nt - 1);
-  if (w0 == w1) return;
-  const int rq = lane, d = kTrMergeDims * static_cast<int>(blockIdx.y) + static_cast<int>(threadIdx.x) / 32;
-  if (4 * rq >= min(p.Tt, n - r * p.Tt) * p.G) return;  // rows past the tile's last node
-  float M[4], L[4], A[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) M[k] = -INFINITY, L[k] = 0.f, A[k] = 0.f;
-  for (int wb = w0; wb <= w1; wb += kTrMergeAhead) {
-    float4 m[kTrMergeAhead], l[kTrMergeAhead], o[kTrMergeAhead];
-#pragma unroll
-    for (int e = 0; e < kTrMergeAhead; ++e) {
-      const int w = wb + e;
-      if (w > w1) continue;
-      const float *sp = p.part + ((static_cast<long long>(w) * p.R + r) * 2 + (w == w0 ? 1 : 0)) * kTrPartFloats + 4 * rq;
-      m[e] = __ldcg(reinterpret_cast<const float4 *>(sp + kHeadDim * kTrRows));
-      l[e] = __ldcg(reinterpret_cast<const float4 *>(sp + (kHeadDim + 1) * kTrRows));
-      o[e] = __ldcg(reinterpret_cast<const float4 *>(sp + d * kTrRows));
+  int b = 0, n = 0, w0 = 0, w1 = -1;
+  if (cut < ranges) {
+    const long long at = worker_begin(total, ranges, cut);
+    long long first = 0;
+    tree_find(p, lane, lane_first, at, &b, &first);
+    n = tree_nodes(p, b, p.ctx_lens[b]);
+    // not between two sequences, a node in this row tile, and no earlier boundary in the sequence
+    if (first != at && r * p.Tt < n && worker_of(total, ranges, first) == cut - 1) {
+      w0 = cut - 1;
+      w1 = worker_of(total, ranges, first + tree_tiles(p, b) - 1);
     }
+  }
+  griddep_wait();  // the attention kernel's partials, and its own reads of what follows this call
+  if (w1 < w0) return;
+  const int rows = min(p.Tt, n - r * p.Tt) * p.G;  // of the row tile
+  const int dl = kTrMergePer * (static_cast<int>(threadIdx.x) / 32), d = kTrMergeDims * static_cast<int>(blockIdx.y) + dl;
+  if (4 * lane < rows) {
+    float M[4], L[4], A[kTrMergePer][4];
 #pragma unroll
-    for (int e = 0; e < kTrMergeAhead; ++e) {
-      if (wb + e > w1) continue;
-      const float mm[4] = {m[e].x, m[e].y, m[e].z, m[e].w}, ll[4] = {l[e].x, l[e].y, l[e].z, l[e].w},
-                  oo[4] = {o[e].x, o[e].y, o[e].z, o[e].w};
+    for (int k = 0; k < 4; ++k) {
+      M[k] = -INFINITY, L[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kTrMergePer; ++e) A[e][k] = 0.f;
+    }
+    float4 m, l, o[kTrMergePer];
+    auto load = [&](int w) {
+      const float *sp =
+          p.part + ((static_cast<long long>(w) * p.Hkv * p.R + unit) * 2 + (w == w0 ? 1 : 0)) * kTrPartFloats + 4 * lane;
+      m = __ldcg(reinterpret_cast<const float4 *>(sp + kHeadDim * kTrRows));
+      l = __ldcg(reinterpret_cast<const float4 *>(sp + (kHeadDim + 1) * kTrRows));
+#pragma unroll
+      for (int e = 0; e < kTrMergePer; ++e) o[e] = __ldcg(reinterpret_cast<const float4 *>(sp + (d + e) * kTrRows));
+    };
+    load(w0);
+    for (int w = w0; w <= w1; ++w) {
+      const float mm[4] = {m.x, m.y, m.z, m.w}, ll[4] = {l.x, l.y, l.z, l.w};
+      float oo[kTrMergePer][4];
+#pragma unroll
+      for (int e = 0; e < kTrMergePer; ++e) oo[e][0] = o[e].x, oo[e][1] = o[e].y, oo[e][2] = o[e].z, oo[e][3] = o[e].w;
+      if (w < w1) load(w + 1);  // in flight while this part is added
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (ll[k] == 0.f) continue;  // a part that saw none of the row's keys
         const float m2 = fmaxf(M[k], mm[k]);
         const float f = fast_exp2(M[k] - m2), h = fast_exp2(mm[k] - m2);
         L[k] = fmaf(L[k], f, ll[k] * h);
-        A[k] = fmaf(A[k], f, oo[k] * h);
+#pragma unroll
+        for (int e = 0; e < kTrMergePer; ++e) A[e][k] = fmaf(A[e][k], f, oo[e][k] * h);
         M[k] = m2;
       }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = 4 * rq + k, tl = row / p.G, g = row - tl * p.G, t = r * p.Tt + tl;
-    if (tl >= p.Tt || t >= n) continue;
-    const float inv = L[k] != 0.f ? 1.f / L[k] : 0.f;
-    p.out[((static_cast<long long>(b) * p.T + t) * p.Hq + kv * p.G + g) * kHeadDim + d] =
-        static_cast<uint16_t>(pack_bf16(A[k] * inv, 0.f) & 0xffffu);
+    for (int k = 0; k < 4; ++k) {
+      const float inv = L[k] != 0.f ? 1.f / L[k] : 0.f;
+#pragma unroll
+      for (int e = 0; e < kTrMergePer; e += 2)
+        *reinterpret_cast<uint32_t *>(&s_out[4 * lane + k][dl + e]) = pack_bf16(A[e][k] * inv, A[e + 1][k] * inv);
+    }
+  }
+  __syncthreads();
+  constexpr int kChunks = kTrMergeDims / 8;  // of 16 bytes
+  for (int x = threadIdx.x; x < rows * kChunks; x += kTrMergeThreads) {
+    const int row = x / kChunks, c = x % kChunks, tl = row / p.G, g = row - tl * p.G;
+    *reinterpret_cast<uint4 *>(p.out + ((static_cast<long long>(b) * p.T + r * p.Tt + tl) * p.Hq + kv * p.G + g) * kHeadDim +
+                               kTrMergeDims * blockIdx.y + 8 * c) = *reinterpret_cast<const uint4 *>(&s_out[row][8 * c]);
   }
 }
 
@@ -725,9 +918,10 @@ gqa_status_t tree_device(int device, int *sms) {
   *sms = g_tree_sms[device].load(std::memory_order_acquire);
   if (*sms > 0) return GQA_OK;
   int n = 0;
-  if (cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTrSmemBytes) != cudaSuccess ||
-      cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
+  if (cudaFuncSetAttribute(tree_attn_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem<1>::kBytes) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(tree_attn_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem<2>::kBytes) !=
+          cudaSuccess ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
@@ -737,23 +931,40 @@ gqa_status_t tree_device(int device, int *sms) {
   return GQA_OK;
 }
 
-gqa_status_t tree_check(const gqa_tree_desc_t &d) {
-  const gqa_status_t st = check_cache_geometry(d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, d.tree_len,
-                                               d.block_size, d.max_seq_len, d.num_cache_blocks);
-  if (st != GQA_OK) return st;
-  return d.tree_len > GQA_MAX_TREE ? GQA_ERR_INVALID_ARG : GQA_OK;
-}
-
 int tree_row_tiles(const gqa_tree_desc_t &d) {
   const int per = kTrRows / (d.num_q_heads / d.num_kv_heads);
   return (d.tree_len + per - 1) / per;
 }
+
+gqa_status_t tree_check(const gqa_tree_desc_t &d) {
+  const gqa_status_t st = check_cache_geometry(d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, d.tree_len,
+                                               d.block_size, d.max_seq_len, d.num_cache_blocks);
+  if (st != GQA_OK) return st;
+  if (d.tree_len > GQA_MAX_TREE) return GQA_ERR_INVALID_ARG;
+  return static_cast<long long>(d.batch) * d.num_kv_heads * tree_row_tiles(d) > 0x7fffffffLL ? GQA_ERR_UNSUPPORTED : GQA_OK;
+}
+
+// CTAs a range: one per KV head and row tile, or pair of row tiles.
+int tree_units(const gqa_tree_desc_t &d) {
+  const int r = tree_row_tiles(d);
+  return d.num_kv_heads * (r > 1 ? (r + 1) / 2 : 1);
+}
+// Ranges of a call: as many as the GPU holds at once, a CTA per SM; where that leaves more than a
+// tenth of it idle (many heads or row tiles), as many as fill two or three rounds, if that is better.
 int tree_max_ranges(const gqa_tree_desc_t &d, int sms) {
-  const int w = kTrCtasPerSm * sms / tree_row_tiles(d);
-  return w > 1 ? w : 1;
+  const long long slots = sms, units = tree_units(d);
+  long long best = 1, best_rounds = (units + slots - 1) / slots;
+  for (long long rounds = 1; rounds <= 3; ++rounds) {
+    const long long w = slots * rounds / units;
+    // of the slots of the rounds, the share that has work: w units / (rounds slots)
+    if (w >= 1 && 10 * w * best_rounds > 11 * best * rounds) best = w, best_rounds = rounds;
+  }
+  return static_cast<int>(best);
 }
 size_t tree_part_bytes(const gqa_tree_desc_t &d, int sms) {
-  return static_cast<size_t>(tree_max_ranges(d, sms)) * tree_row_tiles(d) * 2 * kTrPartFloats * sizeof(float);
+  const int w = tree_max_ranges(d, sms);
+  if (w == 1) return 256;  // nothing is cut
+  return static_cast<size_t>(w) * d.num_kv_heads * tree_row_tiles(d) * 2 * kTrPartFloats * sizeof(float);
 }
 
 }  // namespace
@@ -861,10 +1072,13 @@ extern "C" gqa_status_t gqa_tree_attn(const gqa_tree_desc_t *desc, const void *q
       !make_cache_map(&tv, v_cache, p.Hkv, rows))
     return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_pdl(tree_attn_kernel, dim3(static_cast<unsigned>(p.W * p.R)), dim3(kTrThreads),
-                 static_cast<size_t>(kTrSmemBytes), s, tq, tk, tv, p) != cudaSuccess ||
-      launch_pdl(tree_merge_kernel, dim3(static_cast<unsigned>(p.B * p.Hkv * p.R), kHeadDim / kTrMergeDims),
-                 dim3(kTrMergeThreads), 0, s, p) != cudaSuccess) {
+  const bool pairs = p.R > 1;
+  if (launch_pdl(pairs ? tree_attn_kernel<2> : tree_attn_kernel<1>, dim3(static_cast<unsigned>(p.W * tree_units(d))),
+                 dim3(kTrThreads), static_cast<size_t>(pairs ? TreeSmem<2>::kBytes : TreeSmem<1>::kBytes), s, tq, tk, tv,
+                 p) != cudaSuccess ||
+      (p.W > 1 &&
+       launch_pdl(tree_merge_kernel, dim3(static_cast<unsigned>((p.W - 1) * p.Hkv * p.R), kHeadDim / kTrMergeDims),
+                  dim3(kTrMergeThreads), 0, s, p) != cudaSuccess)) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
