@@ -99,31 +99,98 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
   return n > 0 ? (ctx + n + kTile - 1) / kTile : 0;
 }
 
-// Walks the sequences a range [pos, end) of KV tiles covers.  Every warp of the CTA runs its own
-// copy, all lanes alike.
+// How the batch is cut.  Tiles are numbered sequence after sequence; behind each sequence with tiles
+// but the last, `gap` numbers are left out, the cost of a piece's end in tiles (the streams run
+// dry, O goes out: about 8 us), so that a range with many short sequences gets fewer tiles.  Range w
+// of W has the numbers [worker_begin(total, W, w), worker_begin(total, W, w + 1)).
+constexpr int kTrPieceCost = 10;
+constexpr int kTrMinTiles = 4;  // of a range, so that small batches leave few partials
+struct TreeCut {
+  long long total;  // numbers in use
+  int ranges;
+  int gap;
+  // of the warp's lane: the first number of its sequences (it sums sequences [lane per, lane per + per))
+  long long lane_first;
+};
+// Every lane of a warp calls these alike.
+__device__ __forceinline__ TreeCut tree_cut(const TreeParams &p, int lane) {
+  const int per = (p.B + 31) / 32, b0 = lane * per, b1 = min(p.B, b0 + per);
+  long long tiles = 0;
+  int seqs = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int nt = tree_tiles(p, b);
+    tiles += nt;
+    seqs += nt > 0;
+  }
+  const long long own_tiles = tiles;
+  const int own_seqs = seqs;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, tiles, o);
+    const int z = __shfl_up_sync(0xffffffffu, seqs, o);
+    if (lane >= o) tiles += y, seqs += z;
+  }
+  const long long all = __shfl_sync(0xffffffffu, tiles, 31);
+  const int all_seqs = __shfl_sync(0xffffffffu, seqs, 31);
+  TreeCut c;
+  const long long most = (all + kTrMinTiles - 1) / kTrMinTiles;
+  c.ranges = static_cast<int>(most < p.W ? most : p.W);
+  const long long quarter = c.ranges > 0 ? all / (4 * c.ranges) : 0;  // of a range
+  c.gap = static_cast<int>(quarter < kTrPieceCost ? quarter : kTrPieceCost);
+  c.total = all + (all_seqs > 1 ? static_cast<long long>(c.gap) * (all_seqs - 1) : 0);
+  c.lane_first = tiles - own_tiles + static_cast<long long>(c.gap) * (seqs - own_seqs);
+  return c;
+}
+__device__ __forceinline__ int tree_span(const TreeParams &p, int b, int gap) {
+  const int nt = tree_tiles(p, b);
+  return nt > 0 ? nt + gap : 0;
+}
+// The sequence whose numbers (or the gap behind them) hold `at` < total, and its first number.
+__device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c, long long at, int *b, long long *seq0) {
+  // the last lane whose first number is <= at (lanes without tiles share their successor's)
+  const uint32_t le = __ballot_sync(0xffffffffu, c.lane_first <= at);
+  const int owner = 31 - __clz(le);
+  const int per = (p.B + 31) / 32;
+  long long s = __shfl_sync(0xffffffffu, c.lane_first, owner);
+  int x = owner * per;
+  while (x + 1 < p.B) {
+    const long long nxt = s + tree_span(p, x, c.gap);
+    if (nxt > at) break;
+    s = nxt;
+    ++x;
+  }
+  *b = x;
+  *seq0 = s;
+}
+
+// Walks the sequences a range [pos, end) covers.  Every warp of the CTA runs its own copy, all
+// lanes alike.
 struct TreeWalk {
-  long long pos, end;  // tiles still to do
-  long long seq0;      // first tile of sequence b
-  int b, nt;           // sequence, its tiles
+  long long pos, end;  // numbers still to do
+  long long seq0;      // first number of sequence b
+  int b, nt, gap;      // sequence, its tiles
   // of the piece at hand
   int j0, j1;
   bool whole;          // the piece is its whole sequence
 
-  __device__ __forceinline__ void start(const TreeParams &p, long long begin, long long stop, int b0, long long s0) {
+  __device__ __forceinline__ void start(const TreeParams &p, long long begin, long long stop, int b0, long long s0, int g) {
     pos = begin;
     end = stop;
     b = b0;
     seq0 = s0;
+    gap = g;
     nt = pos < end ? tree_tiles(p, b) : 0;
   }
   // The next piece; false when the range is done.
   __device__ __forceinline__ bool next(const TreeParams &p) {
-    if (pos >= end) return false;
-    while (pos >= seq0 + nt) {
-      seq0 += nt;
+    while (pos < end && pos >= seq0 + nt) {  // on to the next sequence
+      seq0 += nt > 0 ? nt + gap : 0;
+      if (pos < seq0) pos = seq0;
+      if (pos >= end) break;
       ++b;
       nt = tree_tiles(p, b);
     }
+    if (pos >= end) return false;
     j0 = static_cast<int>(pos - seq0);
     const long long left = end - pos;
     j1 = left < nt - j0 ? j0 + static_cast<int>(left) : nt;
@@ -133,39 +200,6 @@ struct TreeWalk {
   }
 };
 
-// The batch's KV tiles, and the sequence (and its first tile) that holds tile `at`: a warp sums
-// its lanes' sequences, then looks into the lane that holds it.  All lanes get the same answer.
-__device__ __forceinline__ long long tree_total(const TreeParams &p, int lane, long long *lane_first) {
-  const int per = (p.B + 31) / 32, b0 = lane * per, b1 = min(p.B, b0 + per);
-  long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += tree_tiles(p, b);
-  long long x = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  *lane_first = x - sum;
-  return __shfl_sync(0xffffffffu, x, 31);
-}
-__device__ __forceinline__ void tree_find(const TreeParams &p, int lane, long long lane_first, long long at, int *b,
-                                          long long *seq0) {
-  // the last lane whose first tile is <= at (lanes without tiles share their successor's first)
-  const uint32_t le = __ballot_sync(0xffffffffu, lane_first <= at);
-  const int owner = 31 - __clz(le);
-  const int per = (p.B + 31) / 32;
-  long long s = __shfl_sync(0xffffffffu, lane_first, owner);
-  int x = owner * per;
-  while (x + 1 < p.B) {
-    const long long nxt = s + tree_tiles(p, x);
-    if (nxt > at) break;
-    s = nxt;
-    ++x;
-  }
-  *b = x;
-  *seq0 = s;
-}
-
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
@@ -173,13 +207,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-// Ranges in use: at least kTrMinTiles tiles each, so that small batches leave few partials.
-constexpr int kTrMinTiles = 4;
-__device__ __forceinline__ int tree_ranges(const TreeParams &p, long long total) {
-  const long long most = (total + kTrMinTiles - 1) / kTrMinTiles;
-  return static_cast<int>(most < p.W ? most : p.W);
 }
 
 }  // namespace
@@ -298,7 +325,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // everything below may come from the preceding kernel
-  griddep_launch_dependents();  // only tree_merge_kernel follows early, and it waits
+  if (p.W > 1) griddep_launch_dependents();  // tree_merge_kernel follows, and it waits
 
   // Sequences with invalid lengths: flagged, zeros in all their rows.
   for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x)) {
@@ -310,19 +337,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (long long c = tid; c < n; c += kTrThreads) dst[c] = make_uint4(0, 0, 0, 0);
   }
 
-  long long lane_first = 0;
-  const long long total = tree_total(p, lane, &lane_first);
-  const int ranges = tree_ranges(p, total);
   TreeWalk walk;
   {
+    const TreeCut cut = tree_cut(p, lane);
     long long begin = 0, stop = 0, seq0 = 0;
     int b = 0;
-    if (w < ranges) {
-      begin = total * w / ranges;
-      stop = total * (w + 1) / ranges;
-      tree_find(p, lane, lane_first, begin, &b, &seq0);
+    if (w < cut.ranges) {
+      begin = worker_begin(cut.total, cut.ranges, w);
+      stop = worker_begin(cut.total, cut.ranges, w + 1);
+      tree_find(p, cut, begin, &b, &seq0);
     }
-    walk.start(p, begin, stop, b, seq0);
+    walk.start(p, begin, stop, b, seq0, cut.gap);
   }
   auto k_ptr = [&](int s) { return smem + Smem::kOffK + s * kTrTileBytes; };
   auto v_ptr = [&](int s) { return smem + Smem::kOffV + s * kTrTileBytes; };
@@ -525,11 +550,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       const bool valid = tl < p.Tt && t < n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const uint64_t *mrow = p.mask + (static_cast<long long>(b) * p.T + t) * p.words;
+      const uint64_t mask0 = valid ? mrow[0] : 0ull;  // on the way while the context is streamed
       // bits 64 x .. 64 x + 63 of the node's mask, none from n on
       auto mask_word = [&](int x) -> uint64_t {
         const int left = n - 64 * x;
         if (left <= 0) return 0ull;
-        const uint64_t m = mrow[x];
+        const uint64_t m = x == 0 ? mask0 : mrow[x];
         return left >= 64 ? m : m & ((1ull << left) - 1ull);
       };
       float m_run = -INFINITY, l_run = 0.f;
@@ -560,27 +586,26 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             ok = false;
             break;
           }
+          // 16-byte chunks: half (c >> 9), slot, chunk; four of a thread's at a time
           bool bad = false;
-          const int share = nr == 2 ? 2 : 1;
-          for (int c = row + (nr == 2 ? st * kTrRows : 0); c < 2 * kTile * 8; c += share * kTrRows) {
-            const int slot = (c >> 3) & (kTile - 1), node = o0 + slot;  // 16-byte chunks: half, row, chunk
-            if (node < 0) continue;
-            uint4 *at = reinterpret_cast<uint4 *>(v_ptr(vs)) + c;
-            if (node >= n) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint4 x = *at;
-            uint32_t y[4] = {x.x, x.y, x.z, x.w};
-            bool hit = false;
+          const int each = nr * kTrRows;
+          for (int cb = row + (nr == 2 ? st * kTrRows : 0); cb < 2 * kTile * 8; cb += 4 * each) {
+            uint4 q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = reinterpret_cast<const uint4 *>(v_ptr(vs))[cb + e * each];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u, hit = true;
-              if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0xffffu, hit = true;
-            }
-            if (hit) {
-              *at = make_uint4(y[0], y[1], y[2], y[3]);
-              bad = true;
+              const int c = cb + e * each, node = o0 + ((c >> 3) & (kTile - 1));
+              if (node < 0) continue;
+              uint32_t y[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+              bool hit = node >= n;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (node >= n) y[k] = 0u;
+                if ((y[k] & 0x7f80u) == 0x7f80u) y[k] &= 0xffff0000u, hit = bad = true;
+                if ((y[k] & 0x7f800000u) == 0x7f800000u) y[k] &= 0xffffu, hit = bad = true;
+              }
+              if (hit) reinterpret_cast<uint4 *>(v_ptr(vs))[c] = make_uint4(y[0], y[1], y[2], y[3]);
             }
           }
           if (bad) atomicMax(&v_bad[piece & 3], static_cast<uint32_t>(piece + 1));
@@ -834,19 +859,18 @@ __global__ void __launch_bounds__(kTrMergeThreads, 3) tree_merge_kernel(const __
   const int lane = threadIdx.x & 31;
   const int unit = static_cast<int>(blockIdx.x) % (p.Hkv * p.R), cut = static_cast<int>(blockIdx.x) / (p.Hkv * p.R) + 1;
   const int r = unit % p.R, kv = unit / p.R;
-  long long lane_first = 0;
-  const long long total = tree_total(p, lane, &lane_first);
-  const int ranges = tree_ranges(p, total);
+  const TreeCut all = tree_cut(p, lane);
   int b = 0, n = 0, w0 = 0, w1 = -1;
-  if (cut < ranges) {
-    const long long at = worker_begin(total, ranges, cut);
+  if (cut < all.ranges) {
+    const long long at = worker_begin(all.total, all.ranges, cut);
     long long first = 0;
-    tree_find(p, lane, lane_first, at, &b, &first);
+    tree_find(p, all, at, &b, &first);
     n = tree_nodes(p, b, p.ctx_lens[b]);
+    const int nt = tree_tiles(p, b);
     // not between two sequences, a node in this row tile, and no earlier boundary in the sequence
-    if (first != at && r * p.Tt < n && worker_of(total, ranges, first) == cut - 1) {
+    if (first != at && at < first + nt && r * p.Tt < n && worker_of(all.total, all.ranges, first) == cut - 1) {
       w0 = cut - 1;
-      w1 = worker_of(total, ranges, first + tree_tiles(p, b) - 1);
+      w1 = worker_of(all.total, all.ranges, first + nt - 1);
     }
   }
   griddep_wait();  // the attention kernel's partials, and its own reads of what follows this call
