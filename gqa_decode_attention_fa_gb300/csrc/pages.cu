@@ -310,17 +310,29 @@ struct KeepParams {
   const int32_t *table, *start, *keep, *counts;
   uint32_t *err;
   int max_keep, max_seq, max_blocks, num_blocks, paged;
-  int cols;  // 16-byte columns of a row that a CTA moves
+  int pools, per;  // pools, and those of a CTA
+  int cols;        // 16-byte columns of a row that a CTA moves
 };
 
-// One CTA per (pool, sequence, slice of the row's columns).  Row keep[i] goes to row i <= keep[i]:
-// rows taken in ascending order, a group at a time, a group read whole before it is written, never
-// overwrite one that is still to be read (the reads left have keep[j] >= j > every row written).
-// Entries with keep[i] = i, a prefix of the list, move nothing.
+// One CTA per (some pools, sequence, slice of the row's columns).  Row keep[i] goes to row
+// i <= keep[i]: rows taken in ascending order, a group at a time, a group read whole before it is
+// written, never overwrite one that is still to be read (the reads left have keep[j] >= j > every
+// row written), so the next group is read before the group at hand is written.  Entries with
+// keep[i] = i, a prefix of the list, move nothing.
+//   Bound by HBM when CTAs enough have work: the host cuts the rows into slices (of 256 bytes at
+// least) where there are few pools and sequences (16 pools x 4 sequences, half of 8000 rows kept:
+// 493 us with whole rows, 175 us in slices), and gives a CTA several pools where there are many,
+// so that a list is checked less often (80 pools x 32 sequences, 5 rows each: 15 us with a CTA a
+// pool, 10.7 us with five pools a CTA).
 constexpr int kKeepThreads = 256;
-constexpr int kKeepDepth = 8;
+constexpr int kKeepDepth = 4;   // rows a thread holds of a group
+constexpr int kKeepLanes = 64;  // rows side by side, at most
+constexpr int kKeepRing = 2048; // entries whose rows are known, in shared memory; filled by halves
+static_assert(3 * kKeepDepth * kKeepLanes <= kKeepRing / 2, "three groups are in use while a half is filled");
 __global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(const __grid_constant__ PoolSet pools,
                                                                  const KeepParams p) {
+  __shared__ int s_still;
+  __shared__ int2 s_rows[kKeepRing];  // (from, to) cache rows of entry i at i % kKeepRing
   griddep_wait();
   const int b = static_cast<int>(blockIdx.y), tid = threadIdx.x;
   const int n = p.counts[b], s0 = p.start[b];
@@ -332,10 +344,11 @@ __global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(const __grid_co
   }
   const int32_t *list = p.keep + static_cast<long long>(b) * p.max_keep;
   const int32_t *pages = p.table + static_cast<long long>(b) * p.max_blocks;
-  // cache row of a slot; the page ids have been checked
+  if (tid == 0) s_still = 0;
+  // cache row of a slot (below 2^31); the page ids have been checked
   auto row_of = [&](int slot) {
-    if (!p.paged) return static_cast<long long>(b) * p.max_seq + slot;
-    return static_cast<long long>(pages[slot / kTile]) * kTile + (slot & (kTile - 1));
+    if (!p.paged) return b * p.max_seq + slot;
+    return pages[slot / kTile] * kTile + (slot & (kTile - 1));
   };
   auto page_ok = [&](int slot) {
     const int pg = pages[slot / kTile];
@@ -353,41 +366,103 @@ __global__ void __launch_bounds__(kKeepThreads) keep_rows_kernel(const __grid_co
         if (p.paged && at != i) bad_page = bad_page || !page_ok(s0 + at) || !page_ok(s0 + i);
       }
     }
-  const int any = __syncthreads_or((bad ? 1 : 0) | (bad_page ? 2 : 0));
-  if (any) {
+  if (__syncthreads_or(bad || bad_page)) {
     const int any_bad = __syncthreads_or(bad);
     if (lead) flag_error(p.err, any_bad ? GQA_DEVERR_POSITION : GQA_DEVERR_PAGE);
     return;
   }
-  // the prefix that stays: the sum over the threads (ascending entries: keep[i] == i implies it for all before)
-  __shared__ int s_still;
-  if (tid == 0) s_still = 0;
-  __syncthreads();
+  // the prefix that stays (ascending entries: keep[i] == i implies it for all before)
   if (still) atomicAdd(&s_still, still);
   __syncthreads();
   const int i0 = s_still;
-  const int row16 = pools.row16[blockIdx.x];
-  const int c0 = static_cast<int>(blockIdx.z) * p.cols, c1 = min(row16, c0 + p.cols);
-  uint4 *base = reinterpret_cast<uint4 *>(pools.base[blockIdx.x]);
-  for (int cb = c0; cb < c1; cb += kKeepThreads) {
-    const int width = min(c1 - cb, kKeepThreads);
-    const int lanes = kKeepThreads / width;  // rows side by side
-    const int rl = tid / width, col = cb + tid - rl * width;
-    const bool works = rl < lanes;
-    for (int g = i0; g < n; g += lanes * kKeepDepth) {
-      uint4 x[kKeepDepth];
-#pragma unroll
-      for (int e = 0; e < kKeepDepth; ++e) {
-        const int i = g + e * lanes + rl;
-        if (works && i < n) x[e] = __ldcg(base + row_of(s0 + list[i]) * row16 + col);
+  if (i0 >= n) return;
+
+  int filled = i0;  // entries below it have been put into the ring
+  auto fill = [&](int count) {
+    const int upto = min(n, filled + count);
+    for (int i = filled + tid; i < upto; i += kKeepThreads)
+      s_rows[i % kKeepRing] = make_int2(row_of(s0 + list[i]), row_of(s0 + i));
+    filled = upto;
+  };
+  fill(kKeepRing);
+  __syncthreads();
+
+  // The groups to move, one after another: pool k, columns from cb, entries from g on.  rl and col are the
+  // thread's row in the group's first `lanes` and its column.
+  struct Group {
+    int k, cb, g, lanes, rl, col;
+  };
+  const int k1 = min(p.pools, (static_cast<int>(blockIdx.x) + 1) * p.per);
+  const int c0 = static_cast<int>(blockIdx.z) * p.cols;
+  auto place = [&](Group &x) {  // the thread's place once k and cb are set; past pools narrower than cb
+    while (x.k < k1) {
+      const int c1 = min(pools.row16[x.k], c0 + p.cols);
+      if (x.cb < c1) {
+        const int width = min(c1 - x.cb, kKeepThreads);
+        x.lanes = min(kKeepLanes, kKeepThreads / width);
+        x.rl = tid / width;
+        x.col = x.cb + tid - x.rl * width;
+        return;
       }
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kKeepDepth; ++e) {
-        const int i = g + e * lanes + rl;
-        if (works && i < n) __stcg(base + row_of(s0 + i) * row16 + col, x[e]);
-      }
+      ++x.k;
+      x.cb = c0;
     }
+  };
+  auto next = [&](Group x) {
+    x.g += x.lanes * kKeepDepth;
+    if (x.g >= n) {
+      x.g = i0;
+      x.cb += kKeepThreads;
+      place(x);
+    }
+    return x;
+  };
+  auto at = [&](const Group &x, int row) {
+    return reinterpret_cast<uint4 *>(pools.base[x.k]) + static_cast<long long>(row) * pools.row16[x.k] + x.col;
+  };
+  auto read = [&](const Group &x, uint4 (&v)[kKeepDepth]) {
+#pragma unroll
+    for (int e = 0; e < kKeepDepth; ++e) {
+      const int i = x.g + e * x.lanes + x.rl;
+      if (x.rl < x.lanes && i < n) v[e] = __ldcg(at(x, s_rows[i % kKeepRing].x));
+    }
+  };
+  auto write = [&](const Group &x, const uint4 (&v)[kKeepDepth]) {
+#pragma unroll
+    for (int e = 0; e < kKeepDepth; ++e) {
+      const int i = x.g + e * x.lanes + x.rl;
+      if (x.rl < x.lanes && i < n) __stcg(at(x, s_rows[i % kKeepRing].y), v[e]);
+    }
+  };
+  // One step: group x is in u; the group after it is read into v, x is written, and the rows the group
+  // after that will need are looked up.  Where a new pool or column block starts over and its first
+  // entries have left the ring, the ring is filled anew first.
+  const bool once = n - i0 <= kKeepRing;
+  auto step = [&](const Group &x, const uint4 (&u)[kKeepDepth], uint4 (&v)[kKeepDepth]) {
+    const Group y = next(x);
+    __syncthreads();  // every thread has read group x, and the rows of group y are known
+    const bool over = y.k < k1 && y.g <= x.g && !once;
+    if (y.k < k1 && !over) read(y, v);
+    write(x, u);
+    if (over) {
+      __syncthreads();
+      filled = i0;
+      fill(kKeepRing);
+      __syncthreads();
+      read(y, v);
+    } else if (y.k < k1 && filled < n && y.g + 2 * y.lanes * kKeepDepth > filled) {
+      fill(kKeepRing / 2);
+    }
+    return y;
+  };
+  Group x{static_cast<int>(blockIdx.x) * p.per, c0, i0, 1, 0, 0};
+  place(x);
+  uint4 u[kKeepDepth], v[kKeepDepth];
+  if (x.k < k1) read(x, u);
+  while (x.k < k1) {
+    x = step(x, u, v);
+    if (x.k >= k1) break;
+    x = step(x, v, u);
   }
 }
 
@@ -523,9 +598,21 @@ extern "C" gqa_status_t gqa_cache_keep_rows(const gqa_keep_desc_t *desc, const g
   p.max_blocks = (d.max_seq_len + kTile - 1) / kTile;
   p.num_blocks = paged ? d.num_blocks : 0;
   p.paged = paged ? 1 : 0;
-  int widest = 1;
+  int widest = 1, sms = 0;
   for (int i = 0; i < num_pools; ++i) widest = set.row16[i] > widest ? set.row16[i] : widest;
-  p.cols = widest;
-  return launched(launch_pdl(keep_rows_kernel, dim3(static_cast<unsigned>(num_pools), static_cast<unsigned>(d.batch), 1),
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d.device) != cudaSuccess) return launched(cudaErrorUnknown);
+  // three CTAs an SM: pools together where there are more (pool, sequence) pairs, slices of the rows
+  // (16 columns, 256 bytes, at least) where there are fewer
+  const long long pairs = static_cast<long long>(num_pools) * d.batch, want = 3LL * sms;
+  long long per = pairs / want, slices = (want + pairs - 1) / pairs;
+  per = per < 1 ? 1 : per > num_pools ? num_pools : per;
+  const long long most = (widest + 15) / 16;
+  slices = slices > most ? most : slices;
+  p.pools = num_pools;
+  p.per = static_cast<int>(per);
+  p.cols = static_cast<int>((widest + slices - 1) / slices);
+  slices = (widest + p.cols - 1) / p.cols;
+  return launched(launch_pdl(keep_rows_kernel, dim3(static_cast<unsigned>((num_pools + per - 1) / per), static_cast<unsigned>(d.batch),
+                                                    static_cast<unsigned>(slices)),
                              dim3(kKeepThreads), 0, static_cast<cudaStream_t>(stream), set, p));
 }
