@@ -14,10 +14,11 @@
 //     product instead of binary64's (1/64 of the binary32 rate here); sine and cosine of the rest
 //     (at most 1/8 turn) are Taylor sums, the large terms in double-word binary32;
 //   * the key rows, which stay in the cache and round as the exact value does (rowmath.cuh).
-//     A row is first computed in binary32 with a bound on its error; where both ends of every
-//     interval round to the same bf16 (about 11 rows of 12) that is the exact value's rounding
-//     too, else the warp repeats the row in double-word (the method of Ziv, "Fast evaluation of
-//     elementary mathematical functions with correctly rounded last bit", ACM TOMS 17(3), 1991).
+//     An element is first computed in binary32 (only the row's r in double-word) with a bound on
+//     its error; where both ends of the interval round to the same bf16 that is the exact value's
+//     rounding too, else the warp repeats the element in double-word (the method of Ziv, "Fast
+//     evaluation of elementary mathematical functions with correctly rounded last bit", ACM TOMS
+//     17(3), 1991): about one pair of rows in ten has such an element.
 // Query rows are computed in binary32 and rounded once.
 #include <math.h>
 #include <string.h>
@@ -46,8 +47,6 @@ struct RopeAppendParams {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRopeWarps = kRopeThreads / 32;
 
 // Cache row of slot `slot` of sequence b, or -1 when its page id is out of range.
 __device__ __forceinline__ long long append_row(const RopeAppendParams &p, int b, int slot) {
@@ -101,7 +100,7 @@ __device__ __forceinline__ f2 abs_f2(f2 x) {
 }
 
 // A lane's place in a row: dims 8 l .. 8 l + 7, as two chunks of 4.
-template <bool kInterleaved>
+template <bool kInterleaved, bool kFull>
 struct RopeLane {
   // the half layout's partners of chunk h: words of lane from[h], its other chunk when `odd`
   bool odd;
@@ -111,11 +110,11 @@ struct RopeLane {
 
   __device__ __forceinline__ void init(int rotary, int l, int base) {
     const int m = rotary / 8;  // chunks of the first elements
-    odd = m & 1;
+    odd = !kFull && (m & 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = 2 * l + h;
-      turns[h] = c < 2 * m;
+      turns[h] = kFull || c < 2 * m;
       first[h] = c < m;
       from[h] = base + ((first[h] ? c + m : c >= m ? c - m : c) >> 1 & 15);
       pair[h] = kInterleaved ? 2 * c : 4 * (first[h] ? c : c - m);
@@ -129,10 +128,10 @@ struct RopeLane {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (kInterleaved) {
-          y[2 * h + e] = turns[h] ? __funnelshift_l(x[2 * h + e], x[2 * h + e], 16) : 0u;
+          y[2 * h + e] = kFull || turns[h] ? __funnelshift_l(x[2 * h + e], x[2 * h + e], 16) : 0u;
         } else {
-          const uint32_t o = __shfl_sync(0xffffffffu, odd ? x[2 * (1 - h) + e] : x[2 * h + e], from[h]);
-          y[2 * h + e] = turns[h] ? o : 0u;
+          const uint32_t o = __shfl_sync(0xffffffffu, !kFull && odd ? x[2 * (1 - h) + e] : x[2 * h + e], from[h]);
+          y[2 * h + e] = kFull || turns[h] ? o : 0u;
         }
       }
   }
@@ -142,62 +141,60 @@ struct RopeLane {
   __device__ __forceinline__ int pair_of(int h, int e) const { return pair[h] + (kInterleaved ? e >> 1 : e); }
 };
 
-// Key rows in double-word arithmetic: the rounding of the exact value.
-template <bool kInterleaved>
-__device__ __noinline__ uint4 key_row_exact(const float4 *cs, const RopeLane<kInterleaved> l, uint4 xv, uint4 wv,
-                                            bool norm, float eps) {
-  const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, w[4] = {wv.x, wv.y, wv.z, wv.w};
-  uint32_t xp[4], wp[4];
-  l.partners(x, xp);
-  l.partners(w, wp);
-  dw rn = {1.f, 0.f};
-  if (norm) {
-    dw ss = {0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = bf16_lo_to_float(x[e]), b = bf16_hi_to_float(x[e]);
-      ss = dw_add(ss, two_sum(__fmul_rn(a, a), __fmul_rn(b, b)));  // the squares are exact
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-      ss = dw_add(ss, dw{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
-    const dw m = dw_add(dw{__fmul_rn(ss.hi, 1.0f / 128.0f), __fmul_rn(ss.lo, 1.0f / 128.0f)}, dw{eps, 0.f});
-    const float r0 = __frcp_rn(__fsqrt_rn(m.hi));
-    const dw e1 = dw_add(dw{1.f, 0.f}, dw_neg(dw_mul(m, two_prod(r0, r0))));  // 1 - m r0^2
-    rn = fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e1.hi));
-  }
-  uint32_t z[4];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int h = e >> 2;
-    // exact products: 8-bit significands
-    const float y = e & 1 ? bf16_hi_to_float(x[e >> 1]) * bf16_hi_to_float(w[e >> 1])
-                          : bf16_lo_to_float(x[e >> 1]) * bf16_lo_to_float(w[e >> 1]);
-    dw turned = {y, 0.f};
-    if (l.turns[h]) {
-      const float yp = e & 1 ? bf16_hi_to_float(xp[e >> 1]) * bf16_hi_to_float(wp[e >> 1])
-                             : bf16_lo_to_float(xp[e >> 1]) * bf16_lo_to_float(wp[e >> 1]);
-      const float4 c = cs[l.pair_of(h, e & 3)];
-      turned = dw_add(dw_mul_f(dw{c.x, c.z}, y), dw_mul_f(dw{c.y, c.w}, l.negative(h, e & 3) ? -yp : yp));
-    }
-    const uint32_t out = round_dw_bf16(norm ? dw_mul(turned, rn) : turned);
-    z[e >> 1] = e & 1 ? z[e >> 1] | (out << 16) : out;
-  }
-  return make_uint4(z[0], z[1], z[2], z[3]);
+// One key element in double-word arithmetic, the rounding of its exact value: y its own product x w, yp
+// its partner's with the sign of the sine term, c its pair's (cos_hi, sin_hi, cos_lo, sin_lo).
+__device__ __noinline__ uint32_t key_element_exact(float y, float yp, float4 c, bool turns, dw rn, bool norm) {
+  dw z = {y, 0.f};
+  if (turns) z = dw_add(dw_mul_f(dw{c.x, c.z}, y), dw_mul_f(dw{c.y, c.w}, yp));
+  return round_dw_bf16(norm ? dw_mul(z, rn) : z);
 }
 
+// r = 1 / sqrt(ss / 128 + eps) of the half warp's row as a double-word, from a lane's 8 values: the squares
+// are exact in binary32 and are summed with the errors of every addition (Knuth's TwoSum, in
+// pairs), a binary32 seed takes one Newton step with its residual.
+__device__ __forceinline__ dw row_inv_rms(const f2 (&v)[4], float eps) {
+  f2 s = mul_f2(v[0], v[0]), err = make_f2(0.f, 0.f);
+  const f2 minus = make_f2(-1.f, -1.f);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) {
+    const f2 q = mul_f2(v[e], v[e]), t = add_f2(s, q);
+    const f2 bb = fma_f2(s, minus, t);                                        // t - s
+    const f2 lost = add_f2(fma_f2(fma_f2(bb, minus, t), minus, s), fma_f2(bb, minus, q));  // (s - (t - bb)) + (q - bb)
+    err = add_f2(err, lost);
+    s = t;
+  }
+  float a, b, ea, eb;
+  split_f2(s, a, b);
+  split_f2(err, ea, eb);
+  dw ss = two_sum(a, b);
+  ss.lo = __fadd_rn(ss.lo, __fadd_rn(ea, eb));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, ss.hi, o), lo = __shfl_xor_sync(0xffffffffu, ss.lo, o);
+    const dw t = two_sum(ss.hi, hi);
+    ss = dw{t.hi, __fadd_rn(t.lo, __fadd_rn(ss.lo, lo))};
+  }
+  const dw m = dw_add(fast_two_sum(__fmul_rn(ss.hi, 1.0f / 128.0f), __fmul_rn(ss.lo, 1.0f / 128.0f)), dw{eps, 0.f});
+  const float r0 = rsqrtf(m.hi);
+  const dw p = two_prod(r0, r0);
+  // 1 - m r0^2: m.hi p.hi is near 1, so the fma gives its difference exactly rounded
+  const float e = __fmaf_rn(-m.lo, p.hi, __fmaf_rn(-m.hi, p.lo, __fmaf_rn(-m.hi, p.hi, 1.f)));
+  return fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e));
+}
+
+// Tokens up to which a CTA has eight warps (the latency of one token), and above which two.
+constexpr int kRopeFew = 512;
 constexpr int kRopeAhead = 4;  // row pairs of a warp whose loads are in flight together
 // Error of a key element computed in binary32, relative to r (|x_i w_i cos| + |x_j w_j sin|), in
-// units of 2^-24: the sum of 128 squares 11 roundings (7 in the lane, 4 between lanes), halved by
-// the root; eps 1/2; the reciprocal root 4 (2 ulp); cos or sin, its product with w, the product
-// with x, the fma, the product with r 1 each -- 15 in all.  20 leaves room for the rounding of
-// the interval's own ends.
-constexpr float kKeyWindow = 20.f * 0x1p-24f;
+// units of 2^-24: the rounding of r to binary32, cos or sin, its product with w, the product with x,
+// the fma and the product with r, 1 each.  8 leaves room for the rounding of the interval's own ends.
+constexpr float kKeyWindow = 8.f * 0x1p-24f;
 
 }  // namespace
 
-template <bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+template <bool kInterleaved, bool kFull, int kRopeWarps>
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 16 : 2) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+  constexpr int kRopeThreads = 32 * kRopeWarps;
   __shared__ float4 cs[kHeadDim / 2];  // m (cos_hi, sin_hi, cos_lo, sin_lo) of pair i
   griddep_wait();  // everything below may come from the preceding kernel
   const int b = static_cast<int>(blockIdx.x) / p.T, t = static_cast<int>(blockIdx.x) - b * p.T;
@@ -238,7 +235,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   }
   const long long crow = append_row(p, b, s0 + t);
   if (crow < 0 && tid == 0) flag_error(p.err, GQA_DEVERR_PAGE);
-  RopeLane<kInterleaved> l;
+  RopeLane<kInterleaved, kFull> l;
   l.init(p.rotary, hl, 16 * half);
   __syncthreads();
 
@@ -256,7 +253,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int h = e >> 1, d = 2 * (e & 1) + k;
-        const float4 v = l.turns[h] ? cs[l.pair_of(h, d)] : make_float4(1.f, 0.f, 0.f, 0.f);
+        const float4 v = kFull || l.turns[h] ? cs[l.pair_of(h, d)] : make_float4(1.f, 0.f, 0.f, 0.f);
         c[k] = v.x * (k ? bf16_hi_to_float(w[e]) : bf16_lo_to_float(w[e]));
         s[k] = v.y * (k ? bf16_hi_to_float(wp[e]) : bf16_lo_to_float(wp[e]));
         if (l.negative(h, d)) s[k] = -s[k];
@@ -327,10 +324,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
       f2 v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = unpack_f2(w[e]);
-      const float rn = p.k_norm_w ? inv_rms(v) : 1.f;
-      const f2 rn2 = make_f2(rn, rn), up = make_f2(kKeyWindow, kKeyWindow), down = make_f2(-kKeyWindow, -kKeyWindow);
-      uint32_t out[4];
-      bool sure = true;
+      const dw rn = p.k_norm_w ? row_inv_rms(v, p.eps) : dw{1.f, 0.f};
+      const f2 rn2 = make_f2(rn.hi, rn.hi), up = make_f2(kKeyWindow, kKeyWindow), down = make_f2(-kKeyWindow, -kKeyWindow);
+      uint32_t out[4], unsure = 0u;  // a bit per element
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const f2 vp = unpack_f2(wp[e]);
@@ -340,14 +336,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
         split_f2(fma_f2(size, down, z), a, c);
         out[e] = pack_bf16(a, c);
         split_f2(fma_f2(size, up, z), a, c);
-        sure = sure && out[e] == pack_bf16(a, c);
+        const uint32_t differ = out[e] ^ pack_bf16(a, c);
         // tiny values, whose binary32 steps are not relative, take the exact path, and so does
         // what is not finite
         split_f2(size, a, c);
-        sure = sure && (a == 0.f || (a > 0x1p-80f && a < 0x1p100f)) && (c == 0.f || (c > 0x1p-80f && c < 0x1p100f));
+        if ((differ & 0xffffu) || !(a == 0.f || (a > 0x1p-80f && a < 0x1p100f))) unsure |= 1u << (2 * e);
+        if ((differ >> 16) || !(c == 0.f || (c > 0x1p-80f && c < 0x1p100f))) unsure |= 2u << (2 * e);
       }
-      uint4 row = make_uint4(out[0], out[1], out[2], out[3]);
-      if (!__all_sync(0xffffffffu, sure)) row = key_row_exact<kInterleaved>(cs, l, x[k], kw, p.k_norm_w != nullptr, p.eps);
+      const uint32_t any = __reduce_or_sync(0xffffffffu, unsure);
+      if (any) {  // the warp repeats those elements exactly
+        const uint32_t ww[4] = {kw.x, kw.y, kw.z, kw.w};
+        uint32_t wwp[4];
+        l.partners(ww, wwp);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (!(any >> e & 1u)) continue;
+          const int h = e >> 2, x2 = e >> 1;
+          auto part = [&](uint32_t q) { return e & 1 ? bf16_hi_to_float(q) : bf16_lo_to_float(q); };
+          const float y = part(w[x2]) * part(ww[x2]), yp = part(wp[x2]) * part(wwp[x2]);  // exact: 8-bit significands
+          const float4 c = l.turns[h] ? cs[l.pair_of(h, e & 3)] : make_float4(1.f, 0.f, 0.f, 0.f);
+          const uint32_t z = key_element_exact(y, l.negative(h, e & 3) ? -yp : yp, c, l.turns[h], rn, p.k_norm_w != nullptr);
+          out[x2] = e & 1 ? (out[x2] & 0xffffu) | (z << 16) : (out[x2] & 0xffff0000u) | z;
+        }
+      }
+      const uint4 row = make_uint4(out[0], out[1], out[2], out[3]);
       if (2 * i + half < p.Hkv) kdst[(2 * i + half) * (kHeadDim / 8)] = row;
     }
   }
@@ -507,8 +519,17 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   p.rotary = rope->rotary_dim;
   p.eps = eps;
   const dim3 grid(static_cast<unsigned>(d.batch) * static_cast<unsigned>(d.num_tokens));
-  auto *kernel = rope->layout == GQA_ROPE_INTERLEAVED ? rope_append_kernel<true> : rope_append_kernel<false>;
-  if (launch_pdl(kernel, grid, dim3(kRopeThreads), 0, static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
+  const long long tokens = static_cast<long long>(d.batch) * d.num_tokens;
+  const bool full = p.rotary == kHeadDim, many = tokens > kRopeFew;
+  const int warps = many ? 2 : 8;
+  void (*kernel)(const RopeAppendParams);
+  if (rope->layout == GQA_ROPE_INTERLEAVED)
+    kernel = full ? (many ? rope_append_kernel<true, true, 2> : rope_append_kernel<true, true, 8>)
+                  : (many ? rope_append_kernel<true, false, 2> : rope_append_kernel<true, false, 8>);
+  else
+    kernel = full ? (many ? rope_append_kernel<false, true, 2> : rope_append_kernel<false, true, 8>)
+                  : (many ? rope_append_kernel<false, false, 2> : rope_append_kernel<false, false, 8>);
+  if (launch_pdl(kernel, grid, dim3(32 * warps), 0, static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
