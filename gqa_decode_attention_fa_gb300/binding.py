@@ -9,6 +9,7 @@ cannot be loaded -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -119,6 +120,8 @@ def header_functions() -> list:
 def load(build: bool = True):
     """Load the library (building it first when stale); raises on failure."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -303,26 +306,53 @@ def prefill_attn_workload(w, out, *, device: int = 0, device_errors=None, stream
 
 # ------------------------------------------------------- rotary append, draft trees, cache pages
 
+# These calls come once a layer and step, so their wrappers keep to a few microseconds: one check
+# a tensor, and the descriptors of the geometries in use are kept (the library reads them during a
+# call only).
+
+class _Torch:
+    """What the wrappers need of torch, looked up at the first call (importing the binding
+    does not import torch)."""
+
+    ready = False
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.i32, cls.bf16, cls.u8 = torch.int32, torch.bfloat16, torch.uint8
+        cls.word32, cls.word64 = (torch.int32, torch.uint32), (torch.int64, torch.uint64)
+        cls.empty = torch.empty
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object
+        cls.stream = staticmethod(raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+        cls.ready = True
+
+
+def _torch():
+    if not _Torch.ready:
+        _Torch.load()
+    return _Torch
+
+
 def _on(device: int, stream) -> int:
     """The stream a call on `device` is queued on: the caller's, else torch's current one there."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return _torch().stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _dev(t, name: str, dtype, shape, device: int, optional: bool = False) -> Optional[int]:
     """Device pointer of a dense tensor of the dtype and shape the call needs (`dtype` a torch
-    dtype or a tuple of them; a None in `shape` takes any size)."""
+    dtype or a tuple of them; a None in `shape`, or for it, takes any size)."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is missing")
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {t.device}")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape and (
+    d = t.dtype
+    if d is not dtype and not (isinstance(dtype, tuple) and d in dtype):
+        raise ValueError(f"{name}: expected {dtype}, got {d}")
+    if shape is not None and t.shape != shape and (
             t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape))):
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -330,9 +360,18 @@ def _dev(t, name: str, dtype, shape, device: int, optional: bool = False) -> Opt
     return t.data_ptr()
 
 
-def _cache_shape(name: str, t, rows: int, num_kv_heads: int, device: int) -> int:
-    import torch
-    p = _dev(t, name, torch.bfloat16, None, device)
+def _err(t, device: int) -> Optional[int]:
+    return None if t is None else _dev(t, "device_errors", _torch().word32, (1,), device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _desc(kind, *fields):
+    """A reference to the descriptor with these fields."""
+    return ctypes.byref(kind(*fields))
+
+
+def _cache(name: str, t, rows: int, num_kv_heads: int, device: int) -> int:
+    p = _dev(t, name, _torch().bf16, None, device)
     if t.numel() != rows * num_kv_heads * 128:
         raise ValueError(f"{name}: expected {rows} rows of {num_kv_heads} x 128, got shape {tuple(t.shape)}")
     return p
@@ -341,11 +380,12 @@ def _cache_shape(name: str, t, rows: int, num_kv_heads: int, device: int) -> int
 def _tokens(t, name: str, batch: int, tokens: int, heads: int, device: int):
     """(pointer, stride in elements between tokens) of a [B, T, H, 128] tensor whose heads are
     dense and whose tokens are evenly spaced -- dense, or a slice of a wider projection."""
-    import torch
-    if t is None or not t.is_cuda or t.device.index != device or t.dtype != torch.bfloat16:
+    if t is None or t.get_device() != device or t.dtype is not _torch().bf16:
         raise ValueError(f"{name}: expected a bfloat16 tensor on cuda:{device}")
-    if tuple(t.shape) != (batch, tokens, heads, 128):
+    if t.shape != (batch, tokens, heads, 128):
         raise ValueError(f"{name}: expected shape {(batch, tokens, heads, 128)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * 128
     sb, st, sh, sd = t.stride()
     if tokens == 1:
         st = sb
@@ -361,59 +401,63 @@ def rope_append(batch: int, num_q_heads: int, num_kv_heads: int, num_tokens: int
                 device_errors=None, stream=None):
     """QK-norm, rotation and append of [B, T] tokens (gqa_rope_append, include/gqa_rope.h).  q, k
     and v may be slices of one projection (token strides are taken from the tensors)."""
-    import torch
-    i32 = torch.int32
+    tt = _torch()
+    i32 = tt.i32
     qp, qs = _tokens(q, "q", batch, num_tokens, num_q_heads, device)
     kp, ks = _tokens(k, "k", batch, num_tokens, num_kv_heads, device)
     vp, vs = _tokens(v, "v", batch, num_tokens, num_kv_heads, device)
     rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
-    desc = RopeDesc(batch, num_q_heads, num_kv_heads, head_dim, num_tokens, block_size, max_seq_len, num_cache_blocks,
-                    device, qs, ks, vs)
+    desc = _desc(RopeDesc, batch, num_q_heads, num_kv_heads, head_dim, num_tokens, block_size, max_seq_len,
+                 num_cache_blocks, device, qs, ks, vs)
     _check(load().gqa_rope_append(
-        ctypes.byref(desc), qp, kp, vp, _cache_shape("k_cache", k_cache, rows, num_kv_heads, device),
-        _cache_shape("v_cache", v_cache, rows, num_kv_heads, device),
+        desc, qp, kp, vp, _cache("k_cache", k_cache, rows, num_kv_heads, device),
+        _cache("v_cache", v_cache, rows, num_kv_heads, device),
         _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
         _dev(slot_start, "slot_start", i32, (batch,), device),
         _dev(positions, "positions", i32, (batch, num_tokens), device, True),
         _dev(counts, "counts", i32, (batch,), device, True),
-        _dev(q_norm_w, "q_norm_w", torch.bfloat16, (128,), device, True),
-        _dev(k_norm_w, "k_norm_w", torch.bfloat16, (128,), device, True), ctypes.byref(rope), float(eps),
-        _dev(q_out, "q_out", torch.bfloat16, (batch, num_tokens, num_q_heads, 128), device),
-        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        _dev(q_norm_w, "q_norm_w", tt.bf16, (128,), device, True),
+        _dev(k_norm_w, "k_norm_w", tt.bf16, (128,), device, True), ctypes.byref(rope), float(eps),
+        _dev(q_out, "q_out", tt.bf16, (batch, num_tokens, num_q_heads, 128), device),
+        _err(device_errors, device), _on(device, stream)),
         "gqa_rope_append")
 
 
 def tree_prepare(parents, ctx_lens, counts, mask, positions, *, device: int = 0, device_errors=None, stream=None):
     """The masks (int64 words) and positions of draft trees from their parents [B, T]
     (gqa_tree_prepare, include/gqa_tree.h)."""
-    import torch
-    i32 = torch.int32
+    tt = _torch()
+    i32 = tt.i32
     pp = _dev(parents, "parents", i32, (None, None), device)
     batch, tree_len = parents.shape
     _check(load().gqa_tree_prepare(
         batch, tree_len, pp, _dev(ctx_lens, "ctx_lens", i32, (batch,), device),
         _dev(counts, "counts", i32, (batch,), device, True),
-        _dev(mask, "mask", (torch.int64, torch.uint64), (batch, tree_len, (tree_len + 63) // 64), device),
+        _dev(mask, "mask", tt.word64, (batch, tree_len, (tree_len + 63) // 64), device),
         _dev(positions, "positions", i32, (batch, tree_len), device), device,
-        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        _err(device_errors, device), _on(device, stream)),
         "gqa_tree_prepare")
 
 
 def tree_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, *,
                          block_size: int = 0, num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0) -> int:
-    desc = TreeDesc(batch, num_q_heads, num_kv_heads, head_dim, tree_len, block_size, max_seq_len, num_cache_blocks,
-                    device)
+    return _workspace_of(batch, num_q_heads, num_kv_heads, head_dim, tree_len, block_size, max_seq_len, num_cache_blocks,
+                         device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_of(*fields) -> int:
     n = ctypes.c_size_t(0)
-    _check(load().gqa_tree_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)), "gqa_tree_workspace_bytes")
+    _check(load().gqa_tree_workspace_bytes(_desc(TreeDesc, *fields), ctypes.byref(n)), "gqa_tree_workspace_bytes")
     return int(n.value)
 
 
 def tree_workspace(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, *,
                    device: int = 0):
     """A workspace for gqa_tree_attn calls of this geometry (any cache layout) that do not overlap."""
-    import torch
-    return torch.empty(tree_workspace_bytes(batch, num_q_heads, num_kv_heads, tree_len, max_seq_len, device=device),
-                       dtype=torch.uint8, device=f"cuda:{device}")
+    tt = _torch()
+    return tt.empty(tree_workspace_bytes(batch, num_q_heads, num_kv_heads, tree_len, max_seq_len, device=device),
+                    dtype=tt.u8, device=f"cuda:{device}")
 
 
 def tree_attn(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, q, k_cache, v_cache,
@@ -422,31 +466,28 @@ def tree_attn(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, ma
     """Attention of draft-tree nodes over the cache (gqa_tree_attn, include/gqa_tree.h).
     ``workspace``: a uint8 tensor of tree_workspace_bytes; None takes one from torch's allocator
     for this call (which knows the current stream only: give one with an explicit ``stream``)."""
-    import torch
-    i32 = torch.int32
+    tt = _torch()
+    i32 = tt.i32
     rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
-    desc = TreeDesc(batch, num_q_heads, num_kv_heads, head_dim, tree_len, block_size, max_seq_len, num_cache_blocks,
-                    device)
-    lib = load()
-    need = ctypes.c_size_t(0)
-    _check(lib.gqa_tree_workspace_bytes(ctypes.byref(desc), ctypes.byref(need)), "gqa_tree_workspace_bytes")
+    fields = (batch, num_q_heads, num_kv_heads, head_dim, tree_len, block_size, max_seq_len, num_cache_blocks, device)
+    need = _workspace_of(*fields)
     if workspace is None:
         if stream is not None:
             raise ValueError("a call on an explicit stream needs a workspace")
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=f"cuda:{device}")
-    ws = _dev(workspace, "workspace", torch.uint8, (None,), device)
-    if workspace.numel() < need.value:
-        raise ValueError(f"workspace: {need.value} bytes needed, got {workspace.numel()}")
+        workspace = tt.empty(need, dtype=tt.u8, device=f"cuda:{device}")
+    ws = _dev(workspace, "workspace", tt.u8, None, device)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace: {need} bytes needed, got {workspace.numel()}")
     shape = (batch, tree_len, num_q_heads, 128)
-    _check(lib.gqa_tree_attn(
-        ctypes.byref(desc), _dev(q, "q", torch.bfloat16, shape, device),
-        _cache_shape("k_cache", k_cache, rows, num_kv_heads, device),
-        _cache_shape("v_cache", v_cache, rows, num_kv_heads, device),
+    _check(load().gqa_tree_attn(
+        _desc(TreeDesc, *fields), _dev(q, "q", tt.bf16, shape, device),
+        _cache("k_cache", k_cache, rows, num_kv_heads, device),
+        _cache("v_cache", v_cache, rows, num_kv_heads, device),
         _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
         _dev(ctx_lens, "ctx_lens", i32, (batch,), device), _dev(counts, "counts", i32, (batch,), device, True),
-        _dev(mask, "mask", (torch.int64, torch.uint64), (batch, tree_len, (tree_len + 63) // 64), device),
-        _dev(out, "out", torch.bfloat16, shape, device), ws,
-        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        _dev(mask, "mask", tt.word64, (batch, tree_len, (tree_len + 63) // 64), device),
+        _dev(out, "out", tt.bf16, shape, device), ws,
+        _err(device_errors, device), _on(device, stream)),
         "gqa_tree_attn")
 
 
@@ -476,21 +517,21 @@ class CachePools:
 
 
 def _page_state(ref_counts, page_table, seq_lens, device: int):
-    import torch
-    i32 = torch.int32
+    tt = _torch()
+    i32 = tt.i32
     ptrs = (_dev(ref_counts, "ref_counts", i32, (None,), device), _dev(page_table, "page_table", i32, (None, None), device),
             _dev(seq_lens, "seq_lens", i32, (page_table.shape[0],), device))
-    return PagesDesc(page_table.shape[0], page_table.shape[1], ref_counts.shape[0], device), ptrs
+    return _desc(PagesDesc, page_table.shape[0], page_table.shape[1], ref_counts.shape[0], device), ptrs
 
 
 def pages_fork(ref_counts, page_table, seq_lens, src, dst, *, device: int = 0, device_errors=None, stream=None):
     """Sequences dst[i] share the pages of sequences src[i] (gqa_pages_fork, include/gqa_pages.h)."""
-    import torch
+    i32 = _torch().i32
     desc, ptrs = _page_state(ref_counts, page_table, seq_lens, device)
     n = src.shape[0]
     _check(load().gqa_pages_fork(
-        ctypes.byref(desc), *ptrs, _dev(src, "src", torch.int32, (n,), device), _dev(dst, "dst", torch.int32, (n,), device),
-        n, _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        desc, *ptrs, _dev(src, "src", i32, (n,), device), _dev(dst, "dst", i32, (n,), device),
+        n, _err(device_errors, device), _on(device, stream)),
         "gqa_pages_fork")
 
 
@@ -498,43 +539,41 @@ def pages_resize(ref_counts, page_table, seq_lens, new_lens, cow_src, cow_dst, *
                  stream=None):
     """Grow, shrink or free sequences (gqa_pages_resize); cow_src / cow_dst [B] receive the pages to
     copy before the sequences are written to (pages_copy), or -1."""
-    import torch
+    i32 = _torch().i32
     desc, ptrs = _page_state(ref_counts, page_table, seq_lens, device)
-    shape = (desc.batch,)
+    shape = (page_table.shape[0],)
     _check(load().gqa_pages_resize(
-        ctypes.byref(desc), *ptrs, _dev(new_lens, "new_lens", torch.int32, shape, device),
-        _dev(cow_src, "cow_src", torch.int32, shape, device), _dev(cow_dst, "cow_dst", torch.int32, shape, device),
-        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        desc, *ptrs, _dev(new_lens, "new_lens", i32, shape, device),
+        _dev(cow_src, "cow_src", i32, shape, device), _dev(cow_dst, "cow_dst", i32, shape, device),
+        _err(device_errors, device), _on(device, stream)),
         "gqa_pages_resize")
 
 
 def pages_copy(pools: CachePools, src, dst, *, device_errors=None, stream=None):
     """Page dst[i] := page src[i] in every pool; src[i] < 0 is skipped (gqa_pages_copy)."""
-    import torch
-    n, device = src.shape[0], pools.device
+    i32, n, device = _torch().i32, src.shape[0], pools.device
     _check(load().gqa_pages_copy(
-        pools.array, len(pools), pools.num_blocks, _dev(src, "src", torch.int32, (n,), device),
-        _dev(dst, "dst", torch.int32, (n,), device), n, device,
-        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        pools.array, len(pools), pools.num_blocks, _dev(src, "src", i32, (n,), device),
+        _dev(dst, "dst", i32, (n,), device), n, device,
+        _err(device_errors, device), _on(device, stream)),
         "gqa_pages_copy")
 
 
 def cache_keep_rows(pools: CachePools, page_table, start, keep, counts, *, max_seq_len: int, device_errors=None,
                     stream=None):
     """Rows start[b] + keep[b][i] move to start[b] + i in every pool (gqa_cache_keep_rows)."""
-    import torch
-    i32, device = torch.int32, pools.device
+    i32, device = _torch().i32, pools.device
     kp = _dev(keep, "keep", i32, (None, None), device)
     batch, width = keep.shape
     paged = page_table is not None
     if paged != (pools.num_blocks > 0) or (not paged and pools.rows != batch * max_seq_len):
         raise ValueError("a page table goes with paged pools; contiguous ones have batch * max_seq_len rows")
-    desc = KeepDesc(batch, width, max_seq_len, 64 if paged else 0, pools.num_blocks, device)
+    desc = _desc(KeepDesc, batch, width, max_seq_len, 64 if paged else 0, pools.num_blocks, device)
     _check(load().gqa_cache_keep_rows(
-        ctypes.byref(desc), pools.array, len(pools),
+        desc, pools.array, len(pools),
         _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
         _dev(start, "start", i32, (batch,), device), kp, _dev(counts, "counts", i32, (batch,), device),
-        _dev(device_errors, "device_errors", (torch.int32, torch.uint32), (1,), device, True), _on(device, stream)),
+        _err(device_errors, device), _on(device, stream)),
         "gqa_cache_keep_rows")
 
 

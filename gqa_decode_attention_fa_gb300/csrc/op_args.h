@@ -2,6 +2,8 @@
 // tree attention, cache pages).
 #pragma once
 
+#include <atomic>
+
 #include "launch.h"
 
 namespace gqa {
@@ -10,10 +12,14 @@ inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<ui
 
 // Is `device` one the call can run on?
 inline gqa_status_t check_device(int device) {
-  int ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess) {
-    cudaGetLastError();
-    return GQA_ERR_CUDA;
+  static std::atomic<int> known{0};  // devices the process sees; it does not change
+  int ndev = known.load(std::memory_order_relaxed);
+  if (ndev == 0) {
+    if (cudaGetDeviceCount(&ndev) != cudaSuccess) {
+      cudaGetLastError();
+      return GQA_ERR_CUDA;
+    }
+    known.store(ndev, std::memory_order_relaxed);
   }
   if (device < 0 || device >= ndev) return GQA_ERR_INVALID_ARG;
   return GQA_OK;

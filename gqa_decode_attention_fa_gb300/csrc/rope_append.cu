@@ -457,6 +457,43 @@ extern "C" gqa_status_t gqa_rope_freqs(const gqa_rope_t *rope, double *freqs, do
   return GQA_OK;
 }
 
+namespace {
+
+// What the kernel takes of a rotary embedding.  The thread's last one is kept (a model has one for
+// all layers and steps, and its 64 powers take longer than a launch): it follows from the fields
+// alone, but for CUSTOM, whose table is read at every call.
+struct RopeTurns {
+  gqa_rope_t of;
+  bool valid = false;
+  uint64_t turns[kHeadDim / 2];
+  float mag_hi, mag_lo;
+};
+
+bool same_rope(const gqa_rope_t &a, const gqa_rope_t &b) {
+  return a.layout == b.layout && a.rotary_dim == b.rotary_dim && a.scaling == b.scaling &&
+         a.original_max_len == b.original_max_len && a.theta == b.theta && a.factor == b.factor &&
+         a.low_freq_factor == b.low_freq_factor && a.high_freq_factor == b.high_freq_factor &&
+         a.beta_fast == b.beta_fast && a.beta_slow == b.beta_slow && a.magnitude == b.magnitude;
+}
+
+gqa_status_t rope_turns(const gqa_rope_t *rope, const RopeTurns **out) {
+  static thread_local RopeTurns last;
+  *out = &last;
+  if (rope && last.valid && rope->scaling != GQA_ROPE_CUSTOM && same_rope(*rope, last.of)) return GQA_OK;
+  last.valid = false;
+  double freqs[kHeadDim / 2], magnitude;
+  const gqa_status_t st = gqa_rope_freqs(rope, freqs, &magnitude);
+  if (st != GQA_OK) return st;
+  for (int i = 0; i < kHeadDim / 2; ++i) last.turns[i] = i < rope->rotary_dim / 2 ? turns_of(freqs[i]) : 0;
+  last.mag_hi = static_cast<float>(magnitude);
+  last.mag_lo = static_cast<float>(magnitude - last.mag_hi);
+  last.of = *rope;
+  last.valid = true;
+  return GQA_OK;
+}
+
+}  // namespace
+
 extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void *q, const void *k, const void *v,
                                         void *k_cache, void *v_cache, const int32_t *page_table,
                                         const int32_t *slot_start, const int32_t *positions, const int32_t *counts,
@@ -483,12 +520,12 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   if (q_out == q && d.q_stride != 0 && d.q_stride != qd) return GQA_ERR_INVALID_ARG;
   RopeAppendParams p;
   memset(&p, 0, sizeof p);
-  double freqs[kHeadDim / 2], magnitude;
-  st = gqa_rope_freqs(rope, freqs, &magnitude);
+  const RopeTurns *turns = nullptr;
+  st = rope_turns(rope, &turns);
   if (st != GQA_OK) return st;
-  for (int i = 0; i < rope->rotary_dim / 2; ++i) p.turns[i] = turns_of(freqs[i]);
-  p.mag_hi = static_cast<float>(magnitude);
-  p.mag_lo = static_cast<float>(magnitude - p.mag_hi);
+  memcpy(p.turns, turns->turns, sizeof p.turns);
+  p.mag_hi = turns->mag_hi;
+  p.mag_lo = turns->mag_lo;
   st = check_device(d.device);
   if (st != GQA_OK) return st;
   DeviceGuard guard(d.device);
