@@ -96,65 +96,65 @@ __device__ __forceinline__ int tree_nodes(const TreeParams &p, int b, int ctx) {
 // KV tiles of sequence b: those up to its last node's slot, none when it has no node.
 __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
   const int ctx = p.ctx_lens[b], n = tree_nodes(p, b, ctx);
-  return n > 0 ? (ctx + n + kTile - 1) / kTile : 0;
+  return n > 0 ? (ctx + n - 1) / kTile + 1 : 0;
 }
 
 // How the batch is cut.  Tiles are numbered sequence after sequence; behind each sequence with tiles
 // but the last, `gap` numbers are left out, the cost of a piece's end in tiles (the streams run
-// dry, O goes out: about 8 us), so that a range with many short sequences gets fewer tiles.  Range w
-// of W has the numbers [worker_begin(total, W, w), worker_begin(total, W, w + 1)).
+// dry, O goes out: about 8 us), so that a range with many short sequences gets fewer tiles.  The
+// numbers, fewer than 2^31, go to the ranges in order, `each` to a range, one more to the first `more`.
 constexpr int kTrPieceCost = 10;
 constexpr int kTrMinTiles = 4;  // of a range, so that small batches leave few partials
 struct TreeCut {
-  long long total;  // numbers in use
-  int ranges;
-  int gap;
-  // of the warp's lane: the first number of its sequences (it sums sequences [lane per, lane per + per))
-  long long lane_first;
+  int ranges, gap, each, more;
+  int lane_first;  // first number of the warp's lane's sequences [lane per, lane per + per)
+
+  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int range_of(int x) const {
+    const int wide = (each + 1) * more;
+    return x < wide ? x / (each + 1) : more + (x - wide) / each;
+  }
 };
 // Every lane of a warp calls these alike.
 __device__ __forceinline__ TreeCut tree_cut(const TreeParams &p, int lane) {
   const int per = (p.B + 31) / 32, b0 = lane * per, b1 = min(p.B, b0 + per);
-  long long tiles = 0;
-  int seqs = 0;
+  int tiles = 0, seqs = 0;
   for (int b = b0; b < b1; ++b) {
     const int nt = tree_tiles(p, b);
     tiles += nt;
     seqs += nt > 0;
   }
-  const long long own_tiles = tiles;
-  const int own_seqs = seqs;
+  const int own_tiles = tiles, own_seqs = seqs;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, tiles, o);
-    const int z = __shfl_up_sync(0xffffffffu, seqs, o);
+    const int y = __shfl_up_sync(0xffffffffu, tiles, o), z = __shfl_up_sync(0xffffffffu, seqs, o);
     if (lane >= o) tiles += y, seqs += z;
   }
-  const long long all = __shfl_sync(0xffffffffu, tiles, 31);
-  const int all_seqs = __shfl_sync(0xffffffffu, seqs, 31);
+  const int all = __shfl_sync(0xffffffffu, tiles, 31), all_seqs = __shfl_sync(0xffffffffu, seqs, 31);
   TreeCut c;
-  const long long most = (all + kTrMinTiles - 1) / kTrMinTiles;
-  c.ranges = static_cast<int>(most < p.W ? most : p.W);
-  const long long quarter = c.ranges > 0 ? all / (4 * c.ranges) : 0;  // of a range
-  c.gap = static_cast<int>(quarter < kTrPieceCost ? quarter : kTrPieceCost);
-  c.total = all + (all_seqs > 1 ? static_cast<long long>(c.gap) * (all_seqs - 1) : 0);
-  c.lane_first = tiles - own_tiles + static_cast<long long>(c.gap) * (seqs - own_seqs);
+  c.ranges = all < 1 ? 0 : max(1, min(p.W, all / kTrMinTiles));
+  const int quarter = c.ranges > 0 ? all / c.ranges / 4 : 0;  // of a range
+  c.gap = min(quarter, kTrPieceCost);
+  const int total = all + c.gap * max(0, all_seqs - 1);
+  c.each = c.ranges > 0 ? total / c.ranges : 0;
+  c.more = total - c.each * c.ranges;
+  c.lane_first = tiles - own_tiles + c.gap * (seqs - own_seqs);
   return c;
 }
 __device__ __forceinline__ int tree_span(const TreeParams &p, int b, int gap) {
   const int nt = tree_tiles(p, b);
   return nt > 0 ? nt + gap : 0;
 }
-// The sequence whose numbers (or the gap behind them) hold `at` < total, and its first number.
-__device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c, long long at, int *b, long long *seq0) {
+// The sequence whose numbers (or the gap behind them) hold `at`, below their end, and its first number.
+__device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c, int at, int *b, int *seq0) {
   // the last lane whose first number is <= at (lanes without tiles share their successor's)
   const uint32_t le = __ballot_sync(0xffffffffu, c.lane_first <= at);
   const int owner = 31 - __clz(le);
   const int per = (p.B + 31) / 32;
-  long long s = __shfl_sync(0xffffffffu, c.lane_first, owner);
+  int s = __shfl_sync(0xffffffffu, c.lane_first, owner);
   int x = owner * per;
   while (x + 1 < p.B) {
-    const long long nxt = s + tree_span(p, x, c.gap);
+    const int nxt = s + tree_span(p, x, c.gap);
     if (nxt > at) break;
     s = nxt;
     ++x;
@@ -166,14 +166,14 @@ __device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c,
 // Walks the sequences a range [pos, end) covers.  Every warp of the CTA runs its own copy, all
 // lanes alike.
 struct TreeWalk {
-  long long pos, end;  // numbers still to do
-  long long seq0;      // first number of sequence b
-  int b, nt, gap;      // sequence, its tiles
+  int pos, end;    // numbers still to do
+  int seq0;        // first number of sequence b
+  int b, nt, gap;  // sequence, its tiles
   // of the piece at hand
   int j0, j1;
-  bool whole;          // the piece is its whole sequence
+  bool whole;  // the piece is its whole sequence
 
-  __device__ __forceinline__ void start(const TreeParams &p, long long begin, long long stop, int b0, long long s0, int g) {
+  __device__ __forceinline__ void start(const TreeParams &p, int begin, int stop, int b0, int s0, int g) {
     pos = begin;
     end = stop;
     b = b0;
@@ -191,9 +191,8 @@ struct TreeWalk {
       nt = tree_tiles(p, b);
     }
     if (pos >= end) return false;
-    j0 = static_cast<int>(pos - seq0);
-    const long long left = end - pos;
-    j1 = left < nt - j0 ? j0 + static_cast<int>(left) : nt;
+    j0 = pos - seq0;
+    j1 = min(nt, j0 + end - pos);
     whole = j0 == 0 && j1 == nt;
     pos += j1 - j0;
     return true;
@@ -296,6 +295,20 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   const int r0 = static_cast<int>(blockIdx.x) % units * NQ, kv = static_cast<int>(blockIdx.x) / units % p.Hkv,
             w = static_cast<int>(blockIdx.x) / units / p.Hkv;
 
+  griddep_wait();  // everything below may come from the preceding kernel
+  if (p.W > 1) griddep_launch_dependents();  // tree_merge_kernel follows, and it waits
+  // every warp finds the CTA's range while tensor memory and the barriers are set up
+  TreeWalk walk;
+  {
+    const TreeCut cut = tree_cut(p, lane);
+    int begin = 0, stop = 0, seq0 = 0, b = 0;
+    if (w < cut.ranges) {
+      begin = cut.begin(w);
+      stop = cut.begin(w + 1);
+      tree_find(p, cut, begin, &b, &seq0);
+    }
+    walk.start(p, begin, stop, b, seq0, cut.gap);
+  }
   if (tid == 0) {
     for (int i = 0; i < Smem::kNumBars; ++i) {
       uint64_t *bar = k_full + i;
@@ -324,8 +337,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();  // everything below may come from the preceding kernel
-  if (p.W > 1) griddep_launch_dependents();  // tree_merge_kernel follows, and it waits
 
   // Sequences with invalid lengths: flagged, zeros in all their rows.
   for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x)) {
@@ -337,18 +348,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (long long c = tid; c < n; c += kTrThreads) dst[c] = make_uint4(0, 0, 0, 0);
   }
 
-  TreeWalk walk;
-  {
-    const TreeCut cut = tree_cut(p, lane);
-    long long begin = 0, stop = 0, seq0 = 0;
-    int b = 0;
-    if (w < cut.ranges) {
-      begin = worker_begin(cut.total, cut.ranges, w);
-      stop = worker_begin(cut.total, cut.ranges, w + 1);
-      tree_find(p, cut, begin, &b, &seq0);
-    }
-    walk.start(p, begin, stop, b, seq0, cut.gap);
-  }
   auto k_ptr = [&](int s) { return smem + Smem::kOffK + s * kTrTileBytes; };
   auto v_ptr = [&](int s) { return smem + Smem::kOffV + s * kTrTileBytes; };
   // A piece's streams: 0 if the CTA's row tiles have no node in the sequence, 1 if only the first
@@ -862,15 +861,15 @@ __global__ void __launch_bounds__(kTrMergeThreads, 3) tree_merge_kernel(const __
   const TreeCut all = tree_cut(p, lane);
   int b = 0, n = 0, w0 = 0, w1 = -1;
   if (cut < all.ranges) {
-    const long long at = worker_begin(all.total, all.ranges, cut);
-    long long first = 0;
+    const int at = all.begin(cut);
+    int first = 0;
     tree_find(p, all, at, &b, &first);
     n = tree_nodes(p, b, p.ctx_lens[b]);
     const int nt = tree_tiles(p, b);
     // not between two sequences, a node in this row tile, and no earlier boundary in the sequence
-    if (first != at && at < first + nt && r * p.Tt < n && worker_of(all.total, all.ranges, first) == cut - 1) {
+    if (first != at && at < first + nt && r * p.Tt < n && all.range_of(first) == cut - 1) {
       w0 = cut - 1;
-      w1 = worker_of(all.total, all.ranges, first + nt - 1);
+      w1 = all.range_of(first + nt - 1);
     }
   }
   griddep_wait();  // the attention kernel's partials, and its own reads of what follows this call
@@ -965,7 +964,11 @@ gqa_status_t tree_check(const gqa_tree_desc_t &d) {
                                                d.block_size, d.max_seq_len, d.num_cache_blocks);
   if (st != GQA_OK) return st;
   if (d.tree_len > GQA_MAX_TREE) return GQA_ERR_INVALID_ARG;
-  return static_cast<long long>(d.batch) * d.num_kv_heads * tree_row_tiles(d) > 0x7fffffffLL ? GQA_ERR_UNSUPPORTED : GQA_OK;
+  // (grid sizes, and the numbers of the batch's tiles with their gaps, are int32)
+  const long long tiles = static_cast<long long>(d.batch) * ((d.max_seq_len + kTile - 1LL) / kTile + kTrPieceCost);
+  return static_cast<long long>(d.batch) * d.num_kv_heads * tree_row_tiles(d) > 0x7fffffffLL || tiles > 0x7fffffffLL
+             ? GQA_ERR_UNSUPPORTED
+             : GQA_OK;
 }
 
 // CTAs a range: one per KV head and row tile, or pair of row tiles.
@@ -983,7 +986,10 @@ int tree_max_ranges(const gqa_tree_desc_t &d, int sms) {
     // of the slots of the rounds, the share that has work: w units / (rounds slots)
     if (w >= 1 && 10 * w * best_rounds > 11 * best * rounds) best = w, best_rounds = rounds;
   }
-  return static_cast<int>(best);
+  // never more than the batch at full capacity could use
+  const long long most = static_cast<long long>(d.batch) * ((d.max_seq_len + kTile - 1LL) / kTile) / kTrMinTiles;
+  best = best < most ? best : most;
+  return static_cast<int>(best < 1 ? 1 : best);
 }
 size_t tree_part_bytes(const gqa_tree_desc_t &d, int sms) {
   const int w = tree_max_ranges(d, sms);
@@ -1078,7 +1084,7 @@ extern "C" gqa_status_t gqa_tree_attn(const gqa_tree_desc_t *desc, const void *q
   p.words = (d.tree_len + 63) / 64;
   p.paged = paged ? 1 : 0;
   p.max_seq = d.max_seq_len;
-  p.max_blocks = (d.max_seq_len + kTile - 1) / kTile;
+  p.max_blocks = static_cast<int>((d.max_seq_len + kTile - 1LL) / kTile);
   p.num_blocks = paged ? d.num_cache_blocks : 0;
   p.W = tree_max_ranges(d, sms);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(kHeadDim)));
