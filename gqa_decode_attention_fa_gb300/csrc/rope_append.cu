@@ -1,6 +1,8 @@
 // QK RMSNorm + rotary embedding + KV append of any number of tokens (include/gqa_rope.h).
 //
-// One CTA of four warps per token.  Half a warp takes a head row, a lane 8 of its dims (one
+// One CTA per token, of one warp, or of eight where the tokens are few (8000 tokens, 40/8 heads: 50.5 us
+// with one warp, 55 with two, 66 with four, 151 with eight; 128 tokens 9.4 us with one, 4.8 with
+// eight; they cross at 512).  Half a warp takes a head row, a lane 8 of its dims (one
 // 16-byte access; four rows' loads in flight): two chunks of 4, since r / 2 is a multiple of 4 and
 // so a chunk's partners are one chunk of one lane.  In the interleaved layout they are in the
 // chunk itself; in the half layout they come by a shuffle of the packed bf16 words.
@@ -182,7 +184,8 @@ __device__ __forceinline__ dw row_inv_rms(const f2 (&v)[4], float eps) {
   return fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e));
 }
 
-// Tokens up to which a CTA has eight warps (the latency of one token), and above which two.
+// Tokens up to which a CTA has eight warps (the latency of one token), and above which one (the lane's
+// set-up once a token).
 constexpr int kRopeFew = 512;
 constexpr int kRopeAhead = 4;  // row pairs of a warp whose loads are in flight together
 // Error of a key element computed in binary32, relative to r (|x_i w_i cos| + |x_j w_j sin|), in
@@ -193,7 +196,7 @@ constexpr float kKeyWindow = 8.f * 0x1p-24f;
 }  // namespace
 
 template <bool kInterleaved, bool kFull, int kRopeWarps>
-__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 16 : 2) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
   constexpr int kRopeThreads = 32 * kRopeWarps;
   __shared__ float4 cs[kHeadDim / 2];  // m (cos_hi, sin_hi, cos_lo, sin_lo) of pair i
   griddep_wait();  // everything below may come from the preceding kernel
@@ -224,14 +227,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 16 : 2) rop
     }
   };
   load(qsrc, p.Hq, warp);
-  if (tid < p.rotary / 2) {
+  for (int i = tid; i < p.rotary / 2; i += kRopeThreads) {
     dw c, s;
-    cos_sin_turn(static_cast<uint64_t>(pos) * p.turns[tid], &c, &s);
+    cos_sin_turn(static_cast<uint64_t>(pos) * p.turns[i], &c, &s);
     if (p.mag_hi != 1.f || p.mag_lo != 0.f) {
       c = dw_mul(c, dw{p.mag_hi, p.mag_lo});
       s = dw_mul(s, dw{p.mag_hi, p.mag_lo});
     }
-    cs[tid] = make_float4(c.hi, s.hi, c.lo, s.lo);
+    cs[i] = make_float4(c.hi, s.hi, c.lo, s.lo);
   }
   const long long crow = append_row(p, b, s0 + t);
   if (crow < 0 && tid == 0) flag_error(p.err, GQA_DEVERR_PAGE);
@@ -558,14 +561,14 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   const dim3 grid(static_cast<unsigned>(d.batch) * static_cast<unsigned>(d.num_tokens));
   const long long tokens = static_cast<long long>(d.batch) * d.num_tokens;
   const bool full = p.rotary == kHeadDim, many = tokens > kRopeFew;
-  const int warps = many ? 2 : 8;
+  const int warps = many ? 1 : 8;
   void (*kernel)(const RopeAppendParams);
   if (rope->layout == GQA_ROPE_INTERLEAVED)
-    kernel = full ? (many ? rope_append_kernel<true, true, 2> : rope_append_kernel<true, true, 8>)
-                  : (many ? rope_append_kernel<true, false, 2> : rope_append_kernel<true, false, 8>);
+    kernel = full ? (many ? rope_append_kernel<true, true, 1> : rope_append_kernel<true, true, 8>)
+                  : (many ? rope_append_kernel<true, false, 1> : rope_append_kernel<true, false, 8>);
   else
-    kernel = full ? (many ? rope_append_kernel<false, true, 2> : rope_append_kernel<false, true, 8>)
-                  : (many ? rope_append_kernel<false, false, 2> : rope_append_kernel<false, false, 8>);
+    kernel = full ? (many ? rope_append_kernel<false, true, 1> : rope_append_kernel<false, true, 8>)
+                  : (many ? rope_append_kernel<false, false, 1> : rope_append_kernel<false, false, 8>);
   if (launch_pdl(kernel, grid, dim3(32 * warps), 0, static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;

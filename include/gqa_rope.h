@@ -104,7 +104,7 @@ typedef struct gqa_rope_desc {
  *   positions  [B, T] int32 device   p >= 0, the rotary position of each token; NULL for
  *              slot_start[b] + t
  *   counts     [B] int32 device   tokens of each sequence, 0 <= counts[b] <= T; NULL for T.
- *              Rows t >= counts[b] of q, k, v and positions are not read, those of q_out not
+ *              Rows t >= counts[b] of q, k, v and positions are not used, those of q_out not
  *              written, and nothing is stored for them.
  *   q_norm_w, k_norm_w   [128] bf16 device, or NULL for no norm on q / on k
  *   rope       the rotary embedding (read during the call only)
