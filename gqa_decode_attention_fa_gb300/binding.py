@@ -342,7 +342,7 @@ def _on(device: int, stream) -> int:
 
 def _dev(t, name: str, dtype, shape, device: int, optional: bool = False) -> Optional[int]:
     """Device pointer of a dense tensor of the dtype and shape the call needs (`dtype` a torch
-    dtype or a tuple of them; a None in `shape`, or for it, takes any size)."""
+    dtype or a tuple of them; a `shape` of None takes any)."""
     if t is None:
         if optional:
             return None
@@ -352,8 +352,7 @@ def _dev(t, name: str, dtype, shape, device: int, optional: bool = False) -> Opt
     d = t.dtype
     if d is not dtype and not (isinstance(dtype, tuple) and d in dtype):
         raise ValueError(f"{name}: expected {dtype}, got {d}")
-    if shape is not None and t.shape != shape and (
-            t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
@@ -428,8 +427,10 @@ def tree_prepare(parents, ctx_lens, counts, mask, positions, *, device: int = 0,
     (gqa_tree_prepare, include/gqa_tree.h)."""
     tt = _torch()
     i32 = tt.i32
-    pp = _dev(parents, "parents", i32, (None, None), device)
+    if parents.dim() != 2:
+        raise ValueError("parents: expected [batch, tree_len]")
     batch, tree_len = parents.shape
+    pp = _dev(parents, "parents", i32, None, device)
     _check(load().gqa_tree_prepare(
         batch, tree_len, pp, _dev(ctx_lens, "ctx_lens", i32, (batch,), device),
         _dev(counts, "counts", i32, (batch,), device, True),
@@ -517,11 +518,13 @@ class CachePools:
 
 
 def _page_state(ref_counts, page_table, seq_lens, device: int):
-    tt = _torch()
-    i32 = tt.i32
-    ptrs = (_dev(ref_counts, "ref_counts", i32, (None,), device), _dev(page_table, "page_table", i32, (None, None), device),
-            _dev(seq_lens, "seq_lens", i32, (page_table.shape[0],), device))
-    return _desc(PagesDesc, page_table.shape[0], page_table.shape[1], ref_counts.shape[0], device), ptrs
+    i32 = _torch().i32
+    if ref_counts.dim() != 1 or page_table.dim() != 2:
+        raise ValueError("ref_counts [num_blocks], page_table [batch, max_blocks]")
+    batch, max_blocks = page_table.shape
+    ptrs = (_dev(ref_counts, "ref_counts", i32, None, device), _dev(page_table, "page_table", i32, None, device),
+            _dev(seq_lens, "seq_lens", i32, (batch,), device))
+    return _desc(PagesDesc, batch, max_blocks, ref_counts.shape[0], device), ptrs
 
 
 def pages_fork(ref_counts, page_table, seq_lens, src, dst, *, device: int = 0, device_errors=None, stream=None):
@@ -563,8 +566,10 @@ def cache_keep_rows(pools: CachePools, page_table, start, keep, counts, *, max_s
                     stream=None):
     """Rows start[b] + keep[b][i] move to start[b] + i in every pool (gqa_cache_keep_rows)."""
     i32, device = _torch().i32, pools.device
-    kp = _dev(keep, "keep", i32, (None, None), device)
+    if keep.dim() != 2:
+        raise ValueError("keep: expected [batch, max_keep]")
     batch, width = keep.shape
+    kp = _dev(keep, "keep", i32, None, device)
     paged = page_table is not None
     if paged != (pools.num_blocks > 0) or (not paged and pools.rows != batch * max_seq_len):
         raise ValueError("a page table goes with paged pools; contiguous ones have batch * max_seq_len rows")
