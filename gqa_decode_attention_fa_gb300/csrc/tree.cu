@@ -7,27 +7,34 @@
 // tiles, which hold the nodes' own slots, are masked, by the bits of the node's mask.
 //
 // Work.  The batch's tokens, in tiles of 64 (one page) sequence after sequence, are cut into W
-// equal contiguous ranges whatever the sequence boundaries, so ragged batches and single long
-// sequences both fill the GPU; the lengths are read on the device.  CTA (w, kv, r) streams KV
-// head kv of range w for row tile r.  The CTAs of a range run side by side: the heads of a token
-// lie next to each other in the cache, and streamed together they read HBM in whole rows
-// (with the heads of a tile read at different times, 8 heads x 8 sequences of 32k took 182 us
-// instead of XXX), and the row tiles share their tiles in L2.  A piece of a range that is a
-// whole sequence writes its output rows; one that is cut leaves (O, m, l) in the workspace and
-// tree_merge_kernel joins the parts in order.
+// contiguous ranges of equal cost whatever the sequence boundaries, so ragged batches and single
+// long sequences both fill the GPU; the lengths are read on the device.  CTA (w, kv, r) streams KV
+// head kv of range w for row tile r, or for two of them.  The CTAs of a range run side by side: the
+// heads of a token lie next to each other in the cache, and streamed together they read HBM in
+// whole rows (8 x 32k single tokens 182 us with the heads of a tile read at different times, 177 us
+// so), and the row tiles share their tiles in L2.  A piece of a range that is a whole sequence
+// writes its output rows; one that is cut leaves (O, m, l) in the workspace and tree_merge_kernel
+// joins the parts in order.
 //
-// Attention CTA, one per SM: a TMA warp streams the K and V tiles through deep rings (a tile takes
-// longer to come from HBM than to be used; with two CTAs an SM and 2 + 3 stages each, the loads in
-// flight did not cover that); two streams of an MMA warp and four softmax warps each work on
-// them, so that one stream's softmax overlaps the other's products.  Where the CTA has two row
-// tiles (R >= 2) each stream takes one and both use every tile: a tile's way through TMA, whose
-// rows of 128 bytes an SM takes at about 50 GB/s, is paid once for 256 rows.  Where it has one, the
-// streams take the even and the odd tiles and join their O at the end (a softmax thread finds
-// both in its own tensor-memory lane).
+// Attention CTA, one per SM: a TMA warp streams the K and V tiles through deep rings; two streams of
+// an MMA warp and four softmax warps each work on them, so that one stream's softmax overlaps the
+// other's products.  Where the CTA has two row tiles (R >= 2) each stream takes one and both use
+// every tile: a tile's way through TMA, whose rows of 128 bytes an SM takes at about 50 GB/s, is
+// paid once for 256 rows.  Where it has one, the streams take the even and the odd tiles and join
+// their O at the end (a softmax thread finds both in its own tensor-memory lane).
 //   A stream's MMA warp issues S = Q K^T into one of two tensor-memory buffers and O += P V, P
 // read from tensor memory as bf16 hi + lo (rounding P to one bf16 would add an error as large as
 // the output's own rounding); a softmax thread holds a row.  The maximum is raised lazily (by more
 // than 2^8), so most tiles rescale nothing.  The pipeline runs on across the pieces of a range.
+//
+// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 168 us = 6.4 TB/s, 0.94 of the
+// measured copy rate; 32 ragged drafts of up to 16 nodes 114 us, 0.80 (start, the ends of the
+// sequences, the merge).  More: the tensor core with P as hi + lo, 1.5 x the products of the
+// formula; 64 nodes on 128k tokens 278 us = 0.99 PFLOP/s of the formula's, 1.48 issued.  Slower and
+// not kept (the last case, us): two CTAs an SM with shorter rings 297; 128-token stages with one S
+// buffer (an MMA of N = 64 takes as long as one of N = 128, but the softmax then waits for it) 312; S
+// and P in buffers of their own 297; tiles brought to L2 by TMA prefetches 3 to 12 ahead, the second
+// pass through TMA costing more than it hides (single tokens 208 to 309).
 #include <math.h>
 #include <string.h>
 
