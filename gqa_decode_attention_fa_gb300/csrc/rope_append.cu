@@ -1,14 +1,17 @@
 // QK RMSNorm + rotary embedding + KV append of any number of tokens (include/gqa_rope.h).
 //
-// One CTA per token, of one warp, or of eight where the tokens are few (8000 tokens, 40/8 heads: 50.5 us
-// with one warp, 55 with two, 66 with four, 151 with eight; 128 tokens 9.4 us with one, 4.8 with
-// eight; they cross at 512).  Half a warp takes a head row, a lane 8 of its dims (one
-// 16-byte access; four rows' loads in flight): two chunks of 4, since r / 2 is a multiple of 4 and
-// so a chunk's partners are one chunk of one lane.  In the interleaved layout they are in the
-// chunk itself; in the half layout they come by a shuffle of the packed bf16 words.
+// One CTA per token.  Its rows, one contiguous block each of queries, keys and values, come to shared
+// memory by three bulk copies while the CTA computes the token's cosines and sines; the values go on
+// to the cache by another one.  Half a warp takes a head row, a lane 8 of its dims: two chunks of 4,
+// since r / 2 is a multiple of 4 and so a chunk's partners are one chunk of one lane.  In the
+// interleaved layout they are in the chunk itself; in the half layout they come by a shuffle of the
+// packed bf16 words.
 //
-// The work is bound by HBM (a token is read once and written once, 28 KB at 40/8 heads) only if
-// the instructions stay few beside it, about 50 a row:
+// The floor is HBM's (a token is read once and written once, 28 KB at 40/8 heads: 8000 tokens 34 us at
+// the measured copy rate); what bounds the kernel is the instructions, 85 a pair of query rows, 270 a
+// pair of key rows, 350 for the angles: 8000 tokens take 49 us = 4.7 TB/s with a token on two warps (51
+// with one, 56 with four).  Where the tokens are few a token has eight warps (128 tokens 4.5 us
+// against 6.3 with two; 512 tokens 9.3 against 7.5).  What keeps the instructions few:
 //   * the norm weights are folded into the lane's cosines and sines, z = r (x_i (w_i c) + x_j
 //     (-+ w_j s)), in pairs (fma.rn.f32x2);
 //   * the angle p f modulo a turn.  f / 2 pi is kept as a 64-bit fraction of a turn, so p times
@@ -61,6 +64,16 @@ __device__ __forceinline__ long long append_row(const RopeAppendParams &p, int b
 }  // namespace
 
 namespace {
+
+// Bulk copy of this CTA's shared memory to global memory (both 16-byte aligned, a multiple of 16
+// bytes); bulk_wait returns once the thread's committed copies are complete.
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+               "r"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // c + v for |c| >= 2 |v|, both double-words (no cancellation): relative error about 2^-46.
 __device__ __forceinline__ dw dw_add_big(dw c, dw v) {
@@ -184,10 +197,10 @@ __device__ __forceinline__ dw row_inv_rms(const f2 (&v)[4], float eps) {
   return fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e));
 }
 
-// Tokens up to which a CTA has eight warps (the latency of one token), and above which one (the lane's
-// set-up once a token).
-constexpr int kRopeFew = 512;
-constexpr int kRopeAhead = 4;  // row pairs of a warp whose loads are in flight together
+// Tokens up to which a CTA has eight warps, and above which two.
+constexpr int kRopeFew = 384;
+// A CTA holds its token's H_q + 2 H_kv rows in shared memory (256 bytes each), as the prefill prologue.
+constexpr int kRopeMaxSmem = 200 * 1024;
 // Error of a key element computed in binary32, relative to r (|x_i w_i cos| + |x_j w_j sin|), in
 // units of 2^-24: the rounding of r to binary32, cos or sin, its product with w, the product with x,
 // the fma and the product with r, 1 each.  8 leaves room for the rounding of the interval's own ends.
@@ -196,9 +209,16 @@ constexpr float kKeyWindow = 8.f * 0x1p-24f;
 }  // namespace
 
 template <bool kInterleaved, bool kFull, int kRopeWarps>
-__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 12 : 2) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
   constexpr int kRopeThreads = 32 * kRopeWarps;
   __shared__ float4 cs[kHeadDim / 2];  // m (cos_hi, sin_hi, cos_lo, sin_lo) of pair i
+  __shared__ __align__(8) uint64_t arrived;
+  extern __shared__ __align__(128) uint4 rows[];  // the token's H_q + 2 H_kv rows, 16 chunks each
+  const uint32_t bar = smem_addr(&arrived);
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
   griddep_wait();  // everything below may come from the preceding kernel
   const int b = static_cast<int>(blockIdx.x) / p.T, t = static_cast<int>(blockIdx.x) - b * p.T;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, hl = lane & 15;
@@ -216,17 +236,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rop
     return;
   }
 
-  // Row pairs: rows 2 i + half of the queries, then of the keys, then of the values.
-  const uint4 *qsrc = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride) + hl;
-  uint4 x[kRopeAhead];
-  auto load = [&](const uint4 *src, int heads, int i0) {
-#pragma unroll
-    for (int e = 0; e < kRopeAhead; ++e) {
-      const int r = 2 * (i0 + e * kRopeWarps) + half;
-      x[e] = r < heads ? src[r * (kHeadDim / 8)] : make_uint4(0, 0, 0, 0);
-    }
-  };
-  load(qsrc, p.Hq, warp);
+  const uint32_t qbytes = static_cast<uint32_t>(p.Hq) * kHeadDim * 2, kbytes = static_cast<uint32_t>(p.Hkv) * kHeadDim * 2;
+  if (tid == 0) {
+    const uint32_t dst = smem_addr(rows);
+    mbar_arrive_expect_tx(bar, qbytes + 2 * kbytes);
+    bulk_load(dst, p.q + tok * p.q_stride, qbytes, bar);
+    bulk_load(dst + qbytes, p.k + tok * p.k_stride, kbytes, bar);
+    bulk_load(dst + qbytes + kbytes, p.v + tok * p.v_stride, kbytes, bar);
+  }
   for (int i = tid; i < p.rotary / 2; i += kRopeThreads) {
     dw c, s;
     cos_sin_turn(static_cast<uint64_t>(pos) * p.turns[i], &c, &s);
@@ -240,7 +257,15 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rop
   if (crow < 0 && tid == 0) flag_error(p.err, GQA_DEVERR_PAGE);
   RopeLane<kInterleaved, kFull> l;
   l.init(p.rotary, hl, 16 * half);
-  __syncthreads();
+  __syncthreads();  // cos and sin, and the barrier's initialisation
+  if (!__all_sync(0xffffffffu, mbar_wait(bar, 0))) {  // the rows never arrived: flag, write nothing
+    if (lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0 && crow >= 0) {  // the values go to the cache as they are
+    bulk_store(p.v_cache + crow * p.Hkv * kHeadDim, smem_addr(rows) + qbytes + kbytes, kbytes);
+    bulk_commit();
+  }
 
   // The lane's cosines and sines with the norm weights folded in.
   f2 A[4], S[4];
@@ -279,16 +304,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rop
     return rsqrtf(ss * (1.0f / 128.0f) + p.eps);
   };
 
-  // queries
+  // Row pairs, a half warp a row: rows 2 i + half of the queries, then of the keys.
   (void)fold(p.q_norm_w);
   uint4 *qdst = reinterpret_cast<uint4 *>(p.q_out + tok * p.Hq * kHeadDim) + hl;
-  for (int i0 = warp; 2 * i0 < p.Hq; i0 += kRopeAhead * kRopeWarps) {
-    if (i0 != warp) load(qsrc, p.Hq, i0);
-#pragma unroll
-    for (int k = 0; k < kRopeAhead; ++k) {
-      const int i = i0 + k * kRopeWarps;
-      if (2 * i >= p.Hq) break;
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+  for (int i = warp; 2 * i < p.Hq; i += kRopeWarps) {
+    const uint4 x = rows[min(2 * i + half, p.Hq - 1) * 16 + hl];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       uint32_t wp[4];
       l.partners(w, wp);
       f2 v[4];
@@ -304,24 +325,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rop
         out[e] = pack_bf16(a, c);
       }
       if (2 * i + half < p.Hq) qdst[(2 * i + half) * (kHeadDim / 8)] = make_uint4(out[0], out[1], out[2], out[3]);
-    }
   }
   if (crow < 0) return;
 
-  // keys
-  const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride) + hl;
-  const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride) + hl;
   uint4 *kdst = reinterpret_cast<uint4 *>(p.k_cache + crow * p.Hkv * kHeadDim) + hl;
-  uint4 *vdst = reinterpret_cast<uint4 *>(p.v_cache + crow * p.Hkv * kHeadDim) + hl;
-  load(ksrc, p.Hkv, warp);
   const uint4 kw = fold(p.k_norm_w);
-  for (int i0 = warp; 2 * i0 < p.Hkv; i0 += kRopeAhead * kRopeWarps) {
-    if (i0 != warp) load(ksrc, p.Hkv, i0);
-#pragma unroll
-    for (int k = 0; k < kRopeAhead; ++k) {
-      const int i = i0 + k * kRopeWarps;
-      if (2 * i >= p.Hkv) break;
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+  for (int i = warp; 2 * i < p.Hkv; i += kRopeWarps) {
+    const uint4 x = rows[(p.Hq + min(2 * i + half, p.Hkv - 1)) * 16 + hl];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       uint32_t wp[4];
       l.partners(w, wp);
       f2 v[4];
@@ -364,17 +375,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 1 ? 20 : 2) rop
       }
       const uint4 row = make_uint4(out[0], out[1], out[2], out[3]);
       if (2 * i + half < p.Hkv) kdst[(2 * i + half) * (kHeadDim / 8)] = row;
-    }
   }
-  // values: stored as they are
-  for (int i0 = warp; 2 * i0 < p.Hkv; i0 += kRopeAhead * kRopeWarps) {
-    load(vsrc, p.Hkv, i0);
-#pragma unroll
-    for (int k = 0; k < kRopeAhead; ++k) {
-      const int r = 2 * (i0 + k * kRopeWarps) + half;
-      if (r < p.Hkv) vdst[r * (kHeadDim / 8)] = x[k];
-    }
-  }
+  if (tid == 0) bulk_wait();  // the values have left shared memory and are written
 }
 
 }  // namespace gqa
@@ -497,6 +499,28 @@ gqa_status_t rope_turns(const gqa_rope_t *rope, const RopeTurns **out) {
 
 }  // namespace
 
+namespace {
+
+// First call on the current device: the kernels' shared memory.
+bool rope_configure(int device) {
+  static std::atomic<bool> done[64];
+  if (device < 64 && done[device].load(std::memory_order_acquire)) return true;
+  auto raise = [](void (*kernel)(const RopeAppendParams)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeMaxSmem) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+               cudaSuccess;
+  };
+  const bool ok = raise(rope_append_kernel<true, true, 2>) && raise(rope_append_kernel<true, true, 8>) &&
+                  raise(rope_append_kernel<true, false, 2>) && raise(rope_append_kernel<true, false, 8>) &&
+                  raise(rope_append_kernel<false, true, 2>) && raise(rope_append_kernel<false, true, 8>) &&
+                  raise(rope_append_kernel<false, false, 2>) && raise(rope_append_kernel<false, false, 8>);
+  if (!ok) cudaGetLastError();
+  if (ok && device < 64) done[device].store(true, std::memory_order_release);
+  return ok;
+}
+
+}  // namespace
+
 extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void *q, const void *k, const void *v,
                                         void *k_cache, void *v_cache, const int32_t *page_table,
                                         const int32_t *slot_start, const int32_t *positions, const int32_t *counts,
@@ -507,6 +531,7 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   gqa_status_t st = check_cache_geometry(d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, d.num_tokens,
                                          d.block_size, d.max_seq_len, d.num_cache_blocks);
   if (st != GQA_OK) return st;
+  if ((static_cast<long long>(d.num_q_heads) + 2LL * d.num_kv_heads) * kHeadDim * 2 > kRopeMaxSmem) return GQA_ERR_UNSUPPORTED;
   if (!q || !k || !v || !k_cache || !v_cache || !slot_start || !q_out) return GQA_ERR_INVALID_ARG;
   const bool paged = d.block_size > 0;
   if (paged != (page_table != nullptr)) return GQA_ERR_INVALID_ARG;
@@ -561,15 +586,17 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   const dim3 grid(static_cast<unsigned>(d.batch) * static_cast<unsigned>(d.num_tokens));
   const long long tokens = static_cast<long long>(d.batch) * d.num_tokens;
   const bool full = p.rotary == kHeadDim, many = tokens > kRopeFew;
-  const int warps = many ? 1 : 8;
+  const int warps = many ? 2 : 8;
+  const size_t smem = static_cast<size_t>(d.num_q_heads + 2 * d.num_kv_heads) * kHeadDim * 2;
+  if (!rope_configure(d.device)) return GQA_ERR_CUDA;
   void (*kernel)(const RopeAppendParams);
   if (rope->layout == GQA_ROPE_INTERLEAVED)
-    kernel = full ? (many ? rope_append_kernel<true, true, 1> : rope_append_kernel<true, true, 8>)
-                  : (many ? rope_append_kernel<true, false, 1> : rope_append_kernel<true, false, 8>);
+    kernel = full ? (many ? rope_append_kernel<true, true, 2> : rope_append_kernel<true, true, 8>)
+                  : (many ? rope_append_kernel<true, false, 2> : rope_append_kernel<true, false, 8>);
   else
-    kernel = full ? (many ? rope_append_kernel<false, true, 1> : rope_append_kernel<false, true, 8>)
-                  : (many ? rope_append_kernel<false, false, 1> : rope_append_kernel<false, false, 8>);
-  if (launch_pdl(kernel, grid, dim3(32 * warps), 0, static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
+    kernel = full ? (many ? rope_append_kernel<false, true, 2> : rope_append_kernel<false, true, 8>)
+                  : (many ? rope_append_kernel<false, false, 2> : rope_append_kernel<false, false, 8>);
+  if (launch_pdl(kernel, grid, dim3(32 * warps), smem, static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }

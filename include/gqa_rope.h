@@ -23,8 +23,8 @@
  *
  * Conventions are those of gqa_decode.h (bf16 as 16-bit storage, row-major device tensors,
  * asynchronous on `stream`, argument errors before any launch, device-side index errors as
- * GQA_DEVERR_* bits).  Nothing is allocated and no state is kept between calls, so calls on
- * different streams may overlap.  The kernel is launched with programmatic stream
+ * GQA_DEVERR_* bits).  Nothing is allocated and no state is kept between calls besides the
+ * kernels' one-time configuration per device, so calls on different streams may overlap.  The kernel is launched with programmatic stream
  * serialization but reads and writes nothing before the preceding kernel has completed,
  * and never lets the next one start early.
  */
@@ -120,7 +120,8 @@ typedef struct gqa_rope_desc {
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensor -- 16 bytes for bf16, 4 for int32 --,
  * page_table given for a contiguous cache or missing for a paged one, bad sizes, strides,
  * rope fields or eps), GQA_ERR_UNSUPPORTED (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16,
- * block_size other than 0 or 64, more than 2^31 - 1 cache rows or tokens), GQA_ERR_CUDA.
+ * block_size other than 0 or 64, more than 2^31 - 1 cache rows or tokens, (H_q + 2 H_kv) x 256 B
+ * above 200 KiB), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void *q, const void *k, const void *v,
                              void *k_cache, void *v_cache, const int32_t *page_table,

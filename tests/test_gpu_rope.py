@@ -144,7 +144,8 @@ def test_scalings_at_far_positions(scaling, layout):
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,T,cap,paged", [(1, 1, 1, 1, 1, False), (1, 40, 8, 1, 256, True), (2, 16, 1, 3, 65, True),
-                                                  (1, 64, 8, 200, 333, True), (33, 5, 5, 2, 64, False), (1, 32, 2, 64, 64, True)])
+                                                  (1, 64, 8, 200, 333, True), (33, 5, 5, 2, 64, False), (1, 32, 2, 64, 64, True),
+                                                  (2, 320, 40, 3, 64, True), (1, 640, 80, 1, 2, False), (1, 1, 1, 500, 500, True)])
 @pytest.mark.parametrize("fused", [False, True])
 def test_sizes_and_strides(B, Hq, Hkv, T, cap, paged, fused):
     d = setup(B, Hq, Hkv, T, cap, paged, seed=B + T, ragged=T > 2, fused=fused)

@@ -117,7 +117,7 @@ def _rope(rope=None, eps=1e-6, args=None, **over):
     (dict(max_seq_len=0), INV), (dict(num_q_heads=0), INV), (dict(head_dim=64), UNS),
     (dict(num_q_heads=9), UNS), (dict(num_q_heads=34), UNS), (dict(block_size=32, num_cache_blocks=4), UNS),
     (dict(block_size=64, num_cache_blocks=0), INV), (dict(q_stride=1020), INV), (dict(q_stride=1028), INV),
-    (dict(k_stride=128), INV), (dict(v_stride=-256), INV), (dict(batch=1024, max_seq_len=1 << 22), UNS),
+    (dict(num_q_heads=801, num_kv_heads=801), UNS), (dict(num_q_heads=1280, num_kv_heads=80), UNS), (dict(k_stride=128), INV), (dict(v_stride=-256), INV), (dict(batch=1024, max_seq_len=1 << 22), UNS),
 ])
 def test_rope_append_refuses_bad_geometry(over, status):
     assert _rope(**over) == status
