@@ -58,6 +58,7 @@ struct TreeParams {
   int words;                    // 64-bit words of a mask row
   int paged, max_seq, max_blocks, num_blocks;
   int W;                        // ranges the grid is sized for
+  int merge_by_sequence;        // the merge's first index is a sequence, else a boundary between ranges
   float scale_log2;
 };
 
@@ -110,10 +111,15 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
 // but the last, `gap` numbers are left out, the cost of a piece's end in tiles (the streams run
 // dry, O goes out: about 8 us), so that a range with many short sequences gets fewer tiles.  The
 // numbers, fewer than 2^31, go to the ranges in order, `each` to a range, one more to the first `more`.
+//   Batches of few short sequences are not cut: a range is a sequence where none is longer, in tiles,
+// than a range, the ends in it and the merge (about kTrMergeCost tiles) would cost otherwise.  (15
+// sequences of 8 tiles, 8 KV heads: XXX us cut, YYY us whole.)  The numbers are then those of the sequences.
 constexpr int kTrPieceCost = 10;
+constexpr int kTrMergeCost = 6;
 constexpr int kTrMinTiles = 4;  // of a range, so that small batches leave few partials
 struct TreeCut {
   int ranges, gap, each, more;
+  bool whole;      // a range is a sequence
   int lane_first;  // first number of the warp's lane's sequences [lane per, lane per + per)
 
   __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
@@ -125,11 +131,12 @@ struct TreeCut {
 // Every lane of a warp calls these alike.
 __device__ __forceinline__ TreeCut tree_cut(const TreeParams &p, int lane) {
   const int per = (p.B + 31) / 32, b0 = lane * per, b1 = min(p.B, b0 + per);
-  int tiles = 0, seqs = 0;
+  int tiles = 0, seqs = 0, longest = 0;
   for (int b = b0; b < b1; ++b) {
     const int nt = tree_tiles(p, b);
     tiles += nt;
     seqs += nt > 0;
+    longest = max(longest, nt);
   }
   const int own_tiles = tiles, own_seqs = seqs;
 #pragma unroll
@@ -142,15 +149,19 @@ __device__ __forceinline__ TreeCut tree_cut(const TreeParams &p, int lane) {
   c.ranges = all < 1 ? 0 : max(1, min(p.W, all / kTrMinTiles));
   const int quarter = c.ranges > 0 ? all / c.ranges / 4 : 0;  // of a range
   c.gap = min(quarter, kTrPieceCost);
-  const int total = all + c.gap * max(0, all_seqs - 1);
+  longest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(longest)));
+  c.whole = c.ranges > 0 && all_seqs <= p.W &&
+            longest <= all / c.ranges + kTrPieceCost * all_seqs / c.ranges + kTrMergeCost;
+  if (c.whole) c.ranges = all_seqs;
+  const int total = c.whole ? all_seqs : all + c.gap * max(0, all_seqs - 1);
   c.each = c.ranges > 0 ? total / c.ranges : 0;
   c.more = total - c.each * c.ranges;
-  c.lane_first = tiles - own_tiles + c.gap * (seqs - own_seqs);
+  c.lane_first = c.whole ? seqs - own_seqs : tiles - own_tiles + c.gap * (seqs - own_seqs);
   return c;
 }
-__device__ __forceinline__ int tree_span(const TreeParams &p, int b, int gap) {
+__device__ __forceinline__ int tree_span(const TreeParams &p, const TreeCut &c, int b) {
   const int nt = tree_tiles(p, b);
-  return nt > 0 ? nt + gap : 0;
+  return nt < 1 ? 0 : c.whole ? 1 : nt + c.gap;
 }
 // The sequence whose numbers (or the gap behind them) hold `at`, below their end, and its first number.
 __device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c, int at, int *b, int *seq0) {
@@ -161,7 +172,7 @@ __device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c,
   int s = __shfl_sync(0xffffffffu, c.lane_first, owner);
   int x = owner * per;
   while (x + 1 < p.B) {
-    const int nxt = s + tree_span(p, x, c.gap);
+    const int nxt = s + tree_span(p, c, x);
     if (nxt > at) break;
     s = nxt;
     ++x;
@@ -313,6 +324,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       begin = cut.begin(w);
       stop = cut.begin(w + 1);
       tree_find(p, cut, begin, &b, &seq0);
+      if (cut.whole) begin = seq0 = 0, stop = tree_tiles(p, b);
     }
     walk.start(p, begin, stop, b, seq0, cut.gap);
   }
@@ -850,88 +862,138 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 }
 
 // ----------------------------------------------------------------------------------- merge
-// One CTA per (boundary between two ranges, KV head and row tile, 32 dims): it joins the parts of
-// the sequence that the boundary cuts, if it is the first to cut it.  A warp takes four dims, a lane
-// four rows (of column-major partials: 512 contiguous bytes a load).  The parts come in the order of
-// the ranges: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, kept as a running (M, sum, sum).
-// What to join follows from the lengths, which the attention kernel has waited for before it let
-// this one start, so it is found before the wait.
-constexpr int kTrMergeDims = 32;
+// out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the parts k of a cut sequence, in the order
+// of the ranges, kChunk parts at a time with a running (M, sum, sum).  A CTA joins kDims dims of one
+// (sequence, KV head, row tile); its first index is the sequence or, where there are more sequences
+// than cuts, a boundary between ranges, whose CTA joins the sequence that it is the first to cut.  A
+// warp takes kDims / 8 dims, a lane four rows of the column-major partials (512 contiguous bytes a
+// load).  All loads of a chunk go out together; (m, l) pass through shared memory, where a thread
+// takes a row and makes its weights for half of the chunk.  What to join follows from the lengths,
+// which the attention kernel has waited for before it let this one start, so that is found before
+// the wait.
+//   Few cut sequences take 8 dims a CTA and 16 parts a chunk (8 tokens on one 4k sequence, 16 parts:
+// XXX us the call, against 26.6 with one part after the other), many take 32 dims and 4 parts.
 constexpr int kTrMergeThreads = 256;
-constexpr int kTrMergePer = kTrMergeDims / (kTrMergeThreads / 32);  // dims of a warp
-constexpr int kTrMergePitch = kTrMergeDims + 8;                     // of the output staged in shared memory
-__global__ void __launch_bounds__(kTrMergeThreads, 3) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ __align__(16) uint16_t s_out[kTrRows][kTrMergePitch];
-  const int lane = threadIdx.x & 31;
-  const int unit = static_cast<int>(blockIdx.x) % (p.Hkv * p.R), cut = static_cast<int>(blockIdx.x) / (p.Hkv * p.R) + 1;
+template <int kDims>
+__global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int kPer = kDims / 8, kChunk = 16 / kPer;
+  constexpr int kPitch = kDims + 8;  // of the output rows staged in shared memory
+  static_assert(kChunk % 2 == 0 && kChunk <= 16, "a thread makes the weights of half a chunk");
+  __shared__ __align__(16) float s_m[kChunk][kTrRows], s_l[kChunk][kTrRows], s_f[kChunk][kTrRows];
+  __shared__ __align__(16) float s_corr[kTrRows], s_sum[2][kTrRows];
+  __shared__ __align__(16) uint16_t s_out[kTrRows][kPitch];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = static_cast<int>(blockIdx.x) % (p.Hkv * p.R), index = static_cast<int>(blockIdx.x) / (p.Hkv * p.R);
   const int r = unit % p.R, kv = unit / p.R;
   const TreeCut all = tree_cut(p, lane);
   int b = 0, n = 0, w0 = 0, w1 = -1;
-  if (cut < all.ranges) {
-    const int at = all.begin(cut);
-    int first = 0;
-    tree_find(p, all, at, &b, &first);
-    n = tree_nodes(p, b, p.ctx_lens[b]);
-    const int nt = tree_tiles(p, b);
-    // not between two sequences, a node in this row tile, and no earlier boundary in the sequence
-    if (first != at && at < first + nt && r * p.Tt < n && all.range_of(first) == cut - 1) {
-      w0 = cut - 1;
-      w1 = all.range_of(first + nt - 1);
+  if (!all.whole && all.ranges > 1) {
+    int first = 0, at = 0;
+    bool mine = true;
+    if (p.merge_by_sequence) {
+      b = index;
+      const int per = (p.B + 31) / 32;
+      first = __shfl_sync(0xffffffffu, all.lane_first, b / per);
+      for (int x = b / per * per; x < b; ++x) first += tree_span(p, all, x);
+    } else {
+      at = all.begin(index + 1);
+      mine = index + 1 < all.ranges;
+      if (mine) tree_find(p, all, at, &b, &first);
     }
-  }
-  griddep_wait();  // the attention kernel's partials, and its own reads of what follows this call
-  if (w1 < w0) return;
-  const int rows = min(p.Tt, n - r * p.Tt) * p.G;  // of the row tile
-  const int dl = kTrMergePer * (static_cast<int>(threadIdx.x) / 32), d = kTrMergeDims * static_cast<int>(blockIdx.y) + dl;
-  if (4 * lane < rows) {
-    float M[4], L[4], A[kTrMergePer][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      M[k] = -INFINITY, L[k] = 0.f;
-#pragma unroll
-      for (int e = 0; e < kTrMergePer; ++e) A[e][k] = 0.f;
-    }
-    float4 m, l, o[kTrMergePer];
-    auto load = [&](int w) {
-      const float *sp =
-          p.part + ((static_cast<long long>(w) * p.Hkv * p.R + unit) * 2 + (w == w0 ? 1 : 0)) * kTrPartFloats + 4 * lane;
-      m = __ldcg(reinterpret_cast<const float4 *>(sp + kHeadDim * kTrRows));
-      l = __ldcg(reinterpret_cast<const float4 *>(sp + (kHeadDim + 1) * kTrRows));
-#pragma unroll
-      for (int e = 0; e < kTrMergePer; ++e) o[e] = __ldcg(reinterpret_cast<const float4 *>(sp + (d + e) * kTrRows));
-    };
-    load(w0);
-    for (int w = w0; w <= w1; ++w) {
-      const float mm[4] = {m.x, m.y, m.z, m.w}, ll[4] = {l.x, l.y, l.z, l.w};
-      float oo[kTrMergePer][4];
-#pragma unroll
-      for (int e = 0; e < kTrMergePer; ++e) oo[e][0] = o[e].x, oo[e][1] = o[e].y, oo[e][2] = o[e].z, oo[e][3] = o[e].w;
-      if (w < w1) load(w + 1);  // in flight while this part is added
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (ll[k] == 0.f) continue;  // a part that saw none of the row's keys
-        const float m2 = fmaxf(M[k], mm[k]);
-        const float f = fast_exp2(M[k] - m2), h = fast_exp2(mm[k] - m2);
-        L[k] = fmaf(L[k], f, ll[k] * h);
-#pragma unroll
-        for (int e = 0; e < kTrMergePer; ++e) A[e][k] = fmaf(A[e][k], f, oo[e][k] * h);
-        M[k] = m2;
+    if (mine) {
+      n = tree_nodes(p, b, p.ctx_lens[b]);
+      const int nt = tree_tiles(p, b);
+      if (nt > 0 && r * p.Tt < n) {
+        w0 = all.range_of(first);
+        w1 = all.range_of(first + nt - 1);
+        // one range, or another boundary is the first in the sequence: nothing to do here
+        if (w0 == w1 || (!p.merge_by_sequence && w0 != index)) w1 = w0 - 1;
       }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float inv = L[k] != 0.f ? 1.f / L[k] : 0.f;
-#pragma unroll
-      for (int e = 0; e < kTrMergePer; e += 2)
-        *reinterpret_cast<uint32_t *>(&s_out[4 * lane + k][dl + e]) = pack_bf16(A[e][k] * inv, A[e + 1][k] * inv);
-    }
   }
+  griddep_wait();  // the attention kernel's partials
+  if (w1 < w0) return;
+  const int rows = min(p.Tt, n - r * p.Tt) * p.G;  // of the row tile
+  const bool live = 4 * lane < rows;
+  const int d0 = kDims * static_cast<int>(blockIdx.y) + kPer * warp;
+  const int row = tid & (kTrRows - 1), side = tid >> 7;  // of the weights
+  float M = -INFINITY, L = 0.f;  // of `row`, alike on both sides
+  float A[kPer][4];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A[e][k] = 0.f;
+  auto part = [&](int w) {
+    return p.part + ((static_cast<long long>(w) * p.Hkv * p.R + unit) * 2 + (w == w0 ? 1 : 0)) * kTrPartFloats + 4 * lane;
+  };
+  for (int wb = w0; wb <= w1; wb += kChunk) {
+    const int parts = min(kChunk, w1 - wb + 1);
+    float4 o[kChunk][kPer];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        o[k][e] = live && k < parts ? __ldcg(reinterpret_cast<const float4 *>(part(wb + k) + (d0 + e) * kTrRows))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = warp; k < parts; k += 8) {
+      const float *sp = part(wb + k);
+      *reinterpret_cast<float4 *>(&s_m[k][4 * lane]) =
+          live ? __ldcg(reinterpret_cast<const float4 *>(sp + kHeadDim * kTrRows)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4 *>(&s_l[k][4 * lane]) =
+          live ? __ldcg(reinterpret_cast<const float4 *>(sp + (kHeadDim + 1) * kTrRows)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    float m2 = M;
+    for (int k = 0; k < parts; ++k)
+      if (s_l[k][row] != 0.f) m2 = fmaxf(m2, s_m[k][row]);  // (l = 0: a part that saw none of the row's keys)
+    float sum = 0.f;
+    for (int k = side * (kChunk / 2); k < min(parts, (side + 1) * (kChunk / 2)); ++k) {
+      const float l = s_l[k][row], f = l != 0.f ? fast_exp2(s_m[k][row] - m2) : 0.f;
+      s_f[k][row] = f;
+      sum = fmaf(l, f, sum);
+    }
+    s_sum[side][row] = sum;
+    const float corr = M == -INFINITY ? 0.f : fast_exp2(M - m2);
+    if (side == 0) s_corr[row] = corr;
+    M = m2;
+    __syncthreads();
+    L = fmaf(L, corr, s_sum[0][row] + s_sum[1][row]);
+    const float4 c4 = *reinterpret_cast<const float4 *>(&s_corr[4 * lane]);
+    const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) A[e][k] *= cc[k];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+      if (k >= parts) break;
+      const float4 f4 = *reinterpret_cast<const float4 *>(&s_f[k][4 * lane]);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        // a part with weight 0 has nothing of the row, whatever its O holds
+        if (f4.x != 0.f) A[e][0] = fmaf(f4.x, o[k][e].x, A[e][0]);
+        if (f4.y != 0.f) A[e][1] = fmaf(f4.y, o[k][e].y, A[e][1]);
+        if (f4.z != 0.f) A[e][2] = fmaf(f4.z, o[k][e].z, A[e][2]);
+        if (f4.w != 0.f) A[e][3] = fmaf(f4.w, o[k][e].w, A[e][3]);
+      }
+    }
+    __syncthreads();  // before the next chunk's (m, l), and for the sums below
+  }
+  if (side == 0) s_corr[row] = L != 0.f ? 1.f / L : 0.f;
   __syncthreads();
-  constexpr int kChunks = kTrMergeDims / 8;  // of 16 bytes
-  for (int x = threadIdx.x; x < rows * kChunks; x += kTrMergeThreads) {
-    const int row = x / kChunks, c = x % kChunks, tl = row / p.G, g = row - tl * p.G;
+  const float4 i4 = *reinterpret_cast<const float4 *>(&s_corr[4 * lane]);
+  const float inv[4] = {i4.x, i4.y, i4.z, i4.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      s_out[4 * lane + k][kPer * warp + e] = static_cast<uint16_t>(pack_bf16(A[e][k] * inv[k], 0.f) & 0xffffu);
+  __syncthreads();
+  constexpr int kChunks = kDims / 8;  // of 16 bytes
+  for (int x = tid; x < rows * kChunks; x += kTrMergeThreads) {
+    const int y = x / kChunks, c = x % kChunks, tl = y / p.G, g = y - tl * p.G;
     *reinterpret_cast<uint4 *>(p.out + ((static_cast<long long>(b) * p.T + r * p.Tt + tl) * p.Hq + kv * p.G + g) * kHeadDim +
-                               kTrMergeDims * blockIdx.y + 8 * c) = *reinterpret_cast<const uint4 *>(&s_out[row][8 * c]);
+                               kDims * blockIdx.y + 8 * c) = *reinterpret_cast<const uint4 *>(&s_out[y][8 * c]);
   }
 }
 
@@ -994,7 +1056,8 @@ int tree_max_ranges(const gqa_tree_desc_t &d, int sms) {
     if (w >= 1 && 10 * w * best_rounds > 11 * best * rounds) best = w, best_rounds = rounds;
   }
   // never more than the batch at full capacity could use
-  const long long most = static_cast<long long>(d.batch) * ((d.max_seq_len + kTile - 1LL) / kTile) / kTrMinTiles;
+  long long most = static_cast<long long>(d.batch) * ((d.max_seq_len + kTile - 1LL) / kTile) / kTrMinTiles;
+  most = most > d.batch ? most : d.batch;
   best = best < most ? best : most;
   return static_cast<int>(best < 1 ? 1 : best);
 }
@@ -1110,12 +1173,16 @@ extern "C" gqa_status_t gqa_tree_attn(const gqa_tree_desc_t *desc, const void *q
     return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool pairs = p.R > 1;
+  p.merge_by_sequence = p.B <= p.W - 1;
+  const long long joins = static_cast<long long>(p.merge_by_sequence ? p.B : p.W - 1) * p.Hkv * p.R;
+  // the fewest dims a CTA with which the joins still run at once (two CTAs an SM), 8 to 32
+  const int dims = joins * (kHeadDim / 8) <= 2LL * sms ? 8 : joins * (kHeadDim / 16) <= 2LL * sms ? 16 : 32;
+  auto *merge = dims == 8 ? tree_merge_kernel<8> : dims == 16 ? tree_merge_kernel<16> : tree_merge_kernel<32>;
   if (launch_pdl(pairs ? tree_attn_kernel<2> : tree_attn_kernel<1>, dim3(static_cast<unsigned>(p.W * tree_units(d))),
                  dim3(kTrThreads), static_cast<size_t>(pairs ? TreeSmem<2>::kBytes : TreeSmem<1>::kBytes), s, tq, tk, tv,
                  p) != cudaSuccess ||
-      (p.W > 1 &&
-       launch_pdl(tree_merge_kernel, dim3(static_cast<unsigned>((p.W - 1) * p.Hkv * p.R), kHeadDim / kTrMergeDims),
-                  dim3(kTrMergeThreads), 0, s, p) != cudaSuccess)) {
+      (p.W > 1 && launch_pdl(merge, dim3(static_cast<unsigned>(joins), static_cast<unsigned>(kHeadDim / dims)),
+                             dim3(kTrMergeThreads), 0, s, p) != cudaSuccess)) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
