@@ -27,10 +27,11 @@
 // the output's own rounding); a softmax thread holds a row.  The maximum is raised lazily (by more
 // than 2^8), so most tiles rescale nothing.  The pipeline runs on across the pieces of a range.
 //
-// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 168 us = 6.4 TB/s, 0.94 of the
-// measured copy rate; 32 ragged drafts of up to 16 nodes 114 us, 0.80 (start, the ends of the
+// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 165 us = 6.5 TB/s, 0.96 of the
+// measured copy rate; 32 ragged drafts of up to 16 nodes 113 us, 0.80 (start, the ends of the
 // sequences, the merge).  More: the tensor core with P as hi + lo, 1.5 x the products of the
-// formula; 64 nodes on 128k tokens 278 us = 0.99 PFLOP/s of the formula's, 1.48 issued.  Slower and
+// formula; 64 nodes on 128k tokens 270 us = 1.02 PFLOP/s of the formula's, 1.53 issued.  Small calls:
+// latency, 9 us for the shortest (2.3 us to find the range and set up, 1.7 to the first scores).  Slower and
 // not kept (the last case, us): two CTAs an SM with shorter rings 297; 128-token stages with one S
 // buffer (an MMA of N = 64 takes as long as one of N = 128, but the softmax then waits for it) 312; S
 // and P in buffers of their own 297; tiles brought to L2 by TMA prefetches 3 to 12 ahead, the second
@@ -58,6 +59,7 @@ struct TreeParams {
   int words;                    // 64-bit words of a mask row
   int paged, max_seq, max_blocks, num_blocks;
   int W;                        // ranges the grid is sized for
+  int out_wide;                 // `out` is 32-byte aligned
   int merge_by_sequence;        // the merge's first index is a sequence, else a boundary between ranges
   float scale_log2;
 };
@@ -113,7 +115,7 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
 // numbers, fewer than 2^31, go to the ranges in order, `each` to a range, one more to the first `more`.
 //   Batches of few short sequences are not cut: a range is a sequence where none is longer, in tiles,
 // than a range, the ends in it and the merge (about kTrMergeCost tiles) would cost otherwise.  (15
-// sequences of 8 tiles, 8 KV heads: XXX us cut, YYY us whole.)  The numbers are then those of the sequences.
+// sequences of 8 tiles, 8 KV heads: 26 us cut, 17 us whole.)  The numbers are then those of the sequences.
 constexpr int kTrPieceCost = 10;
 constexpr int kTrMergeCost = 6;
 constexpr int kTrMinTiles = 4;  // of a range, so that small batches leave few partials
@@ -184,9 +186,11 @@ __device__ __forceinline__ void tree_find(const TreeParams &p, const TreeCut &c,
 // Walks the sequences a range [pos, end) covers.  Every warp of the CTA runs its own copy, all
 // lanes alike.
 struct TreeWalk {
-  int pos, end;    // numbers still to do
-  int seq0;        // first number of sequence b
-  int b, nt, gap;  // sequence, its tiles
+  int pos, end;         // numbers still to do
+  int seq0;             // first number of sequence b
+  int b, gap;
+  int ctx, n, nt;       // sequence b: context, nodes (-1: invalid lengths), tiles
+  int ctx_next, n_next; // of sequence b + 1, on the way while b is worked on
   // of the piece at hand
   int j0, j1;
   bool whole;  // the piece is its whole sequence
@@ -197,7 +201,21 @@ struct TreeWalk {
     b = b0;
     seq0 = s0;
     gap = g;
-    nt = pos < end ? tree_tiles(p, b) : 0;
+    nt = 0;
+    if (pos < end) {
+      fetch(p, b);
+      enter(p);
+    }
+  }
+  __device__ __forceinline__ void fetch(const TreeParams &p, int x) {
+    ctx_next = x < p.B ? p.ctx_lens[x] : 0;
+    n_next = x < p.B && p.counts ? p.counts[x] : p.T;
+  }
+  __device__ __forceinline__ void enter(const TreeParams &p) {  // sequence b, whose lengths were fetched
+    ctx = ctx_next;
+    n = (ctx >= 0 && n_next >= 0 && n_next <= p.T && static_cast<long long>(ctx) + n_next <= p.max_seq) ? n_next : -1;
+    nt = n > 0 ? (ctx + n - 1) / kTile + 1 : 0;
+    fetch(p, b + 1);
   }
   // The next piece; false when the range is done.
   __device__ __forceinline__ bool next(const TreeParams &p) {
@@ -206,7 +224,7 @@ struct TreeWalk {
       if (pos < seq0) pos = seq0;
       if (pos >= end) break;
       ++b;
-      nt = tree_tiles(p, b);
+      enter(p);
     }
     if (pos >= end) return false;
     j0 = pos - seq0;
@@ -219,6 +237,17 @@ struct TreeWalk {
 
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+// 32 bytes to global memory: a thread's whole sector, in one store where the address allows it.
+__device__ __forceinline__ void store_32b(uint16_t *dst, const uint32_t (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -371,9 +400,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   auto v_ptr = [&](int s) { return smem + Smem::kOffV + s * kTrTileBytes; };
   // A piece's streams: 0 if the CTA's row tiles have no node in the sequence, 1 if only the first
   // has (the streams share its tiles), 2 if both have (each stream takes all tiles for its own).
-  auto row_tiles = [&](int b) {
-    const int n = tree_nodes(p, b, p.ctx_lens[b]);
-    return r0 * p.Tt >= n ? 0 : (NQ == 2 && (r0 + 1) * p.Tt < n) ? 2 : 1;
+  auto row_tiles = [&](const TreeWalk &x) {
+    return r0 * p.Tt >= x.n ? 0 : (NQ == 2 && (r0 + 1) * p.Tt < x.n) ? 2 : 1;
   };
 
   if (warp == kTrProducerWarp) {
@@ -383,7 +411,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     int it = 0, piece = 0, queries = 0;  // KV tiles, pieces, loads of queries so far: stages and phases
     bool ok = true;
     while (ok && walk.next(p)) {
-      const int b = walk.b, j0 = walk.j0, j1 = walk.j1, nr = row_tiles(b);
+      const int b = walk.b, j0 = walk.j0, j1 = walk.j1, nr = row_tiles(walk);
       if (nr == 0) continue;
       auto row_of = [&](int j) -> int {  // -kTile where there is none: TMA fills zeros
         if (j >= j1) return -kTile;
@@ -498,7 +526,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         return true;
       };
       while (ok && walk.next(p)) {
-        const int nr = row_tiles(walk.b);
+        const int nr = row_tiles(walk);
         if (nr == 0) continue;
         const int nt = walk.j1 - walk.j0, step = nr == 1 ? 2 : 1, first = nr == 1 ? st : 0;
         const uint64_t qd = qd0 + (nr == 2 ? st * (kTrQBytes / 16) : 0);
@@ -561,7 +589,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     };
     while (ok && walk.next(p)) {
       const int b = walk.b, j0 = walk.j0, j1 = walk.j1;
-      const int ctx = p.ctx_lens[b], n = tree_nodes(p, b, ctx), nr = row_tiles(b);
+      const int ctx = walk.ctx, n = walk.n, nr = row_tiles(walk);
       if (nr == 0) continue;
       const int r = r0 + (nr == 2 ? st : 0), step = nr == 1 ? 2 : 1, first = nr == 1 ? st : 0;
       const int t = r * p.Tt + tl;  // this row's node
@@ -604,26 +632,30 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             ok = false;
             break;
           }
-          // 16-byte chunks: half (c >> 9), slot, chunk; four of a thread's at a time
+          // 16-byte chunks: slot, half, chunk, from the first node's slot on
           bool bad = false;
-          const int each = nr * kTrRows;
-          for (int cb = row + (nr == 2 ? st * kTrRows : 0); cb < 2 * kTile * 8; cb += 4 * each) {
-            uint4 q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = reinterpret_cast<const uint4 *>(v_ptr(vs))[cb + e * each];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = cb + e * each, node = o0 + ((c >> 3) & (kTile - 1));
-              if (node < 0) continue;
-              uint32_t y[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
-              bool hit = node >= n;
+          const int c1 = kTile * 16, each = nr * kTrRows;
+          for (int c = 16 * max(0, -o0) + row + (nr == 2 ? st * kTrRows : 0); c < c1; c += each) {
+            const int slot = c >> 4;
+            uint4 *at = reinterpret_cast<uint4 *>(v_ptr(vs)) + ((c & 8) << 6) + slot * 8 + (c & 7);
+            if (o0 + slot >= n) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            const uint4 q = *at;
+            // an exponent of all ones carries into the sign's place
+            const uint32_t ones = (((q.x & 0x7f807f80u) + 0x00800080u) | ((q.y & 0x7f807f80u) + 0x00800080u) |
+                                   ((q.z & 0x7f807f80u) + 0x00800080u) | ((q.w & 0x7f807f80u) + 0x00800080u)) &
+                                  0x80008000u;
+            if (ones) {
+              uint32_t y[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                if (node >= n) y[k] = 0u;
-                if ((y[k] & 0x7f80u) == 0x7f80u) y[k] &= 0xffff0000u, hit = bad = true;
-                if ((y[k] & 0x7f800000u) == 0x7f800000u) y[k] &= 0xffffu, hit = bad = true;
+                if ((y[k] & 0x7f80u) == 0x7f80u) y[k] &= 0xffff0000u;
+                if ((y[k] & 0x7f800000u) == 0x7f800000u) y[k] &= 0xffffu;
               }
-              if (hit) reinterpret_cast<uint4 *>(v_ptr(vs))[c] = make_uint4(y[0], y[1], y[2], y[3]);
+              *at = make_uint4(y[0], y[1], y[2], y[3]);
+              bad = true;
             }
           }
           if (bad) atomicMax(&v_bad[piece & 3], static_cast<uint32_t>(piece + 1));
@@ -786,15 +818,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           float o[32];
           if (nr == 1) {
             const uint32_t t0 = tmem + lane_base + kTrTmemO + 32 * c4;
-            tmem_ld32(t0, o);
-            tmem_wait_ld();
             const float f0 = st == 0 ? f_own : f_other, f1 = st == 0 ? f_other : f_own;
+            tmem_ld32(t0, o);
             if (two) {
               float o1[32];
               tmem_ld32(t0 + kTrTmemStream, o1);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e] * f0);
+            } else {
+              tmem_wait_ld();
             }
           } else {
             tmem_ld32(tm + kTrTmemO + 32 * c4, o);
@@ -825,13 +858,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) mine[(32 * c4 + e) * kTrRows + row] = o[e];
           } else if (valid) {
-            uint4 *d4 = reinterpret_cast<uint4 *>(dst + 32 * c4);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              d4[q] = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
-                                 pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                 pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                 pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+            for (int q = 0; q < 2; ++q) {
+              uint32_t x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = pack_bf16(o[16 * q + 2 * e] * inv, o[16 * q + 2 * e + 1] * inv);
+              store_32b(dst + 32 * c4 + 16 * q, x, p.out_wide);
+            }
           }
         }
         if (!walk.whole && (nr == 2 || st == 0)) {
@@ -872,7 +905,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 // which the attention kernel has waited for before it let this one start, so that is found before
 // the wait.
 //   Few cut sequences take 8 dims a CTA and 16 parts a chunk (8 tokens on one 4k sequence, 16 parts:
-// XXX us the call, against 26.6 with one part after the other), many take 32 dims and 4 parts.
+// 16.3 us the call, against 26.6 with one part after the other), many take 32 dims and 4 parts (8 x 32k
+// single tokens, 64 joins of 3 to 4 parts: 165 us the call, against 178 with 8 dims).
 constexpr int kTrMergeThreads = 256;
 template <int kDims>
 __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __grid_constant__ TreeParams p) {
@@ -1157,6 +1191,7 @@ extern "C" gqa_status_t gqa_tree_attn(const gqa_tree_desc_t *desc, const void *q
   p.max_blocks = static_cast<int>((d.max_seq_len + kTile - 1LL) / kTile);
   p.num_blocks = paged ? d.num_cache_blocks : 0;
   p.W = tree_max_ranges(d, sms);
+  p.out_wide = aligned_to(out, 32) ? 1 : 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(kHeadDim)));
 
   const long long rows = paged ? static_cast<long long>(d.num_cache_blocks) * kTile

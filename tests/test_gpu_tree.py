@@ -293,6 +293,17 @@ def test_a_stream_of_the_callers():
         call(w, ws=w["ws"][:256])
 
 
+def test_outputs_at_any_16_byte_boundary():
+    w = make(3, 8, 2, 5, [100, 0, 70], seed=18)
+    call(w)
+    want = w["out"].clone()
+    room = torch.zeros(w["out"].numel() + 8, dtype=torch.bfloat16, device="cuda")
+    w["out"] = room[8:].view(want.shape)
+    assert w["out"].data_ptr() % 32 == 16
+    call(w)
+    assert torch.equal(w["out"].view(torch.int16), want.view(torch.int16)) and not bool(room[:8].any())
+
+
 def test_wrapper_refuses_wrong_tensors():
     w = make(2, 8, 2, 4, [40, 3], seed=14)
     for name, bad in [("q", w["q"].float()), ("q", w["q"][:, :3]), ("k", w["k"].cpu()), ("mask", w["mask"][:, :, :0]), ("mask", w["mask"].int()),
