@@ -474,7 +474,7 @@ gqa_status_t check_state(const gqa_pages_desc_t *desc, const void *refs, const v
                          const void *err) {
   if (!desc || !refs || !table || !lens) return GQA_ERR_INVALID_ARG;
   if (desc->batch < 1 || desc->batch > GQA_MAX_BATCH || desc->max_blocks < 1 || desc->num_blocks < 1 ||
-      desc->num_blocks >= (1 << 25) || desc->max_blocks >= (1 << 25))
+      desc->num_blocks >= (1 << 25) || static_cast<long long>(desc->batch) * desc->max_blocks > 0x7fffffffLL)
     return GQA_ERR_INVALID_ARG;
   if (!aligned_to(refs, 4) || !aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(err, 4))
     return GQA_ERR_INVALID_ARG;

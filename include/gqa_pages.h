@@ -16,7 +16,8 @@
  *
  * Results do not depend on timing: pages are taken lowest id first, in the order of the
  * sequences and of their pages.  Conventions are those of gqa_decode.h; int32 tensors 4-byte
- * aligned; nothing is allocated and no state is kept.  Kernels are launched with
+ * aligned; nothing is allocated and no state is kept (the first call of each kind on a device
+ * loads its kernel: make it before capturing a graph).  Kernels are launched with
  * programmatic stream serialization but read and write nothing before the preceding kernel
  * has completed, and never let the next one start early.
  */
@@ -45,7 +46,7 @@ typedef struct gqa_pool {
 /* Shape of the page state. */
 typedef struct gqa_pages_desc {
     int batch;      /* B sequences, 1..GQA_MAX_BATCH */
-    int max_blocks; /* entries of a sequence's page-table row (>= 1) */
+    int max_blocks; /* entries of a sequence's page-table row (>= 1; B * max_blocks < 2^31) */
     int num_blocks; /* pages of the pool, 1 .. 2^25 - 1 */
     int device;     /* CUDA device ordinal the call runs on */
 } gqa_pages_desc_t;

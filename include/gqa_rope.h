@@ -19,12 +19,14 @@
  *   z_i  = m (y_i cos a - y_j sin a),  z_j = m (y_j cos a + y_i sin a),  a = p f_i
  * for each pair (i, j) of index i, p = positions[b][t], m the magnitude; z = y in the dims
  * from r on.  z is rounded once to bf16; for keys, which stay in the cache, the rounding is
- * that of the exact value (as in the decode step); queries are computed in binary32.
+ * that of the exact value (as in the decode step); queries are computed in binary32.  A row's sum of
+ * squares has to be finite in binary32 where it is normalised (|x| below about 10^18).
  *
  * Conventions are those of gqa_decode.h (bf16 as 16-bit storage, row-major device tensors,
  * asynchronous on `stream`, argument errors before any launch, device-side index errors as
  * GQA_DEVERR_* bits).  Nothing is allocated and no state is kept between calls besides the
- * kernels' one-time configuration per device, so calls on different streams may overlap.  The kernel is launched with programmatic stream
+ * kernels' one-time configuration per device (make a first call before capturing a graph), so
+ * calls on different streams may overlap.  The kernel is launched with programmatic stream
  * serialization but reads and writes nothing before the preceding kernel has completed,
  * and never lets the next one start early.
  */

@@ -12,7 +12,7 @@
  * tensors, bf16 tensors 16-byte aligned, int32 ones 4-byte and masks 8-byte aligned,
  * asynchronous on `stream`, argument errors before any launch, device-side index errors as
  * GQA_DEVERR_* bits).  Nothing is allocated; no state is kept between calls besides the
- * kernels' one-time configuration per device.  Scratch memory is the caller's `workspace`:
+ * kernels' one-time configuration per device (make a first call before capturing a graph).  Scratch memory is the caller's `workspace`:
  * calls that may overlap (different streams, two graphs replayed at once) need one each.
  * Kernels are launched with programmatic stream serialization but read and write nothing
  * before the preceding kernel has completed, and the last kernel of a call never lets the

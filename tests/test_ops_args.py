@@ -189,7 +189,7 @@ def test_tree_prepare_refuses_bad_arguments():
 def test_page_state_refusals():
     lib = binding.load()
     good = (2, 4, 16, 0)
-    for bad in [(0, 4, 16, 0), (1025, 4, 16, 0), (2, 0, 16, 0), (2, 4, 0, 0), (2, 4, 1 << 25, 0)]:
+    for bad in [(0, 4, 16, 0), (1025, 4, 16, 0), (2, 0, 16, 0), (2, 4, 0, 0), (2, 4, 1 << 25, 0), (1024, 1 << 21, 16, 0)]:
         d = binding.PagesDesc(*bad)
         assert lib.gqa_pages_fork(ctypes.byref(d), DUMMY, DUMMY, DUMMY, DUMMY, DUMMY, 1, None, None) == INV
         assert lib.gqa_pages_resize(ctypes.byref(d), DUMMY, DUMMY, DUMMY, DUMMY, DUMMY, DUMMY, None, None) == INV
