@@ -344,7 +344,30 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 
   griddep_wait();  // everything below may come from the preceding kernel
   if (p.W > 1) griddep_launch_dependents();  // tree_merge_kernel follows, and it waits
-  // every warp finds the CTA's range while tensor memory and the barriers are set up
+  // Tensor memory, barriers and maps are set up by a warp each, while the others look for the range.
+  if (warp == kTrMmaWarp) {
+    tmem_alloc(smem_addr(tmem_slot), kTrTmemCols);
+    tmem_relinquish();
+  } else if (warp == kTrMmaWarp + 1) {
+    for (int i = lane; i < Smem::kNumBars; i += 32) {
+      uint64_t *bar = k_full + i;
+      // the queries, and tiles that both streams use, are given back by both; P comes from a stream's
+      // four softmax warps; O is read by all eight
+      int count = 1;
+      if ((bar >= k_empty && bar < v_full) || (bar >= v_empty && bar < s_full)) count = NQ;
+      if (bar == q_empty) count = 2;
+      if (bar >= p_full && bar < pv_done) count = 4;
+      if ((bar >= o_free && bar < drain) || bar == meet) count = 8;
+      mbar_init(smem_addr(bar), count);
+    }
+    if (lane < 4) v_bad[lane] = 0;
+    fence_barrier_init();
+    __syncwarp();
+  } else if (warp == kTrProducerWarp && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
   TreeWalk walk;
   {
     const TreeCut cut = tree_cut(p, lane);
@@ -356,30 +379,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       if (cut.whole) begin = seq0 = 0, stop = tree_tiles(p, b);
     }
     walk.start(p, begin, stop, b, seq0, cut.gap);
-  }
-  if (tid == 0) {
-    for (int i = 0; i < Smem::kNumBars; ++i) {
-      uint64_t *bar = k_full + i;
-      // the queries, and tiles that both streams use, are given back by both; P comes from a stream's
-      // four softmax warps; O is read by all eight
-      int count = 1;
-      if ((bar >= k_empty && bar < v_full) || (bar >= v_empty && bar < s_full)) count = NQ;
-      if (bar == q_empty) count = 2;
-      if (bar >= p_full && bar < pv_done) count = 4;
-      if ((bar >= o_free && bar < drain) || bar == meet) count = 8;
-      mbar_init(smem_addr(bar), count);
-    }
-    for (int i = 0; i < 4; ++i) v_bad[i] = 0;
-    fence_barrier_init();
-  }
-  if (warp == kTrProducerWarp && lane == 0) {
-    prefetch_tensormap(&tmQ);
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
-  }
-  if (warp == kTrMmaWarp) {
-    tmem_alloc(smem_addr(tmem_slot), kTrTmemCols);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
