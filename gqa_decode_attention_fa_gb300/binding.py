@@ -365,7 +365,9 @@ def _err(t, device: int) -> Optional[int]:
 
 @functools.lru_cache(maxsize=1024)
 def _desc(kind, *fields):
-    """A reference to the descriptor with these fields."""
+    """A reference to the descriptor with these fields (ctypes would drop the upper bits of larger ones)."""
+    if any(not -2**31 <= int(x) < 2**31 for x in fields):
+        raise ValueError(f"{kind.__name__}: a field of {fields} does not fit 32 bits")
     return ctypes.byref(kind(*fields))
 
 
@@ -480,15 +482,17 @@ def tree_attn(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, ma
     if workspace.numel() < need:
         raise ValueError(f"workspace: {need} bytes needed, got {workspace.numel()}")
     shape = (batch, tree_len, num_q_heads, 128)
+    qp, op = _dev(q, "q", tt.bf16, shape, device), _dev(out, "out", tt.bf16, shape, device)
+    if qp == op:
+        raise ValueError("out: must not be q, which other CTAs still read")
     _check(load().gqa_tree_attn(
-        _desc(TreeDesc, *fields), _dev(q, "q", tt.bf16, shape, device),
+        _desc(TreeDesc, *fields), qp,
         _cache("k_cache", k_cache, rows, num_kv_heads, device),
         _cache("v_cache", v_cache, rows, num_kv_heads, device),
         _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
         _dev(ctx_lens, "ctx_lens", i32, (batch,), device), _dev(counts, "counts", i32, (batch,), device, True),
         _dev(mask, "mask", tt.word64, (batch, tree_len, (tree_len + 63) // 64), device),
-        _dev(out, "out", tt.bf16, shape, device), ws,
-        _err(device_errors, device), _on(device, stream)),
+        op, ws, _err(device_errors, device), _on(device, stream)),
         "gqa_tree_attn")
 
 
@@ -511,6 +515,9 @@ class CachePools:
             if size == 0 or size % self.rows:
                 raise ValueError(f"pool {i}: {size} bytes are not {self.rows} rows")
             self.array[i] = Pool(t.data_ptr(), size // self.rows)
+        spans = sorted((p.base, p.row_bytes * self.rows) for p in self.array)
+        if any(a + size > b for (a, size), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("pools: two of the tensors overlap, their rows would be moved twice")
         self.tensors = tensors
 
     def __len__(self):

@@ -78,7 +78,8 @@ gqa_status_t gqa_pages_fork(const gqa_pages_desc_t *desc, int32_t *ref_counts, i
  * the last of them (by index) keeps it.
  *   new_lens [B] int32 device
  *   cow_src, cow_dst [B] int32 device   written: the pages to copy, or -1
- * If there are too few free pages, nothing changes and GQA_DEVERR_NOPAGE is set (cow_* are all -1).  A
+ * If there are too few free pages, nothing changes and GQA_DEVERR_NOPAGE is set (cow_* are all -1):
+ * the sequences must not be written to then, a last page that they share has not been split.  A
  * sequence whose length or new length is beyond its row (GQA_DEVERR_SEQLEN) or
  * whose table names a page outside the pool or a free one, where the call needs it
  * (GQA_DEVERR_PAGE), is left as it is.
@@ -91,7 +92,8 @@ gqa_status_t gqa_pages_resize(const gqa_pages_desc_t *desc, int32_t *ref_counts,
 /*
  * gqa_pages_copy -- page dst[i] := page src[i] in every pool, for i < num_pairs
  * (1..GQA_MAX_PAGE_PAIRS).
- *   pools      host array [num_pools] (1..GQA_MAX_POOLS), read during the call only; pools must not overlap
+ *   pools      host array [num_pools] (1..GQA_MAX_POOLS), read during the call only; pools must not
+ *              overlap (their rows would be moved twice), here and in gqa_cache_keep_rows
  *   num_blocks pages of each pool (its size is num_blocks * 64 * row_bytes)
  *   src, dst   [num_pairs] int32 device   src[i] < 0: the pair is not used
  * A pair with a page outside the pool (GQA_DEVERR_PAGE), or whose dst is an earlier used pair's dst or

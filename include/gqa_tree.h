@@ -78,8 +78,8 @@ gqa_status_t gqa_tree_workspace_bytes(const gqa_tree_desc_t *desc, size_t *bytes
  *   mask       [B, T, ceil(T/64)] uint64 device   as gqa_tree_prepare writes it; any pattern is
  *              allowed (bits from n_b on are ignored)
  *   out        [B, T, H_q, d] bf16 device   softmax over the seen keys of q . K / sqrt(d), applied to
- *              V; zeros for a node that sees no key; rows t >= n_b are left as they were.  Must not
- *              overlap any input.
+ *              V; zeros for a node that sees no key (or whose every score is -infinity); rows t >= n_b
+ *              are left as they were.  Must not overlap any input.
  *   workspace  device memory of gqa_tree_workspace_bytes bytes, 256-byte aligned; its contents need
  *              not be set and are not kept
  *   device_errors   optional device pointer to a uint32.  c_b < 0 (GQA_DEVERR_POSITION), n_b

@@ -422,3 +422,13 @@ def test_wrapper_refuses_wrong_tensors():
         binding.CachePools([torch.zeros(100, dtype=torch.uint8, device="cuda")], num_blocks=1)
     with pytest.raises(ValueError):
         binding.CachePools([], num_blocks=1)
+
+
+def test_pools_that_overlap_are_refused():
+    """Two pools on the same memory would have their rows moved twice."""
+    whole = torch.zeros(4 * 64 * 48, dtype=torch.uint8, device="cuda")
+    row = 4 * 64 * 16
+    binding.CachePools([whole[:row], whole[row:2 * row]], num_blocks=4)   # next to each other
+    for pools in ([whole[:row], whole[:row]], [whole[16:row + 16], whole[:row]], [whole[row - 16:2 * row - 16], whole[:row]]):
+        with pytest.raises(ValueError):
+            binding.CachePools(pools, num_blocks=4)

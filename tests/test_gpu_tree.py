@@ -396,3 +396,10 @@ def test_prepare_contains_bad_parents_and_lengths():
     np.testing.assert_array_equal(mask[0].cpu().numpy(), pack(ancestors(fixed, T), T))
     assert pos[0].tolist() == [10, 11, 10, 12, 10, 11]
     assert bool((mask[1:] == 77).all()) and bool((pos[1:] == -5).all())
+
+
+def test_output_over_the_queries_is_refused():
+    z = lambda *n: torch.zeros(n, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    ctx, mask, q = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.ones((1, 1, 1), dtype=torch.int64, device="cuda"), z(1, 1, 4, 128)
+    with pytest.raises(ValueError):
+        binding.tree_attn(1, 4, 1, 1, 64, q, z(64, 1, 128), z(64, 1, 128), None, ctx, None, mask, q.view(1, 1, 4, 128))

@@ -235,3 +235,12 @@ def test_copy_and_keep_refusals():
         assert keep(**over) == INV, over
     assert keep(block_size=32) == UNS and keep(num_blocks=1 << 26) == UNS
     assert lib.gqa_cache_keep_rows(None, good, 2, *[DUMMY] * 4, None, None) == INV
+
+
+def test_fields_beyond_32_bits_are_refused():
+    for field in (1 << 31, (1 << 32) + 64, -(1 << 31) - 1):
+        with pytest.raises(ValueError):
+            binding._desc(binding.PagesDesc, 2, field, 16, 0)
+        with pytest.raises(ValueError):
+            binding.tree_workspace_bytes(2, 8, 2, 4, field)
+    binding._desc(binding.PagesDesc, 2, (1 << 31) - 1, 16, 0)
