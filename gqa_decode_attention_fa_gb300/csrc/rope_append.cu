@@ -2,16 +2,17 @@
 //
 // One CTA per token.  Its rows, one contiguous block each of queries, keys and values, come to shared
 // memory by three bulk copies while the CTA computes the token's cosines and sines; the values go on
-// to the cache by another one.  Half a warp takes a head row, a lane 8 of its dims: two chunks of 4,
-// since r / 2 is a multiple of 4 and so a chunk's partners are one chunk of one lane.  In the
-// interleaved layout they are in the chunk itself; in the half layout they come by a shuffle of the
-// packed bf16 words.
+// to the cache by another one.  Half a warp takes a head row, a lane 8 of its dims with their
+// partners among them: two chunks of 4 dims that are r / 2 apart (half; r / 2 is a multiple of 4) or
+// follow each other (interleaved).
 //
 // The floor is HBM's (a token is read once and written once, 28 KB at 40/8 heads: 8000 tokens 34 us at
-// the measured copy rate); what bounds the kernel is the instructions, 85 a pair of query rows, 270 a
-// pair of key rows, 350 for the angles: 8000 tokens take 49 us = 4.7 TB/s with a token on two warps (51
-// with one, 56 with four).  Where the tokens are few a token has eight warps (128 tokens 4.5 us
-// against 6.3 with two; 512 tokens 9.3 against 7.5).  What keeps the instructions few:
+// the measured copy rate); the kernel comes within 1.2 of it, 3460 instructions a token and the waits
+// for its rows: 8000 tokens take 41 us = 5.5 TB/s with a token on two warps (47 with one, 44 with
+// three, 46 with four; 49 with the partners of the half layout in another lane, reached by shuffles).
+// Where the tokens are few a token has four warps (128 tokens 4.0 us against 5.3 with two, 1024 7.2
+// against 7.8; 1280 9.8 against 8.9; eight warps are no faster at 32 tokens and slower from 256 on).
+// What keeps the instructions few:
 //   * the norm weights are folded into the lane's cosines and sines, z = r (x_i (w_i c) + x_j
 //     (-+ w_j s)), in pairs (fma.rn.f32x2);
 //   * the angle p f modulo a turn.  f / 2 pi is kept as a 64-bit fraction of a turn, so p times
@@ -52,7 +53,6 @@ struct RopeAppendParams {
 
 namespace {
 
-
 // Cache row of slot `slot` of sequence b, or -1 when its page id is out of range.
 __device__ __forceinline__ long long append_row(const RopeAppendParams &p, int b, int slot) {
   if (!p.paged) return static_cast<long long>(b) * p.max_seq + slot;
@@ -60,10 +60,6 @@ __device__ __forceinline__ long long append_row(const RopeAppendParams &p, int b
   if (pg < 0 || pg >= p.num_blocks) return -1;
   return static_cast<long long>(pg) * kTile + (slot & (kTile - 1));
 }
-
-}  // namespace
-
-namespace {
 
 // Bulk copy of this CTA's shared memory to global memory (both 16-byte aligned, a multiple of 16
 // bytes); bulk_wait returns once the thread's committed copies are complete.
@@ -114,44 +110,57 @@ __device__ __forceinline__ f2 abs_f2(f2 x) {
   return r;
 }
 
-// A lane's place in a row: dims 8 l .. 8 l + 7, as two chunks of 4.
+__device__ __forceinline__ f2 swap_f2(f2 x) {
+  float a, b;
+  split_f2(x, a, b);
+  return make_f2(b, a);
+}
+
+// A lane's 8 dims of a row, as two chunks of 4 whose partners the lane holds too: in the half layout
+// chunk l of the first elements and the one r / 2 dims on, for l < r / 8, else two chunks that do
+// not turn; in the interleaved layout, where partners are neighbours, chunks 2 l and 2 l + 1.
 template <bool kInterleaved, bool kFull>
 struct RopeLane {
-  // the half layout's partners of chunk h: words of lane from[h], its other chunk when `odd`
-  bool odd;
-  int from[2];
-  bool turns[2], first[2];
-  int pair[2];  // the chunk's first pair
+  int chunk[2], pair[2];  // and the chunk's first pair
+  bool turns[2];
 
-  __device__ __forceinline__ void init(int rotary, int l, int base) {
-    const int m = rotary / 8;  // chunks of the first elements
-    odd = !kFull && (m & 1);
+  __device__ __forceinline__ void init(int rotary, int l) {
+    const int m = kFull ? kHeadDim / 8 : rotary / 8;  // chunks of the first elements
+    const bool split = !kInterleaved && (kFull || l < m);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int c = 2 * l + h;
-      turns[h] = kFull || c < 2 * m;
-      first[h] = c < m;
-      from[h] = base + ((first[h] ? c + m : c >= m ? c - m : c) >> 1 & 15);
-      pair[h] = kInterleaved ? 2 * c : 4 * (first[h] ? c : c - m);
+      chunk[h] = split ? l + h * m : 2 * l + h;
+      turns[h] = kFull || (kInterleaved ? chunk[h] < 2 * m : split);
+      pair[h] = kInterleaved ? 2 * chunk[h] : 4 * l;
     }
   }
-  // The partners of the row's words x (bf16 pairs); zeros in chunks that do not turn, which have
-  // no sine term (and must not meet 0 x inf).
-  __device__ __forceinline__ void partners(const uint32_t (&x)[4], uint32_t (&y)[4]) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (kInterleaved) {
-          y[2 * h + e] = kFull || turns[h] ? __funnelshift_l(x[2 * h + e], x[2 * h + e], 16) : 0u;
-        } else {
-          const uint32_t o = __shfl_sync(0xffffffffu, !kFull && odd ? x[2 * (1 - h) + e] : x[2 * h + e], from[h]);
-          y[2 * h + e] = kFull || turns[h] ? o : 0u;
-        }
-      }
+  // the lane's words (bf16 pairs) of a row: of its 32 uint2 chunks
+  __device__ __forceinline__ void load(const uint2 *row, uint32_t (&w)[4]) const {
+    if (kInterleaved) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(row + chunk[0]);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+      const uint2 x = row[chunk[0]], y = row[chunk[1]];
+      w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
+    }
   }
-  __device__ __forceinline__ bool negative(int h, int e) const {  // the sign of dim 4 h + e's sine term
-    return kInterleaved ? (e & 1) == 0 : first[h];
+  __device__ __forceinline__ void store(uint2 *row, const uint32_t (&w)[4]) const {
+    if (kInterleaved) {
+      *reinterpret_cast<uint4 *>(row + chunk[0]) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      row[chunk[0]] = make_uint2(w[0], w[1]);
+      row[chunk[1]] = make_uint2(w[2], w[3]);
+    }
+  }
+  // The partners of values 2 e and 2 e + 1; zeros in chunks that do not turn, which have no sine
+  // term (and must not meet 0 x inf).
+  __device__ __forceinline__ f2 partners(const f2 (&v)[4], int e) const {
+    const f2 x = kInterleaved ? swap_f2(v[e]) : v[e ^ 2];
+    return kFull || turns[e >> 1] ? x : make_f2(0.f, 0.f);
+  }
+  // The sign of dim 4 h + e's sine term is minus.  Chunks that do not turn have it too: x - 0 is x.
+  __device__ __forceinline__ bool negative(int h, int e) const {
+    return (kInterleaved ? (e & 1) == 0 : h == 0) || !(kFull || turns[h]);
   }
   __device__ __forceinline__ int pair_of(int h, int e) const { return pair[h] + (kInterleaved ? e >> 1 : e); }
 };
@@ -197,8 +206,8 @@ __device__ __forceinline__ dw row_inv_rms(const f2 (&v)[4], float eps) {
   return fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e));
 }
 
-// Tokens up to which a CTA has eight warps, and above which two.
-constexpr int kRopeFew = 384;
+// Tokens up to which a CTA has four warps, and above which two.
+constexpr int kRopeFew = 1024;
 // A CTA holds its token's H_q + 2 H_kv rows in shared memory (256 bytes each), as the prefill prologue.
 constexpr int kRopeMaxSmem = 200 * 1024;
 // Error of a key element computed in binary32, relative to r (|x_i w_i cos| + |x_j w_j sin|), in
@@ -209,7 +218,7 @@ constexpr float kKeyWindow = 8.f * 0x1p-24f;
 }  // namespace
 
 template <bool kInterleaved, bool kFull, int kRopeWarps>
-__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 12 : 2) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 13 : 7) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
   constexpr int kRopeThreads = 32 * kRopeWarps;
   __shared__ float4 cs[kHeadDim / 2];  // m (cos_hi, sin_hi, cos_lo, sin_lo) of pair i
   __shared__ __align__(8) uint64_t arrived;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 12 : 2) rop
   const long long crow = append_row(p, b, s0 + t);
   if (crow < 0 && tid == 0) flag_error(p.err, GQA_DEVERR_PAGE);
   RopeLane<kInterleaved, kFull> l;
-  l.init(p.rotary, hl, 16 * half);
+  l.init(p.rotary, hl);
   __syncthreads();  // cos and sin, and the barrier's initialisation
   if (!__all_sync(0xffffffffu, mbar_wait(bar, 0))) {  // the rows never arrived: flag, write nothing
     if (lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
@@ -267,14 +276,13 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 12 : 2) rop
     bulk_commit();
   }
 
-  // The lane's cosines and sines with the norm weights folded in.
-  f2 A[4], S[4];
+  // The lane's cosines and sines with the norm weights folded in (w: its own weights).
+  f2 A[4], S[4], w[4];
   auto fold = [&](const uint16_t *weights) {
-    const uint4 wv = weights ? reinterpret_cast<const uint4 *>(weights)[hl]
-                             : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // ones
-    const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
-    uint32_t wp[4];
-    l.partners(w, wp);
+    uint32_t words[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};  // ones
+    if (weights) l.load(reinterpret_cast<const uint2 *>(weights), words);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = unpack_f2(words[e]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float c[2], s[2];
@@ -282,14 +290,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 12 : 2) rop
       for (int k = 0; k < 2; ++k) {
         const int h = e >> 1, d = 2 * (e & 1) + k;
         const float4 v = kFull || l.turns[h] ? cs[l.pair_of(h, d)] : make_float4(1.f, 0.f, 0.f, 0.f);
-        c[k] = v.x * (k ? bf16_hi_to_float(w[e]) : bf16_lo_to_float(w[e]));
-        s[k] = v.y * (k ? bf16_hi_to_float(wp[e]) : bf16_lo_to_float(wp[e]));
-        if (l.negative(h, d)) s[k] = -s[k];
+        c[k] = v.x;
+        s[k] = l.negative(h, d) ? -v.y : v.y;
       }
-      A[e] = make_f2(c[0], c[1]);
-      S[e] = make_f2(s[0], s[1]);
+      A[e] = mul_f2(w[e], make_f2(c[0], c[1]));
+      S[e] = mul_f2(l.partners(w, e), make_f2(s[0], s[1]));
     }
-    return wv;
   };
   // r of a row (1 where there is no norm), from its values
   auto inv_rms = [&](const f2 (&v)[4]) {
@@ -305,76 +311,70 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 12 : 2) rop
   };
 
   // Row pairs, a half warp a row: rows 2 i + half of the queries, then of the keys.
-  (void)fold(p.q_norm_w);
-  uint4 *qdst = reinterpret_cast<uint4 *>(p.q_out + tok * p.Hq * kHeadDim) + hl;
+  const uint2 *const held = reinterpret_cast<const uint2 *>(rows);  // 32 chunks of 4 dims a row
+  fold(p.q_norm_w);
+  uint2 *qdst = reinterpret_cast<uint2 *>(p.q_out + tok * p.Hq * kHeadDim);
   for (int i = warp; 2 * i < p.Hq; i += kRopeWarps) {
-    const uint4 x = rows[min(2 * i + half, p.Hq - 1) * 16 + hl];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t wp[4];
-      l.partners(w, wp);
-      f2 v[4];
+    uint32_t x[4], out[4];
+    l.load(held + min(2 * i + half, p.Hq - 1) * 32, x);
+    f2 v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = unpack_f2(w[e]);
-      const float rn = p.q_norm_w ? inv_rms(v) : 1.f;
-      const f2 rn2 = make_f2(rn, rn);
-      uint32_t out[4];
+    for (int e = 0; e < 4; ++e) v[e] = unpack_f2(x[e]);
+    const float rn = p.q_norm_w ? inv_rms(v) : 1.f;
+    const f2 rn2 = make_f2(rn, rn);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a, c;
-        split_f2(mul_f2(rn2, fma_f2(v[e], A[e], mul_f2(unpack_f2(wp[e]), S[e]))), a, c);
-        out[e] = pack_bf16(a, c);
-      }
-      if (2 * i + half < p.Hq) qdst[(2 * i + half) * (kHeadDim / 8)] = make_uint4(out[0], out[1], out[2], out[3]);
+    for (int e = 0; e < 4; ++e) {
+      float a, c;
+      split_f2(mul_f2(rn2, fma_f2(v[e], A[e], mul_f2(l.partners(v, e), S[e]))), a, c);
+      out[e] = pack_bf16(a, c);
+    }
+    if (2 * i + half < p.Hq) l.store(qdst + (2 * i + half) * 32, out);
   }
   if (crow < 0) return;
-
-  uint4 *kdst = reinterpret_cast<uint4 *>(p.k_cache + crow * p.Hkv * kHeadDim) + hl;
-  const uint4 kw = fold(p.k_norm_w);
+  uint2 *kdst = reinterpret_cast<uint2 *>(p.k_cache + crow * p.Hkv * kHeadDim);
+  fold(p.k_norm_w);
   for (int i = warp; 2 * i < p.Hkv; i += kRopeWarps) {
-    const uint4 x = rows[(p.Hq + min(2 * i + half, p.Hkv - 1)) * 16 + hl];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t wp[4];
-      l.partners(w, wp);
-      f2 v[4];
+    uint32_t x[4];
+    l.load(held + (p.Hq + min(2 * i + half, p.Hkv - 1)) * 32, x);
+    f2 v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = unpack_f2(w[e]);
-      const dw rn = p.k_norm_w ? row_inv_rms(v, p.eps) : dw{1.f, 0.f};
-      const f2 rn2 = make_f2(rn.hi, rn.hi), up = make_f2(kKeyWindow, kKeyWindow), down = make_f2(-kKeyWindow, -kKeyWindow);
-      uint32_t out[4], unsure = 0u;  // a bit per element
+    for (int e = 0; e < 4; ++e) v[e] = unpack_f2(x[e]);
+    const dw rn = p.k_norm_w ? row_inv_rms(v, p.eps) : dw{1.f, 0.f};
+    const f2 rn2 = make_f2(rn.hi, rn.hi), up = make_f2(kKeyWindow, kKeyWindow), down = make_f2(-kKeyWindow, -kKeyWindow);
+    uint32_t out[4], unsure = 0u;  // a bit per element
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f2 vp = unpack_f2(wp[e]);
-        const f2 z = mul_f2(rn2, fma_f2(v[e], A[e], mul_f2(vp, S[e])));
-        const f2 size = mul_f2(rn2, fma_f2(abs_f2(v[e]), abs_f2(A[e]), abs_f2(mul_f2(vp, S[e]))));
-        float a, c;
-        split_f2(fma_f2(size, down, z), a, c);
-        out[e] = pack_bf16(a, c);
-        split_f2(fma_f2(size, up, z), a, c);
-        const uint32_t differ = out[e] ^ pack_bf16(a, c);
-        // tiny values, whose binary32 steps are not relative, take the exact path, and so does
-        // what is not finite
-        split_f2(size, a, c);
-        if ((differ & 0xffffu) || !(a == 0.f || (a > 0x1p-80f && a < 0x1p100f))) unsure |= 1u << (2 * e);
-        if ((differ >> 16) || !(c == 0.f || (c > 0x1p-80f && c < 0x1p100f))) unsure |= 2u << (2 * e);
+    for (int e = 0; e < 4; ++e) {
+      const f2 t = mul_f2(l.partners(v, e), S[e]);
+      const f2 z = mul_f2(rn2, fma_f2(v[e], A[e], t));
+      const f2 size = mul_f2(rn2, fma_f2(abs_f2(v[e]), abs_f2(A[e]), abs_f2(t)));
+      float a, c;
+      split_f2(fma_f2(size, down, z), a, c);
+      out[e] = pack_bf16(a, c);
+      split_f2(fma_f2(size, up, z), a, c);
+      const uint32_t differ = out[e] ^ pack_bf16(a, c);
+      // tiny values, whose binary32 steps are not relative, take the exact path, and so does
+      // what is not finite
+      split_f2(size, a, c);
+      if ((differ & 0xffffu) || !(a == 0.f || (a > 0x1p-80f && a < 0x1p100f))) unsure |= 1u << (2 * e);
+      if ((differ >> 16) || !(c == 0.f || (c > 0x1p-80f && c < 0x1p100f))) unsure |= 2u << (2 * e);
+    }
+    const uint32_t any = __reduce_or_sync(0xffffffffu, unsure);
+    if (any) {  // the warp repeats those elements exactly
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (!(any >> e & 1u)) continue;
+        const int h = e >> 2, x2 = e >> 1;
+        const f2 y2 = mul_f2(v[x2], w[x2]), yp2 = mul_f2(l.partners(v, x2), l.partners(w, x2));  // exact: 8-bit significands
+        float y[2], yp[2];
+        split_f2(y2, y[0], y[1]);
+        split_f2(yp2, yp[0], yp[1]);
+        const float4 c = l.turns[h] ? cs[l.pair_of(h, e & 3)] : make_float4(1.f, 0.f, 0.f, 0.f);
+        const uint32_t z = key_element_exact(y[e & 1], l.negative(h, e & 3) ? -yp[e & 1] : yp[e & 1], c, l.turns[h], rn,
+                                             p.k_norm_w != nullptr);
+        out[x2] = e & 1 ? (out[x2] & 0xffffu) | (z << 16) : (out[x2] & 0xffff0000u) | z;
       }
-      const uint32_t any = __reduce_or_sync(0xffffffffu, unsure);
-      if (any) {  // the warp repeats those elements exactly
-        const uint32_t ww[4] = {kw.x, kw.y, kw.z, kw.w};
-        uint32_t wwp[4];
-        l.partners(ww, wwp);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!(any >> e & 1u)) continue;
-          const int h = e >> 2, x2 = e >> 1;
-          auto part = [&](uint32_t q) { return e & 1 ? bf16_hi_to_float(q) : bf16_lo_to_float(q); };
-          const float y = part(w[x2]) * part(ww[x2]), yp = part(wp[x2]) * part(wwp[x2]);  // exact: 8-bit significands
-          const float4 c = l.turns[h] ? cs[l.pair_of(h, e & 3)] : make_float4(1.f, 0.f, 0.f, 0.f);
-          const uint32_t z = key_element_exact(y, l.negative(h, e & 3) ? -yp : yp, c, l.turns[h], rn, p.k_norm_w != nullptr);
-          out[x2] = e & 1 ? (out[x2] & 0xffffu) | (z << 16) : (out[x2] & 0xffff0000u) | z;
-        }
-      }
-      const uint4 row = make_uint4(out[0], out[1], out[2], out[3]);
-      if (2 * i + half < p.Hkv) kdst[(2 * i + half) * (kHeadDim / 8)] = row;
+    }
+    if (2 * i + half < p.Hkv) l.store(kdst + (2 * i + half) * 32, out);
   }
   if (tid == 0) bulk_wait();  // the values have left shared memory and are written
 }
@@ -510,10 +510,10 @@ bool rope_configure(int device) {
            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
                cudaSuccess;
   };
-  const bool ok = raise(rope_append_kernel<true, true, 2>) && raise(rope_append_kernel<true, true, 8>) &&
-                  raise(rope_append_kernel<true, false, 2>) && raise(rope_append_kernel<true, false, 8>) &&
-                  raise(rope_append_kernel<false, true, 2>) && raise(rope_append_kernel<false, true, 8>) &&
-                  raise(rope_append_kernel<false, false, 2>) && raise(rope_append_kernel<false, false, 8>);
+  const bool ok = raise(rope_append_kernel<true, true, 2>) && raise(rope_append_kernel<true, true, 4>) &&
+                  raise(rope_append_kernel<true, false, 2>) && raise(rope_append_kernel<true, false, 4>) &&
+                  raise(rope_append_kernel<false, true, 2>) && raise(rope_append_kernel<false, true, 4>) &&
+                  raise(rope_append_kernel<false, false, 2>) && raise(rope_append_kernel<false, false, 4>);
   if (!ok) cudaGetLastError();
   if (ok && device < 64) done[device].store(true, std::memory_order_release);
   return ok;
@@ -586,16 +586,16 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   const dim3 grid(static_cast<unsigned>(d.batch) * static_cast<unsigned>(d.num_tokens));
   const long long tokens = static_cast<long long>(d.batch) * d.num_tokens;
   const bool full = p.rotary == kHeadDim, many = tokens > kRopeFew;
-  const int warps = many ? 2 : 8;
+  const int warps = many ? 2 : 4;
   const size_t smem = static_cast<size_t>(d.num_q_heads + 2 * d.num_kv_heads) * kHeadDim * 2;
   if (!rope_configure(d.device)) return GQA_ERR_CUDA;
   void (*kernel)(const RopeAppendParams);
   if (rope->layout == GQA_ROPE_INTERLEAVED)
-    kernel = full ? (many ? rope_append_kernel<true, true, 2> : rope_append_kernel<true, true, 8>)
-                  : (many ? rope_append_kernel<true, false, 2> : rope_append_kernel<true, false, 8>);
+    kernel = full ? (many ? rope_append_kernel<true, true, 2> : rope_append_kernel<true, true, 4>)
+                  : (many ? rope_append_kernel<true, false, 2> : rope_append_kernel<true, false, 4>);
   else
-    kernel = full ? (many ? rope_append_kernel<false, true, 2> : rope_append_kernel<false, true, 8>)
-                  : (many ? rope_append_kernel<false, false, 2> : rope_append_kernel<false, false, 8>);
+    kernel = full ? (many ? rope_append_kernel<false, true, 2> : rope_append_kernel<false, true, 4>)
+                  : (many ? rope_append_kernel<false, false, 2> : rope_append_kernel<false, false, 4>);
   if (launch_pdl(kernel, grid, dim3(32 * warps), smem, static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;

@@ -281,3 +281,25 @@ def test_random_geometries():
         before, norm = snapshot(d), bool(rng.integers(0, 2))
         call(d, rope, norm)
         verify(d, rope, before, norm)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("r", [8, 40, 96])
+def test_dims_that_do_not_turn_keep_their_bits(layout, r):
+    """Without a norm, z = y = x there: every finite bf16, zeros of either sign and infinities."""
+    B, T = 2, 150
+    d = setup(B, 6, 3, T, 256, True, seed=r)
+    every = np.array([x for x in range(1 << 16) if x & 0x7fff <= 0x7f80], np.uint16)   # all but NaN
+    rng = np.random.default_rng(r)
+    for name in ("q", "k"):
+        bits = as_bits(d[name]).copy()
+        bits[..., r:] = rng.choice(every, bits[..., r:].shape)
+        bits[..., -1] = 0x8000
+        d[name] = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+    call(d, binding.Rope(layout=layout, rotary_dim=r), norm=False)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(as_bits(d["out"])[..., r:], as_bits(d["q"])[..., r:])
+    for b in range(B):
+        s = int(d["start"][b])
+        kept = as_bits(d["kc"])[rows_of(d, b, np.arange(s, s + T))]
+        np.testing.assert_array_equal(kept[..., r:], as_bits(d["k"][b])[..., r:])
