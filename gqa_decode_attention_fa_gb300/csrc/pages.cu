@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kStateThreads = 1024;
 static_assert(GQA_MAX_BATCH <= kStateThreads, "a thread per sequence");
+static_assert(kStateThreads == 1024, "block_scan sums the words of 32 warps");
 constexpr int kPageList = 4096;  // free pages handed out per round
 
 __device__ __forceinline__ int pages_of(int len) { return len / kTile + (len % kTile != 0); }
@@ -172,8 +173,7 @@ __global__ void __launch_bounds__(kStateThreads) pages_resize_kernel(const PageS
   for (int j = warp; j < s.B; j += kStateThreads / 32)
     for (int c = s_need[j] + lane; c < s_have[j]; c += 32)
       atomicAdd(s.refs + s.table[static_cast<long long>(j) * s.max_blocks + c], -1);
-  __threadfence();
-  int last = -1;
+  int last = -1;  // (the barrier below orders the counts before they are read; no fence: it costs 2 us)
   if (active && want > len && len % kTile != 0) {
     last = s.table[static_cast<long long>(b) * s.max_blocks + have - 1];
     if (last < 0 || last >= s.num_blocks) last = -2;
