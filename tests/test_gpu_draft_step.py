@@ -1,6 +1,8 @@
 """A speculative decoding step end to end, as a serving loop runs it: fork, grow with
 copy-on-write, rotary append of the drafted tree, tree attention, the accepted path moved into
 place, the rest of the pages given back -- against plain decode steps of the accepted tokens."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -179,3 +181,73 @@ def test_a_captured_draft_step_replays():
         for a, b in zip(got, (q_rot, out, s.k[0], s.v[0])):
             assert torch.equal(bits(a), bits(b))
     assert int(s.err) == 0
+
+
+def test_threads_with_streams_of_their_own():
+    """Steps of several host threads at once, each with its rotary embedding, sizes and stream, give
+    the bits of the same steps one after another."""
+    ropes = [binding.Rope(theta=1e6), binding.Rope(theta=1e4, layout="interleaved", rotary_dim=64),
+             binding.Rope(theta=5e5, scaling="linear", factor=4.0), binding.Rope(rotary_dim=32, scaling="custom", freqs=np.linspace(1, 0.1, 16))]
+
+    def inputs(i):
+        s = Loop(2 + i, 256, 16 + 4 * i, seed=10 + i)
+        B, T = s.B, 3 + 2 * i
+        for x in s.k + s.v:
+            x.copy_(s.rn(*x.shape))
+        d = dict(s=s, T=T, ctx=i32([10 + 17 * b for b in range(B)]), parents=i32([[t // 2 - 1 if t else -1 for t in range(T)]] * B))
+        d["mask"] = torch.zeros(B, T, 1, dtype=torch.int64, device="cuda")
+        d["positions"] = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+        d["qkv"] = [(s.rn(B, T, Hq, D), s.rn(B, T, Hkv, D), s.rn(B, T, Hkv, D)) for _ in range(6)]
+        d["rot"], d["out"] = [s.rn(B, T, Hq, D) for _ in range(6)], [s.rn(B, T, Hq, D) for _ in range(6)]
+        d["ws"] = binding.tree_workspace(B, Hq, Hkv, T, s.cap)
+        d["keep"], d["took"] = i32([[0, 2, -1]] * B), i32([2] * B)
+        return d
+
+    def steps(i, d, stream):
+        s, T, B = d["s"], d["T"], d["s"].B
+        to = dict(device_errors=s.err, stream=stream)
+        paged = dict(block_size=64, num_cache_blocks=s.blocks)
+        binding.pages_resize(s.refs, s.table, s.lens, d["full"], s.cow[0], s.cow[1], **to)
+        for (q, k, v), rot, out in zip(d["qkv"], d["rot"], d["out"]):
+            binding.tree_prepare(d["parents"], d["ctx"], None, d["mask"], d["positions"], **to)
+            binding.rope_append(B, Hq, Hkv, T, s.cap, q, k, v, s.k[0], s.v[0], s.table, d["ctx"], d["positions"], None, s.wq, s.wk,
+                                ropes[i], EPS, rot, **paged, **to)
+            binding.tree_attn(B, Hq, Hkv, T, s.cap, rot, s.k[0], s.v[0], s.table, d["ctx"], None, d["mask"], out, workspace=d["ws"],
+                              **paged, **to)
+            binding.cache_keep_rows(s.pools, s.table, d["ctx"], d["keep"], d["took"], max_seq_len=s.cap, **to)
+
+    def results(d):
+        return [bits(x) for x in d["rot"] + d["out"] + d["s"].k + d["s"].v]
+
+    want = []
+    for i in range(4):
+        d = inputs(i)
+        d["full"] = i32([d["s"].cap] * d["s"].B)
+        steps(i, d, None)
+        torch.cuda.synchronize()
+        assert int(d["s"].err) == 0
+        want.append(results(d))
+    again = [inputs(i) for i in range(4)]
+    for d in again:
+        d["full"] = i32([d["s"].cap] * d["s"].B)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            steps(i, again[i], streams[i])
+        except Exception as e:  # a thread's own would not reach the test
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i in range(4):
+        assert int(again[i]["s"].err) == 0
+        for a, b in zip(results(again[i]), want[i]):
+            assert torch.equal(a, b)
