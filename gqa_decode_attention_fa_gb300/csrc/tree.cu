@@ -35,8 +35,9 @@
 // not kept (the last case, us): two CTAs an SM with shorter rings 297; 128-token stages with one S
 // buffer (an MMA of N = 64 takes as long as one of N = 128, but the softmax then waits for it) 312; S
 // and P in buffers of their own 297; sixteen softmax warps of 16 rows each, through the 16-lane shapes of
-// tensor memory, 283 (ragged drafts 108, the shortest call 9.7), with stages of 128 tokens 417; tiles brought to L2 by TMA prefetches 3 to 12 ahead, the second
-// pass through TMA costing more than it hides (single tokens 208 to 309).
+// tensor memory, 283 (ragged drafts 108, the shortest call 9.7), with stages of 128 tokens 417; tiles
+// brought to L2 by TMA prefetches 3 to 12 ahead, the second pass through TMA costing more than it hides
+// (single tokens 208 to 309).
 #include <math.h>
 #include <string.h>
 
