@@ -27,15 +27,15 @@
 // the output's own rounding); a softmax thread holds a row.  The maximum is raised lazily (by more
 // than 2^8), so most tiles rescale nothing.  The pipeline runs on across the pieces of a range.
 //
-// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 165 us = 6.5 TB/s, 0.96 of the
-// measured copy rate; 32 ragged drafts of up to 16 nodes 113 us, 0.80 (start, the ends of the
+// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 163 us = 6.6 TB/s, 0.97 of the
+// measured copy rate; 32 ragged drafts of up to 16 nodes 108 us, 0.84 (start, the ends of the
 // sequences, the merge).  More: the tensor core with P as hi + lo, 1.5 x the products of the
-// formula; 64 nodes on 128k tokens 270 us = 1.02 PFLOP/s of the formula's, 1.53 issued.  Small calls:
+// formula; 64 nodes on 128k tokens 265 us = 1.04 PFLOP/s of the formula's, 1.56 issued.  Small calls:
 // latency, 9 us for the shortest (2.3 us to find the range and set up, 1.7 to the first scores).  Slower and
 // not kept (the last case, us): two CTAs an SM with shorter rings 297; 128-token stages with one S
 // buffer (an MMA of N = 64 takes as long as one of N = 128, but the softmax then waits for it) 312; S
 // and P in buffers of their own 297; sixteen softmax warps of 16 rows each, through the 16-lane shapes of
-// tensor memory, 283 (ragged drafts 108, the shortest call 9.7), with stages of 128 tokens 417; tiles
+// tensor memory, 283 (ragged drafts 108 as now, the shortest call 9.7), with stages of 128 tokens 417; tiles
 // brought to L2 by TMA prefetches 3 to 12 ahead, the second pass through TMA costing more than it hides
 // (single tokens 208 to 309).
 #include <math.h>
@@ -812,28 +812,30 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // (NaN stays NaN)
         uint16_t *dst = p.out + ((static_cast<long long>(b) * p.T + t) * p.Hq + kv * p.G + g) * kHeadDim;
         float *mine = p.part + (((static_cast<long long>(w) * p.Hkv + kv) * p.R + r) * 2 + (j0 > 0 ? 0 : 1)) * kTrPartFloats;
-        const int c0 = nr == 1 ? 2 * st : 0, c1 = nr == 1 ? c0 + 2 : 4;
+        const int c0 = 2 * st;  // where streams share the rows
         const bool two = nr == 1 && j1 - j0 > 1;  // both streams have an O
-#pragma unroll 1
-        for (int c4 = c0; c4 < c1; ++c4) {
-          float o[32];
-          if (nr == 1) {
-            const uint32_t t0 = tmem + lane_base + kTrTmemO + 32 * c4;
-            const float f0 = st == 0 ? f_own : f_other, f1 = st == 0 ? f_other : f_own;
-            tmem_ld32(t0, o);
-            if (two) {
-              float o1[32];
-              tmem_ld32(t0 + kTrTmemStream, o1);
-              tmem_wait_ld();
+        // Streams that share the rows: the thread's 64 dims of both O in one go.  (The end of a piece is
+        // time that neither stream works: with the dims 32 at a time ragged drafts took 113 us.)
+        float both[2][32];
+        if (nr == 1) {
+          const uint32_t t0 = tmem + lane_base + kTrTmemO + 32 * c0;
+          const float f0 = st == 0 ? f_own : f_other, f1 = st == 0 ? f_other : f_own;
+          float o1[2][32];
+          tmem_ld32(t0, both[0]);
+          tmem_ld32(t0 + 32, both[1]);
+          if (two) {
+            tmem_ld32(t0 + kTrTmemStream, o1[0]);
+            tmem_ld32(t0 + kTrTmemStream + 32, o1[1]);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e] * f0);
-            } else {
-              tmem_wait_ld();
-            }
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) both[x][e] = fmaf(o1[x][e], f1, both[x][e] * f0);
           } else {
-            tmem_ld32(tm + kTrTmemO + 32 * c4, o);
             tmem_wait_ld();
           }
+        }
+        auto emit = [&](int c4, float (&o)[32]) {
           if (bad && valid) {
             // values of seen nodes that are not finite: p x inf for some p > 0
 #pragma unroll 1
@@ -866,6 +868,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
               for (int e = 0; e < 8; ++e) x[e] = pack_bf16(o[16 * q + 2 * e] * inv, o[16 * q + 2 * e + 1] * inv);
               store_32b(dst + 32 * c4 + 16 * q, x, p.out_wide);
             }
+          }
+        };
+        if (nr == 1) {
+          emit(c0, both[0]);
+          emit(c0 + 1, both[1]);
+        } else {
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            tmem_ld32(tm + kTrTmemO + 32 * c4, both[0]);
+            tmem_wait_ld();
+            emit(c4, both[0]);
           }
         }
         if (!walk.whole && (nr == 2 || st == 0)) {
@@ -907,7 +920,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 // the wait.
 //   Few cut sequences take 8 dims a CTA and 16 parts a chunk (8 tokens on one 4k sequence, 16 parts:
 // 16.3 us the call, against 26.6 with one part after the other), many take 32 dims and 4 parts (8 x 32k
-// single tokens, 64 joins of 3 to 4 parts: 165 us the call, against 178 with 8 dims).
+// single tokens, 64 joins of 3 to 4 parts: 163 us the call, against 178 with 8 dims).
 constexpr int kTrMergeThreads = 256;
 template <int kDims>
 __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __grid_constant__ TreeParams p) {
