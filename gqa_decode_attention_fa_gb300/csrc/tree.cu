@@ -308,6 +308,34 @@ __global__ void __launch_bounds__(GQA_MAX_TREE) tree_prepare_kernel(const int32_
 }
 
 // ------------------------------------------------------------------------------- attention
+// The values of the seen nodes u0 <= u < u1 that are not finite, which the products left out, come to
+// dims d0 .. d1 - 1 of a node's row after all: p x inf for some p > 0.  The row, which this thread has just
+// written, is the output's, scaled by inv, or column-major in the workspace.
+__device__ __noinline__ void add_nonfinite(const TreeParams &p, int b, int t, int kv, int ctx, int u0, int u1, int d0, int d1,
+                                           uint16_t *out, float *part, float inv) {
+  const uint64_t *mrow = p.mask + (static_cast<long long>(b) * p.T + t) * p.words;
+  for (int u = u0; u < u1; ++u) {
+    if (!((mrow[u >> 6] >> (u & 63)) & 1ull)) continue;
+    const int slot = ctx + u;
+    long long crow = static_cast<long long>(b) * p.max_seq + slot;
+    if (p.paged) {
+      const int pg = p.page_table[static_cast<long long>(b) * p.max_blocks + slot / kTile];
+      if (pg < 0 || pg >= p.num_blocks) continue;
+      crow = static_cast<long long>(pg) * kTile + (slot & (kTile - 1));
+    }
+    const uint16_t *v = p.v_cache + (crow * p.Hkv + kv) * kHeadDim;
+#pragma unroll 1
+    for (int d = d0; d < d1; ++d) {
+      const uint32_t y = v[d];
+      if ((y & 0x7f80u) != 0x7f80u) continue;
+      if (out)
+        out[d] = static_cast<uint16_t>(pack_bf16(bf16_lo_to_float(out[d]) + bf16_lo_to_float(y) * inv, 0.f) & 0xffffu);
+      else
+        part[d * kTrRows] += bf16_lo_to_float(y);
+    }
+  }
+}
+
 template <int NQ>
 __global__ void __launch_bounds__(kTrThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -812,75 +840,46 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // (NaN stays NaN)
         uint16_t *dst = p.out + ((static_cast<long long>(b) * p.T + t) * p.Hq + kv * p.G + g) * kHeadDim;
         float *mine = p.part + (((static_cast<long long>(w) * p.Hkv + kv) * p.R + r) * 2 + (j0 > 0 ? 0 : 1)) * kTrPartFloats;
-        const int c0 = 2 * st;  // where streams share the rows
+        // 64 dims at a time, of both O where the streams share the rows: the end of a piece is time that
+        // neither stream works (with 32 at a time ragged drafts took 113 us).
+        const int c0 = nr == 1 ? 2 * st : 0, c1 = nr == 1 ? c0 + 2 : 4;
         const bool two = nr == 1 && j1 - j0 > 1;  // both streams have an O
-        // Streams that share the rows: the thread's 64 dims of both O in one go.  (The end of a piece is
-        // time that neither stream works: with the dims 32 at a time ragged drafts took 113 us.)
-        float both[2][32];
-        if (nr == 1) {
-          const uint32_t t0 = tmem + lane_base + kTrTmemO + 32 * c0;
-          const float f0 = st == 0 ? f_own : f_other, f1 = st == 0 ? f_other : f_own;
-          float o1[2][32];
-          tmem_ld32(t0, both[0]);
-          tmem_ld32(t0 + 32, both[1]);
+        const uint32_t from = nr == 1 ? tmem + lane_base : tm;
+        const float f0 = st == 0 ? f_own : f_other, f1 = st == 0 ? f_other : f_own;
+#pragma unroll 1
+        for (int c4 = c0; c4 < c1; c4 += 2) {
+          float o[2][32];
+          tmem_ld32(from + kTrTmemO + 32 * c4, o[0]);
+          tmem_ld32(from + kTrTmemO + 32 * c4 + 32, o[1]);
           if (two) {
-            tmem_ld32(t0 + kTrTmemStream, o1[0]);
-            tmem_ld32(t0 + kTrTmemStream + 32, o1[1]);
+            float o1[2][32];
+            tmem_ld32(from + kTrTmemO + kTrTmemStream + 32 * c4, o1[0]);
+            tmem_ld32(from + kTrTmemO + kTrTmemStream + 32 * c4 + 32, o1[1]);
             tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) both[x][e] = fmaf(o1[x][e], f1, both[x][e] * f0);
+              for (int e = 0; e < 32; ++e) o[x][e] = fmaf(o1[x][e], f1, o[x][e] * f0);
           } else {
             tmem_wait_ld();
           }
-        }
-        auto emit = [&](int c4, float (&o)[32]) {
-          if (bad && valid) {
-            // values of seen nodes that are not finite: p x inf for some p > 0
-#pragma unroll 1
-            for (int u = max(0, j0 * kTile - ctx); u < min(n, j1 * kTile - ctx); ++u) {
-              if (!((mask_word(u >> 6) >> (u & 63)) & 1ull)) continue;
-              const int slot = ctx + u;
-              long long crow = static_cast<long long>(b) * p.max_seq + slot;
-              if (p.paged) {
-                const int pg = p.page_table[static_cast<long long>(b) * p.max_blocks + slot / kTile];
-                if (pg < 0 || pg >= p.num_blocks) continue;
-                crow = static_cast<long long>(pg) * kTile + (slot & (kTile - 1));
-              }
-              const uint32_t *v = reinterpret_cast<const uint32_t *>(p.v_cache + (crow * p.Hkv + kv) * kHeadDim) + 16 * c4;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t y = v[e];
-                if ((y & 0x7f80u) == 0x7f80u) o[2 * e] += bf16_lo_to_float(y);
-                if ((y & 0x7f800000u) == 0x7f800000u) o[2 * e + 1] += bf16_hi_to_float(y);
-              }
-            }
-          }
           if (!walk.whole) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mine[(32 * c4 + e) * kTrRows + row] = o[e];
+            for (int e = 0; e < 64; ++e) mine[(32 * c4 + e) * kTrRows + row] = o[e >> 5][e & 31];
           } else if (valid) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < 4; ++q) {
               uint32_t x[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = pack_bf16(o[16 * q + 2 * e] * inv, o[16 * q + 2 * e + 1] * inv);
+              for (int e = 0; e < 8; ++e)
+                x[e] = pack_bf16(o[q >> 1][16 * (q & 1) + 2 * e] * inv, o[q >> 1][16 * (q & 1) + 2 * e + 1] * inv);
               store_32b(dst + 32 * c4 + 16 * q, x, p.out_wide);
             }
           }
-        };
-        if (nr == 1) {
-          emit(c0, both[0]);
-          emit(c0 + 1, both[1]);
-        } else {
-#pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            tmem_ld32(tm + kTrTmemO + 32 * c4, both[0]);
-            tmem_wait_ld();
-            emit(c4, both[0]);
-          }
         }
+        if (bad && valid)
+          add_nonfinite(p, b, t, kv, ctx, max(0, j0 * kTile - ctx), min(n, j1 * kTile - ctx), 32 * c0, 32 * c1,
+                        walk.whole ? dst : nullptr, mine + row, inv);
         if (!walk.whole && (nr == 2 || st == 0)) {
           mine[kHeadDim * kTrRows + row] = m_run;
           mine[(kHeadDim + 1) * kTrRows + row] = l_run;
