@@ -86,7 +86,8 @@ gqa_status_t gqa_tree_workspace_bytes(const gqa_tree_desc_t *desc, size_t *bytes
  *              outside [0, T] or c_b + n_b > max_seq_len (GQA_DEVERR_SEQLEN) gives zeros in all T
  *              rows of the sequence; a page id outside the pool (GQA_DEVERR_PAGE) reads that page as zeros.
  * Keys and values that a node does not see have no effect on it whatever they hold (NaN and
- * infinities included), nor do slots from c_b + n_b on.  The rounding of the result does not
+ * infinities included), nor do slots from c_b + n_b on.  A value of the context that is not finite
+ * makes that dim of every node infinite or NaN.  The rounding of the result does not
  * depend on timing: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (as gqa_prefill_attn; also B (ceil(max_seq_len/64)
  * + 10) or B H_kv ceil(T / floor(128 / G)) above 2^31 - 1), GQA_ERR_CUDA.

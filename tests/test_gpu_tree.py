@@ -403,3 +403,43 @@ def test_output_over_the_queries_is_refused():
     ctx, mask, q = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.ones((1, 1, 1), dtype=torch.int64, device="cuda"), z(1, 1, 4, 128)
     with pytest.raises(ValueError):
         binding.tree_attn(1, 4, 1, 1, 64, q, z(64, 1, 128), z(64, 1, 128), None, ctx, None, mask, q.view(1, 1, 4, 128))
+
+
+@pytest.mark.parametrize("T", [9, 70])
+@pytest.mark.parametrize("ctx", [40, 3001])
+def test_values_that_are_not_finite_reach_the_nodes_that_see_them(ctx, T):
+    """In sequences whole to a range and in cut ones, with one row tile and with two: +inf, both
+    infinities, NaN, each in a dim of its own."""
+    w = make(1, 8, 2, T, [ctx], seed=ctx + T, slack=70)
+    before = w["out"].clone()
+    call(w)
+    verify(w, before)
+    base = w["out"].clone()
+    bits = w["mask"][0].cpu().numpy()
+    sees = lambda t, u: bool((int(bits[t, u // 64]) >> (u % 64)) & 1)  # noqa: E731
+    pairs = [(t, u, x) for t in range(T) for u in range(t) for x in range(u) if sees(t, u) and sees(t, x)]
+    node, u, x = pairs[-1]                                  # a node and two that it sees
+    row = lambda y: rows_of(w, 0, torch.tensor([ctx + y], device="cuda"))  # noqa: E731
+    w["v"][row(u), 0, 5] = float("inf")
+    w["v"][row(u), 0, 100] = float("inf")
+    w["v"][row(x), 0, 100] = float("-inf")
+    w["v"][row(u), 1, 40] = float("nan")
+    w["v"][row(x), 1, 127] = float("-inf")
+    call(w)
+    torch.cuda.synchronize()
+    for t in range(T):
+        want = base[0, t].clone()
+        first, second = want[:4], want[4:]
+        if sees(t, u):
+            first[:, 5] = float("inf")
+            first[:, 100] = float("nan") if sees(t, x) else float("inf")
+            second[:, 40] = float("nan")
+        elif sees(t, x):
+            first[:, 100] = float("-inf")
+        if sees(t, x):
+            second[:, 127] = float("-inf")
+        got = w["out"][0, t]
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan), t
+        assert torch.equal(got[~nan], want[~nan]), t
+    assert int(w["err"]) == 0
