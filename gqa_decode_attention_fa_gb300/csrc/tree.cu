@@ -73,8 +73,8 @@ constexpr int kTrStreams = 2;
 constexpr int kTrMmaWarp = 8;                // and 9: a stream's each
 constexpr int kTrProducerWarp = 10;
 constexpr int kTrThreads = 32 * 11;
-// Tensor memory: a stream's two S buffers (64 fp32 columns each; P overwrites S as bf16 pairs, hi in
-// the first 32 columns, lo in the next) and its O (128 columns).
+// Tensor memory: a stream's two S buffers (64 fp32 columns each; P overwrites S as bf16 pairs, each 32
+// keys' hi in 16 columns, their lo in the next 16) and its O (128 columns).
 constexpr uint32_t kTrTmemStream = 256;
 constexpr uint32_t kTrTmemCols = kTrStreams * kTrTmemStream;
 constexpr uint32_t kTrTmemO = 128;
@@ -250,6 +250,24 @@ __device__ __forceinline__ void store_32b(uint16_t *dst, const uint32_t (&x)[8],
     reinterpret_cast<uint4 *>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<uint4 *>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
   }
+}
+// 16 columns of the thread's row, as tmem_ld32 and tmem_st32.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -547,10 +565,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         tc_fence_after();
         const uint64_t vd = vd0 + static_cast<uint64_t>(sv * (kTrTileBytes / 16));
         const uint32_t pt = tm + 64 * pb;
-        umma_bf16_ts(tm + kTrTmemO, pt, vd, kIdO, first ? 0u : 1u);
 #pragma unroll
-        for (int k = 1; k < 2 * kTile / 16; ++k)  // hi, then lo
-          umma_bf16_ts(tm + kTrTmemO, pt + 8 * k, vd + 128 * (k % (kTile / 16)), kIdO, 1u);
+        for (int k = 0; k < 2 * kTile / 16; ++k) {  // 16 keys each: hi of all, then lo
+          const int x = k % (kTile / 16);
+          umma_bf16_ts(tm + kTrTmemO, pt + 32 * (x >> 1) + 8 * (x & 1) + 16 * (k / (kTile / 16)), vd + 128 * x, kIdO,
+                       k > 0 || !first ? 1u : 0u);
+        }
         if (NQ == 1) umma_commit(smem_addr(&v_empty[sv]));
         return true;
       };
@@ -761,37 +781,40 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             break;
           }
           tc_fence_after();
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            float o[32];
-            tmem_ld32(tm + kTrTmemO + 32 * c4, o);
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tm + kTrTmemO + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= corr;
-            tmem_st32(tm + kTrTmemO + 32 * c4, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st16(tm + kTrTmemO + c, o);
           }
         }
         // P = 2^(s - m) as bf16 hi + lo pairs into the S buffer's columns: hi the leading 8 bits of the
         // significand as they are, lo the rest rounded (to 2^-16 of the weight in all)
-        uint32_t ph[32], pl[32];
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen no key yet: P = 0
         const f2 scale2 = make_f2(p.scale_log2, p.scale_log2), neg2 = make_f2(neg_m, neg_m), minus = make_f2(-1.f, -1.f);
         f2 rs[4] = {{0}, {0}, {0}, {0}};
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float v0, v1, e0, e1;
-          split_f2(fma_f2(make_f2(sv[2 * c], sv[2 * c + 1]), scale2, neg2), v0, v1);
-          v0 = fast_exp2(v0);
-          v1 = fast_exp2(v1);
-          const f2 v = make_f2(v0, v1);
-          rs[c & 3] = add_f2(rs[c & 3], v);
-          const uint32_t h0 = __float_as_uint(v0) & 0xffff0000u, h1 = __float_as_uint(v1) & 0xffff0000u;
-          ph[c] = __byte_perm(h0, h1, 0x7632);
-          split_f2(fma_f2(make_f2(__uint_as_float(h0), __uint_as_float(h1)), minus, v), e0, e1);
-          pl[c] = pack_bf16(e0, e1);
+        for (int x = 0; x < kTile; x += 32) {  // 32 keys at a time, or the registers do not hold it all
+          uint32_t ph[16], pl[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float v0, v1, e0, e1;
+            split_f2(fma_f2(make_f2(sv[x + 2 * c], sv[x + 2 * c + 1]), scale2, neg2), v0, v1);
+            v0 = fast_exp2(v0);
+            v1 = fast_exp2(v1);
+            const f2 v = make_f2(v0, v1);
+            rs[c & 3] = add_f2(rs[c & 3], v);
+            const uint32_t h0 = __float_as_uint(v0) & 0xffff0000u, h1 = __float_as_uint(v1) & 0xffff0000u;
+            ph[c] = __byte_perm(h0, h1, 0x7632);
+            split_f2(fma_f2(make_f2(__uint_as_float(h0), __uint_as_float(h1)), minus, v), e0, e1);
+            pl[c] = pack_bf16(e0, e1);
+          }
+          tmem_st16(tm + 64 * sb + x, ph);
+          tmem_st16(tm + 64 * sb + x + 16, pl);
         }
-        tmem_st32(tm + 64 * sb, ph);
-        tmem_st32(tm + 64 * sb + 32, pl);
         float l0, l1;
         split_f2(add_f2(add_f2(rs[0], rs[1]), add_f2(rs[2], rs[3])), l0, l1);
         l_run += l0 + l1;
