@@ -27,15 +27,15 @@
 // the output's own rounding); a softmax thread holds a row.  The maximum is raised lazily (by more
 // than 2^8), so most tiles rescale nothing.  The pipeline runs on across the pieces of a range.
 //
-// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 163 us = 6.6 TB/s, 0.97 of the
-// measured copy rate; 32 ragged drafts of up to 16 nodes 108 us, 0.84 (start, the ends of the
+// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 159 us = 6.7 TB/s, 0.99 of the
+// measured copy rate; 32 ragged drafts of up to 16 nodes 104 us, 0.88 (start, the ends of the
 // sequences, the merge).  More: the tensor core with P as hi + lo, 1.5 x the products of the
-// formula; 64 nodes on 128k tokens 265 us = 1.04 PFLOP/s of the formula's, 1.56 issued.  Small calls:
-// latency, 9 us for the shortest (2.3 us to find the range and set up, 1.7 to the first scores).  Slower and
+// formula; 64 nodes on 128k tokens 263 us = 1.04 PFLOP/s of the formula's, 1.57 issued.  Small calls:
+// latency, 8 us for the shortest (2.3 us to find the range and set up, 1.7 to the first scores).  Slower and
 // not kept (the last case, us): two CTAs an SM with shorter rings 297; 128-token stages with one S
 // buffer (an MMA of N = 64 takes as long as one of N = 128, but the softmax then waits for it) 312; S
 // and P in buffers of their own 297; sixteen softmax warps of 16 rows each, through the 16-lane shapes of
-// tensor memory, 283 (ragged drafts 108 as now, the shortest call 9.7), with stages of 128 tokens 417; tiles
+// tensor memory, 283 (ragged drafts 108, the shortest call 9.7), with stages of 128 tokens 417; tiles
 // brought to L2 by TMA prefetches 3 to 12 ahead, the second pass through TMA costing more than it hides
 // (single tokens 208 to 309).
 #include <math.h>
@@ -113,13 +113,13 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
 
 // How the batch is cut.  Tiles are numbered sequence after sequence; behind each sequence with tiles
 // but the last, `gap` numbers are left out, the cost of a piece's end in tiles (the streams run
-// dry, O goes out: about 8 us), so that a range with many short sequences gets fewer tiles.  The
+// dry, O goes out: about 5 us), so that a range with many short sequences gets fewer tiles.  The
 // numbers, fewer than 2^31, go to the ranges in order, `each` to a range, one more to the first `more`.
 //   Batches of few short sequences are not cut: a range is a sequence where none is longer, in tiles,
 // than a range, the ends in it and the merge (about kTrMergeCost tiles) would cost otherwise.  (15
-// sequences of 8 tiles, 8 KV heads: 26 us cut, 17 us whole.)  The numbers are then those of the sequences.
-constexpr int kTrPieceCost = 10;
-constexpr int kTrMergeCost = 6;
+// sequences of 8 tiles, 8 KV heads: 26 us cut, 15 us whole.)  The numbers are then those of the sequences.
+constexpr int kTrPieceCost = 7;
+constexpr int kTrMergeCost = 8;
 constexpr int kTrMinTiles = 4;  // of a range, so that small batches leave few partials
 struct TreeCut {
   int ranges, gap, each, more;
@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 // the wait.
 //   Few cut sequences take 8 dims a CTA and 16 parts a chunk (8 tokens on one 4k sequence, 16 parts:
 // 16.3 us the call, against 26.6 with one part after the other), many take 32 dims and 4 parts (8 x 32k
-// single tokens, 64 joins of 3 to 4 parts: 163 us the call, against 178 with 8 dims).
+// single tokens, 64 joins of 3 to 4 parts: 159 us the call, against 178 with 8 dims).
 constexpr int kTrMergeThreads = 256;
 template <int kDims>
 __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __grid_constant__ TreeParams p) {

@@ -90,7 +90,7 @@ gqa_status_t gqa_tree_workspace_bytes(const gqa_tree_desc_t *desc, size_t *bytes
  * makes that dim of every node infinite or NaN.  The rounding of the result does not
  * depend on timing: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (as gqa_prefill_attn; also B (ceil(max_seq_len/64)
- * + 10) or B H_kv ceil(T / floor(128 / G)) above 2^31 - 1), GQA_ERR_CUDA.
+ * + 7) or B H_kv ceil(T / floor(128 / G)) above 2^31 - 1), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_tree_attn(const gqa_tree_desc_t *desc, const void *q, const void *k_cache, const void *v_cache,
                            const int32_t *page_table, const int32_t *ctx_lens, const int32_t *counts,
