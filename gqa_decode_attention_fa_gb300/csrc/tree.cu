@@ -1040,11 +1040,11 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
       const float4 f4 = *reinterpret_cast<const float4 *>(&s_f[k][4 * lane]);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        // a part with weight 0 has nothing of the row, whatever its O holds
-        if (f4.x != 0.f) A[e][0] = fmaf(f4.x, o[k][e].x, A[e][0]);
-        if (f4.y != 0.f) A[e][1] = fmaf(f4.y, o[k][e].y, A[e][1]);
-        if (f4.z != 0.f) A[e][2] = fmaf(f4.z, o[k][e].z, A[e][2]);
-        if (f4.w != 0.f) A[e][3] = fmaf(f4.w, o[k][e].w, A[e][3]);
+        // A part with weight 0 too: its O is finite, and adds nothing, unless a value that the row sees is not
+        A[e][0] = fmaf(f4.x, o[k][e].x, A[e][0]);
+        A[e][1] = fmaf(f4.y, o[k][e].y, A[e][1]);
+        A[e][2] = fmaf(f4.z, o[k][e].z, A[e][2]);
+        A[e][3] = fmaf(f4.w, o[k][e].w, A[e][3]);
       }
     }
     __syncthreads();  // before the next chunk's (m, l), and for the sums below

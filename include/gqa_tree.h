@@ -87,7 +87,8 @@ gqa_status_t gqa_tree_workspace_bytes(const gqa_tree_desc_t *desc, size_t *bytes
  *              rows of the sequence; a page id outside the pool (GQA_DEVERR_PAGE) reads that page as zeros.
  * Keys and values that a node does not see have no effect on it whatever they hold (NaN and
  * infinities included), nor do slots from c_b + n_b on.  A value of the context that is not finite
- * makes that dim of every node infinite or NaN.  The rounding of the result does not
+ * makes that dim of every node infinite or NaN, one of a node that dim of every node that sees it, however
+ * small its weight.  The rounding of the result does not
  * depend on timing: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (as gqa_prefill_attn; also B (ceil(max_seq_len/64)
  * + 7) or B H_kv ceil(T / floor(128 / G)) above 2^31 - 1), GQA_ERR_CUDA.

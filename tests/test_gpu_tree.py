@@ -443,3 +443,41 @@ def test_values_that_are_not_finite_reach_the_nodes_that_see_them(ctx, T):
         assert torch.equal(torch.isnan(got), nan), t
         assert torch.equal(got[~nan], want[~nan]), t
     assert int(w["err"]) == 0
+
+
+@pytest.mark.parametrize("T", [9, 70])
+@pytest.mark.parametrize("where", ["context", "node"])
+def test_values_that_are_not_finite_count_however_small_their_weight(T, where):
+    """A cut sequence with one row tile and with two; scores of some ranges lie 2^300 in weight below the
+    row's largest, and those hold the values: 0 x inf is NaN, so no rounding of a weight to zero
+    makes such a dim finite.  Nodes that do not see the value keep their bits."""
+    ctx = 8000
+    w = make(1, 8, 2, T, [ctx], seed=T, slack=70)
+    rows = rows_of(w, 0, torch.arange(ctx + T, device="cuda"))
+    w["q"].fill_(2.0)
+    high = slice(4000, None) if where == "context" else slice(0, 4000)
+    w["k"][rows] = (0.25 * w["k"][rows].float()).to(torch.bfloat16)
+    w["k"][rows[high]] += 10.0                              # scores of 128 x 20 / 11.3 = 226, 2^326 in weight
+    call(w)
+    o, s = reference(w, 0)
+    # scores of 226 sum 128 products of 20: binary32 is off by at most 128 2^-24 2560 / 11.3 = 0.0017
+    # in a weight, which with the rest (2^-12) stays below 2^-8
+    assert float(((w["out"][0].double() - o).abs() - 2.0 ** -8 * o.abs() - 2.0 ** -8 * s).max()) <= 0
+    base = w["out"].clone()
+    at = 100 if where == "context" else ctx + T // 2
+    seen = [where == "context" or bool((int(w["mask"][0, t, (T // 2) // 64]) >> ((T // 2) % 64)) & 1) for t in range(T)]
+    assert any(seen)
+    hit = {(0, 7): float("inf"), (0, 100): float("nan"), (1, 64): float("-inf")}
+    for (kv, d), x in hit.items():
+        w["v"][rows[at], kv, d] = x
+    call(w)
+    torch.cuda.synchronize()
+    for t in range(T):
+        touched = torch.zeros(8, D, dtype=torch.bool, device="cuda")
+        if seen[t]:
+            for kv, d in hit:
+                touched[4 * kv:4 * kv + 4, d] = True
+        got = w["out"][0, t]
+        assert torch.equal(torch.isfinite(got), ~touched), t
+        assert torch.equal(got[~touched], base[0, t][~touched]), t
+    assert int(w["err"]) == 0
