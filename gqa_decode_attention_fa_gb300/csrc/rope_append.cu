@@ -199,11 +199,16 @@ __device__ __forceinline__ dw row_inv_rms(const f2 (&v)[4], float eps) {
     ss = dw{t.hi, __fadd_rn(t.lo, __fadd_rn(ss.lo, lo))};
   }
   const dw m = dw_add(fast_two_sum(__fmul_rn(ss.hi, 1.0f / 128.0f), __fmul_rn(ss.lo, 1.0f / 128.0f)), dw{eps, 0.f});
-  const float r0 = rsqrtf(m.hi);
+  // r of m 4^-h, in [1, 4), so that no low word is subnormal (that of r0^2 would lose bits from m of 2^101 on)
+  const int h = max(-63, min(63, ((__float_as_int(m.hi) >> 23) - 127) >> 1));
+  const float scale = __int_as_float((127 - 2 * h) << 23), back = __int_as_float((127 - h) << 23);
+  const dw u = {__fmul_rn(m.hi, scale), __fmul_rn(m.lo, scale)};
+  const float r0 = rsqrtf(u.hi);
   const dw p = two_prod(r0, r0);
-  // 1 - m r0^2: m.hi p.hi is near 1, so the fma gives its difference exactly rounded
-  const float e = __fmaf_rn(-m.lo, p.hi, __fmaf_rn(-m.hi, p.lo, __fmaf_rn(-m.hi, p.hi, 1.f)));
-  return fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e));
+  // 1 - u r0^2: u.hi p.hi is near 1, so the fma gives its difference exactly rounded
+  const float e = __fmaf_rn(-u.lo, p.hi, __fmaf_rn(-u.hi, p.lo, __fmaf_rn(-u.hi, p.hi, 1.f)));
+  const dw r = fast_two_sum(r0, __fmul_rn(__fmul_rn(0.5f, r0), e));
+  return dw{__fmul_rn(r.hi, back), __fmul_rn(r.lo, back)};
 }
 
 // Tokens up to which a CTA has four warps, and above which two.

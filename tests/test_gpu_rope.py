@@ -303,3 +303,30 @@ def test_dims_that_do_not_turn_keep_their_bits(layout, r):
         s = int(d["start"][b])
         kept = as_bits(d["kc"])[rows_of(d, b, np.arange(s, s + T))]
         np.testing.assert_array_equal(kept[..., r:], as_bits(d["k"][b])[..., r:])
+
+
+def round_to_bf16(z):
+    """float64 values rounded once to bf16, ties to even, as float64."""
+    b = z.view(torch.int64)
+    return ((b + ((1 << 44) - 1) + ((b >> 45) & 1)) >> 45 << 45).view(torch.float64)
+
+
+@pytest.mark.parametrize("size", [8e17, 1e16, 1.0])
+def test_keys_of_many_rows_round_as_the_exact_value(size):
+    """10^8 key elements of normalised rows up to the largest that the norm takes, at position 0, where
+    z = r x w: a relative error of r of 2^-31 would change several of the roundings.  The 64-bit
+    value's own error is 2^-50."""
+    B, H, T = 8, 8, 4096
+    for seed in range(4):
+        d = setup(B, H, H, T, T, paged=False, seed=20 + seed)
+        d["k"] = (d["k"].float() * size).to(torch.bfloat16)
+        d["start"].zero_()
+        d["positions"] = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+        call(d, binding.Rope())
+        x = d["k"].double()
+        z = x / torch.sqrt(x.square().mean(-1, keepdim=True) + float(np.float32(1e-6))) * d["wk"].double()
+        assert bool(torch.isfinite(x.float().square().sum(-1)).all())
+        want, got = round_to_bf16(z), d["kc"].view(B, T, H, 128).double()
+        off = (got != want) & ((z - 0.5 * (got + want)).abs() > K_WINDOW * z.abs())   # (want is a midpoint's neighbour)
+        assert int(off.sum()) == 0, (int(off.sum()), float(z[off][0]), float(got[off][0]))
+    assert int(d["err"]) == 0
