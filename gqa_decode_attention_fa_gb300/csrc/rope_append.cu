@@ -174,8 +174,9 @@ __device__ __noinline__ uint32_t key_element_exact(float y, float yp, float4 c, 
 }
 
 // r = 1 / sqrt(ss / 128 + eps) of the half warp's row as a double-word, from a lane's 8 values: the squares
-// are exact in binary32 and are summed with the errors of every addition (Knuth's TwoSum, in
-// pairs), a binary32 seed takes one Newton step with its residual.
+// are exact in binary32 (those of values below 2^-67 are not, which a mean of 2^-100 and more hides) and
+// are summed with the errors of every addition (Knuth's TwoSum, in pairs), a binary32 seed takes one
+// Newton step with its residual.
 __device__ __forceinline__ dw row_inv_rms(const f2 (&v)[4], float eps) {
   f2 s = mul_f2(v[0], v[0]), err = make_f2(0.f, 0.f);
   const f2 minus = make_f2(-1.f, -1.f);

@@ -19,8 +19,11 @@
  *   z_i  = m (y_i cos a - y_j sin a),  z_j = m (y_j cos a + y_i sin a),  a = p f_i
  * for each pair (i, j) of index i, p = positions[b][t], m the magnitude; z = y in the dims
  * from r on.  z is rounded once to bf16; for keys, which stay in the cache, the rounding is
- * that of the exact value (as in the decode step); queries are computed in binary32.  A row's sum of
- * squares has to be finite in binary32 where it is normalised (|x| below about 10^18).
+ * that of the exact value (as in the decode step); queries are computed in binary32.  Where a
+ * row is normalised, mean(x^2) + eps has to lie between 2^-100 and 2^120: |x| below about 10^18, and
+ * from an eps of 10^-30 on no row is too small.  A row outside it (with a smaller eps: a zero row, or
+ * |x| below about 10^-15) gets values of no meaning, NaN and infinities among them, and no other
+ * row does.
  *
  * Conventions are those of gqa_decode.h (bf16 as 16-bit storage, row-major device tensors,
  * asynchronous on `stream`, argument errors before any launch, device-side index errors as

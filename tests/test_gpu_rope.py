@@ -330,3 +330,40 @@ def test_keys_of_many_rows_round_as_the_exact_value(size):
         off = (got != want) & ((z - 0.5 * (got + want)).abs() > K_WINDOW * z.abs())   # (want is a midpoint's neighbour)
         assert int(off.sum()) == 0, (int(off.sum()), float(z[off][0]), float(got[off][0]))
     assert int(d["err"]) == 0
+
+
+@pytest.mark.parametrize("eps,size", [(0.0, 3e-15), (0.0, 1.0), (0.0, 5e17), (1e-30, 3e-20), (1e-30, 1e-30)])
+def test_small_rows_with_little_or_no_eps(eps, size):
+    """Rows down to the least mean(x^2) + eps that the header names."""
+    d = setup(2, 8, 4, 9, 64, paged=True, seed=30)
+    for x in (d["q"], d["k"]):
+        x.copy_((x.float() * size).to(torch.bfloat16))
+    before, rope = snapshot(d), binding.Rope()
+    call(d, rope, eps=eps)
+    verify(d, rope, before, eps=eps)
+
+
+def test_rows_below_the_norms_range_reach_no_other_row():
+    """eps = 0 with zero rows and rows whose squares vanish in binary32: no other row, query, key
+    or value, and no other token is changed by them."""
+    d = setup(2, 8, 4, 9, 64, paged=True, seed=31)
+    rope = binding.Rope()
+    kc0, vc0 = d["kc"].clone(), d["vc"].clone()
+    call(d, rope, eps=0.0)
+    kc, vc, out = d["kc"].clone(), d["vc"].clone(), d["out"].clone()
+    small = [(0, 0, 0, 0.0), (0, 4, 3, 1e-23), (1, 8, 1, 1e-38), (1, 2, 2, 0.0)]
+    for b, t, h, f in small:
+        d["k"][b, t, h] = (d["k"][b, t, h].float() * f).to(torch.bfloat16)
+        d["q"][b, t, 2 * h + 1] = (d["q"][b, t, 2 * h + 1].float() * f).to(torch.bfloat16)
+    d["kc"].copy_(kc0)
+    d["vc"].copy_(vc0)
+    call(d, rope, eps=0.0)
+    start = d["start"].cpu().numpy()
+    for b, t, h, _ in small:
+        row = int(rows_of(d, b, np.array([start[b] + t]))[0])
+        kc[row, h] = d["kc"][row, h]
+        out[b, t, 2 * h + 1] = d["out"][b, t, 2 * h + 1]
+    np.testing.assert_array_equal(as_bits(d["kc"]), as_bits(kc))
+    np.testing.assert_array_equal(as_bits(d["vc"]), as_bits(vc))
+    np.testing.assert_array_equal(as_bits(d["out"]), as_bits(out))
+    assert int(d["err"]) == 0
