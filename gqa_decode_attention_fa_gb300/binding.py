@@ -456,10 +456,13 @@ def _workspace_of(*fields) -> int:
 
 
 def tree_workspace(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, max_seq_len: int, *,
-                   device: int = 0):
-    """A workspace for gqa_tree_attn calls of this geometry (any cache layout) that do not overlap."""
+                   block_size: int = 0, num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0):
+    """A workspace for gqa_tree_attn calls of this geometry that do not overlap.  Its size does not depend
+    on the cache's layout, but the limit on a cache's rows does: a page table whose batch *
+    max_seq_len passes 2^31 - 1 (a pool smaller than every sequence at full length) needs the paged layout here."""
     tt = _torch()
-    return tt.empty(tree_workspace_bytes(batch, num_q_heads, num_kv_heads, tree_len, max_seq_len, device=device),
+    return tt.empty(tree_workspace_bytes(batch, num_q_heads, num_kv_heads, tree_len, max_seq_len, block_size=block_size,
+                                         num_cache_blocks=num_cache_blocks, head_dim=head_dim, device=device),
                     dtype=tt.u8, device=f"cuda:{device}")
 
 

@@ -481,3 +481,25 @@ def test_values_that_are_not_finite_count_however_small_their_weight(T, where):
         assert torch.equal(torch.isfinite(got), ~touched), t
         assert torch.equal(got[~touched], base[0, t][~touched]), t
     assert int(w["err"]) == 0
+
+
+def test_workspace_of_a_page_table_larger_than_any_pool():
+    """batch * max_seq_len past 2^31 - 1 rows over a small pool: no contiguous cache has that size, a paged
+    one does, and a call on an explicit stream gets its workspace and runs."""
+    B, Hq, Hkv, T, cap, blocks = 80, 8, 2, 3, 1 << 25, 9
+    assert B * cap > 2 ** 31
+    with pytest.raises(binding.GqaError):
+        binding.tree_workspace(B, Hq, Hkv, T, cap)
+    ws = binding.tree_workspace(B, Hq, Hkv, T, cap, block_size=64, num_cache_blocks=blocks)
+    assert ws.numel() == binding.tree_workspace_bytes(B, Hq, Hkv, T, cap, block_size=64, num_cache_blocks=blocks)
+    small = make(B, Hq, Hkv, T, np.arange(B) % 9, seed=19)
+    assert ws.numel() >= binding.tree_workspace(B, Hq, Hkv, T, small["cap"]).numel()
+    # the first column of a table that wide: nine pages, shared by the sequences (the call only reads)
+    w = dict(small, cap=cap, blocks=blocks, ws=ws, stream=torch.cuda.Stream())
+    w["table"] = torch.full((B, cap // 64), -1, dtype=torch.int32, device="cuda")
+    w["table"][:, 0] = torch.arange(B, device="cuda") % blocks
+    w["k"], w["v"] = small["k"][:blocks * 64].contiguous(), small["v"][:blocks * 64].contiguous()
+    before = w["out"].clone()
+    torch.cuda.synchronize()
+    call(w)
+    verify(w, before)
