@@ -79,7 +79,11 @@ gqa_status_t gqa_pages_fork(const gqa_pages_desc_t *desc, int32_t *ref_counts, i
  *   new_lens [B] int32 device
  *   cow_src, cow_dst [B] int32 device   written: the pages to copy, or -1
  * If there are too few free pages, nothing changes and GQA_DEVERR_NOPAGE is set (cow_* are all -1):
- * the sequences must not be written to then, a last page that they share has not been split.  A
+ * the sequences must not be written to then, a last page that they share has not been split.  Where
+ * nobody can look at the error word in between (a captured step), seq_lens less the lengths before the
+ * call is what each sequence was granted, 0 where it could not grow: as the counts of
+ * gqa_tree_prepare, gqa_rope_append and gqa_tree_attn, and as the limit of gqa_cache_keep_rows', it
+ * keeps the step from touching a slot that the sequence has not got.  A
  * sequence whose length or new length is beyond its row (GQA_DEVERR_SEQLEN) or
  * whose table names a page outside the pool or a free one, where the call needs it
  * (GQA_DEVERR_PAGE), is left as it is.

@@ -251,3 +251,71 @@ def test_threads_with_streams_of_their_own():
         assert int(again[i]["s"].err) == 0
         for a, b in zip(results(again[i]), want[i]):
             assert torch.equal(a, b)
+
+
+def test_a_captured_step_whose_growth_fails_changes_no_page():
+    """resize -> copy -> prepare -> rope_append -> tree_attn -> keep_rows -> resize in one graph, with too few free pages
+    for one replay.  The step's counts are what the resize granted, seq_lens less the lengths before it, so
+    the page that two sequences still share is not written; with pages enough the same graph splits it."""
+    B, cap, T = 3, 256, 5
+    s = Loop(B, cap, 6, seed=30)
+    s.resize(i32([100, 0, 128]))                                            # two pages, none, two
+    binding.pages_fork(s.refs, s.table, s.lens, i32([0]), i32([1]), device_errors=s.err)
+    for x in s.k + s.v:
+        x.copy_(s.rn(*x.shape))
+    ctx, granted, took, wanted = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(4))
+    drafted, accepted = i32([T, T, T]), i32([2, 3, 1])
+    parents, keep = i32([list(range(-1, T - 1))] * B), i32([[0, 2, 4, -1, -1], [1, 2, 3, -1, -1], [4, -1, -1, -1, -1]])
+    mask, positions = torch.zeros(B, T, 1, dtype=torch.int64, device="cuda"), torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    q, k, v = s.rn(B, T, Hq, D), s.rn(B, T, Hkv, D), s.rn(B, T, Hkv, D)
+    q_rot, out = s.rn(B, T, Hq, D), s.rn(B, T, Hq, D)
+    rope, paged, err = binding.Rope(theta=THETA), dict(block_size=64, num_cache_blocks=s.blocks), dict(device_errors=s.err)
+
+    def step():
+        ctx.copy_(s.lens)
+        torch.add(ctx, drafted, out=wanted)
+        s.resize(wanted)
+        torch.sub(s.lens, ctx, out=granted)
+        torch.minimum(accepted, granted, out=took)
+        binding.tree_prepare(parents, ctx, granted, mask, positions, **err)
+        for layer in range(LAYERS):
+            binding.rope_append(B, Hq, Hkv, T, cap, q, k, v, s.k[layer], s.v[layer], s.table, ctx, positions, granted, s.wq, s.wk, rope,
+                                EPS, q_rot, **paged, **err)
+            binding.tree_attn(B, Hq, Hkv, T, cap, q_rot, s.k[layer], s.v[layer], s.table, ctx, granted, mask, out, **paged, **err)
+        binding.cache_keep_rows(s.pools, s.table, ctx, keep, took, max_seq_len=cap, **err)
+        torch.add(ctx, took, out=wanted)
+        s.resize(wanted)
+
+    state = [s.refs, s.table, s.lens, out, q_rot] + s.k + s.v
+    start = [x.clone() for x in state]
+    step()                                                                  # loads every kernel
+    for x, y in zip(state, start):
+        x.copy_(y)
+    s.err.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    # 6 pages, 4 in use; needed: one for the split of the shared page, one for the full sequence: enough
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(s.err) == 0 and s.lens.tolist() == [102, 103, 129] and granted.tolist() == [T] * 3
+    a, b = s.table[0, 1].item(), s.table[1, 1].item()
+    assert a != b and s.refs[a].item() == s.refs[b].item() == 1
+    # one free page: the growth fails as a whole
+    for x, y in zip(state, start):
+        x.copy_(y)
+    free = (s.refs == 0).nonzero().flatten()[0]
+    s.refs[free] = 1
+    before = [x.clone() for x in state]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(s.err) == binding.DEVERR_NOPAGE
+    assert granted.tolist() == [0] * 3 and took.tolist() == [0] * 3 and bool((s.cow == -1).all())
+    for x, y in zip(state, before):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    # and with the page back the same graph goes on
+    s.err.zero_()
+    s.refs[free] = 0
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(s.err) == 0 and s.lens.tolist() == [102, 103, 129]
