@@ -501,8 +501,8 @@ def tree_attn(batch: int, num_q_heads: int, num_kv_heads: int, tree_len: int, ma
 
 class CachePools:
     """The pools of a cache that share a page table (K and V of every layer; the index and scale
-    tensors of a 4-bit cache): tensors of `rows` rows, paged with num_blocks * 64 rows, else
-    contiguous.  Keeps the tensors alive."""
+    tensors of a 4-bit cache whose num_kv_heads is a multiple of 4): tensors of `rows` rows of a multiple
+    of 16 bytes, paged with num_blocks * 64 rows, else contiguous.  Keeps the tensors alive."""
 
     def __init__(self, tensors, num_blocks: int = 0, rows: int = 0):
         tensors = list(tensors)
@@ -517,6 +517,9 @@ class CachePools:
             size = t.numel() * t.element_size()
             if size == 0 or size % self.rows:
                 raise ValueError(f"pool {i}: {size} bytes are not {self.rows} rows")
+            if size // self.rows % 16 or size // self.rows > 1 << 20:
+                raise ValueError(f"pool {i}: rows of {size // self.rows} bytes; the page calls move rows of a multiple of 16, up "
+                                 "to 2^20 (the scales of a 4-bit cache: num_kv_heads a multiple of 4)")
             self.array[i] = Pool(t.data_ptr(), size // self.rows)
         spans = sorted((p.base, p.row_bytes * self.rows) for p in self.array)
         if any(a + size > b for (a, size), (b, _) in zip(spans, spans[1:])):

@@ -3,7 +3,8 @@
  * (libgqa_decode.so).
  *
  * A page is 64 token slots of every pool (the K and V pools of each layer, or the index and
- * scale pools of a 4-bit cache: all share one page table).  The state, device memory of the
+ * scale pools of a 4-bit cache with H_kv a multiple of 4, since a token's scales are 4 H_kv bytes and
+ * rows are moved 16 bytes at a time: all share one page table).  The state, device memory of the
  * caller's, is
  *   ref_counts [num_blocks] int32         how many sequences hold each page; 0 = free
  *   page_table [B, max_blocks] int32      pages of each sequence, -1 where it has none

@@ -432,3 +432,36 @@ def test_pools_that_overlap_are_refused():
     for pools in ([whole[:row], whole[:row]], [whole[16:row + 16], whole[:row]], [whole[row - 16:2 * row - 16], whole[:row]]):
         with pytest.raises(ValueError):
             binding.CachePools(pools, num_blocks=4)
+
+
+@pytest.mark.parametrize("heads", [1, 2, 3, 5, 6, 7])
+def test_pools_whose_rows_the_calls_cannot_move_are_refused_by_name(heads):
+    """A 4-bit cache's scales (4 bytes a head) where that is no multiple of 16 bytes, and rows past 2^20."""
+    blocks = 3
+    idx = torch.zeros(blocks * 64, heads, 64, dtype=torch.uint8, device="cuda")
+    scale = torch.zeros(blocks * 64, heads, dtype=torch.float32, device="cuda")
+    binding.CachePools([idx], num_blocks=blocks)
+    with pytest.raises(ValueError, match="multiple of 4"):
+        binding.CachePools([idx, scale], num_blocks=blocks)
+    with pytest.raises(ValueError, match="multiple of 16"):
+        binding.CachePools([torch.zeros(2, (1 << 20) + 16, dtype=torch.uint8, device="cuda")], rows=2)
+
+
+@pytest.mark.parametrize("heads", [4, 8, 12])
+def test_pages_of_a_4_bit_cache(heads):
+    """Indices and scales as the 4-bit decode step lays them out: pages copied, rows kept."""
+    blocks, rng = 6, np.random.default_rng(heads)
+    idx = [torch.from_numpy(rng.integers(0, 256, (blocks * 64, heads, 64), dtype=np.uint8)).cuda() for _ in range(2)]
+    scale = [torch.from_numpy(rng.random((blocks * 64, heads), dtype=np.float32)).cuda() for _ in range(2)]
+    pools = binding.CachePools(idx + scale, num_blocks=blocks)
+    want = [x.cpu().numpy().copy() for x in idx + scale]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    binding.pages_copy(pools, i32([2, -1, 0]), i32([5, -1, 1]))
+    binding.cache_keep_rows(pools, i32([[4, 3]]), i32([60]), i32([[1, 5, 9, -1]]), i32([3]), max_seq_len=128)
+    for w, x in zip(want, idx + scale):
+        w[5 * 64:], w[64:128] = w[2 * 64:3 * 64], w[:64].copy()
+        at = lambda slot: [4, 3][slot // 64] * 64 + slot % 64  # noqa: E731
+        old = w.copy()
+        for i, k in enumerate((1, 5, 9)):
+            w[at(60 + i)] = old[at(60 + k)]
+        np.testing.assert_array_equal(x.cpu().numpy(), w)
