@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeWarps == 2 ? 13 : 7) rop
   __syncthreads();  // cos and sin, and the barrier's initialisation
   if (!__all_sync(0xffffffffu, mbar_wait(bar, 0))) {  // the rows never arrived: flag, write nothing
     if (lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+    (void)mbar_wait(bar, 0);  // do not leave while copies into this CTA's shared memory may be in flight
     return;
   }
   if (tid == 0 && crow >= 0) {  // the values go to the cache as they are
