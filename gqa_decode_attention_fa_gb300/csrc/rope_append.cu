@@ -10,8 +10,12 @@
 // the measured copy rate); the kernel comes within 1.2 of it, 3460 instructions a token and the waits
 // for its rows: 8000 tokens take 41 us = 5.5 TB/s with a token on two warps (47 with one, 44 with
 // three, 46 with four; 49 with the partners of the half layout in another lane, reached by shuffles).
-// Where the tokens are few a token has four warps (128 tokens 4.0 us against 5.3 with two, 1024 7.2
-// against 7.8; 1280 9.8 against 8.9; eight warps are no faster at 32 tokens and slower from 256 on).
+// Where the tokens are few, up to 1024, a token has four warps (40/8 heads, four against two: 128 tokens 4.1 us
+// against 5.5, 1024 9.3 against 9.7; 1280 12.1 against 11.2; eight warps are no faster at 32 tokens and
+// slower from 256 on).  The crossing is the same with 8/8 heads (1024 6.1 against 5.8, 2048 11.0 against 9.4)
+// and 16/1; with 64/8 the two are close from there on (1280 14.8 against 14.0, 2048 19.2 against 21.7, 8192 57.4
+// against 58.0).  With the most rows a token four would be faster throughout (320/40, two CTAs an SM:
+// 8192 tokens 346 us against 531): the rule does not look at the heads.
 // What keeps the instructions few:
 //   * the norm weights are folded into the lane's cosines and sines, z = r (x_i (w_i c) + x_j
 //     (-+ w_j s)), in pairs (fma.rn.f32x2);
@@ -403,7 +407,7 @@ uint64_t turns_of(double f) {
   const unsigned __int128 lo = static_cast<unsigned __int128>(m) * 0x7f09d5f47d4d3770ull;
   const unsigned __int128 hi = static_cast<unsigned __int128>(m) * 0x28be60db9391054aull + (lo >> 64);
   // m c = hi 2^64 + (lo mod 2^64); shift is above 64, so the low word only rounds
-  const int s = shift - 64;             // 37 .. 126
+  const int s = shift - 64;             // 36 .. 126
   const uint64_t t = static_cast<uint64_t>(hi >> s) + static_cast<uint64_t>((hi >> (s - 1)) & 1);
   return f < 0 ? 0 - t : t;
 }

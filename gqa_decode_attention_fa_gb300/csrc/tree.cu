@@ -27,11 +27,13 @@
 // the output's own rounding); a softmax thread holds a row.  The maximum is raised lazily (by more
 // than 2^8), so most tiles rescale nothing.  The pipeline runs on across the pieces of a range.
 //
-// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 159 us = 6.7 TB/s, 0.99 of the
-// measured copy rate; 32 ragged drafts of up to 16 nodes 104 us, 0.88 (start, the ends of the
-// sequences, the merge).  More: the tensor core with P as hi + lo, 1.5 x the products of the
-// formula; 64 nodes on 128k tokens 263 us = 1.04 PFLOP/s of the formula's, 1.57 issued.  Small calls:
-// latency, 8 us for the shortest (2.3 us to find the range and set up, 1.7 to the first scores).  Slower and
+// Bounds.  One row tile: HBM (K and V once); 8 x 32k single tokens 160 us = 6.7 TB/s, 0.99 of the
+// measured copy rate; 32 ragged drafts of up to 16 nodes 105 us, 0.87 (start, the ends of the
+// sequences, the merge).  Many short sequences: their ends; 256 single tokens on 200 each 78 us, 0.41.
+// More row tiles: the tensor core with P as hi + lo, 1.5 x the products of the formula; 64 nodes on 128k
+// tokens 263 us = 1.05 PFLOP/s of the formula's, 1.57 issued, and 280 us where calls follow each other for
+// more than 5 ms or so (the card's power limit: 1.93 GHz instead of 2.07).  Small calls: latency,
+// 8 us for the shortest (2.3 us to find the range and set up, 1.7 to the first scores).  Slower and
 // not kept (the last case, us): two CTAs an SM with shorter rings 297; 128-token stages with one S
 // buffer (an MMA of N = 64 takes as long as one of N = 128, but the softmax then waits for it) 312; S
 // and P in buffers of their own 297; sixteen softmax warps of 16 rows each, through the 16-lane shapes of
@@ -112,8 +114,10 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int b) {
 }
 
 // How the batch is cut.  Tiles are numbered sequence after sequence; behind each sequence with tiles
-// but the last, `gap` numbers are left out, the cost of a piece's end in tiles (the streams run
-// dry, O goes out: about 5 us), so that a range with many short sequences gets fewer tiles.  The
+// but the last, `gap` numbers are left out, the cost of a piece's end in tiles, so that a range with many
+// short sequences gets fewer tiles.  (The streams run dry, O goes out: about 3 us of a CTA, four tiles
+// at HBM's pace.  7 counts the end of two row tiles alike, and was the faster: 32 ragged drafts 103.7 us and 64
+// sequences of 300 to 3000 tokens 80.7, against 104.7 and 82.3 with 10.)  The
 // numbers, fewer than 2^31, go to the ranges in order, `each` to a range, one more to the first `more`.
 //   Batches of few short sequences are not cut: a range is a sequence where none is longer, in tiles,
 // than a range, the ends in it and the merge (about kTrMergeCost tiles) would cost otherwise.  (15
@@ -942,7 +946,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 // the wait.
 //   Few cut sequences take 8 dims a CTA and 16 parts a chunk (8 tokens on one 4k sequence, 16 parts:
 // 16.3 us the call, against 26.6 with one part after the other), many take 32 dims and 4 parts (8 x 32k
-// single tokens, 64 joins of 3 to 4 parts: 159 us the call, against 178 with 8 dims).
+// single tokens, 64 joins of 3 to 4 parts: 160 us the call, against 178 with 8 dims).
 constexpr int kTrMergeThreads = 256;
 template <int kDims>
 __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __grid_constant__ TreeParams p) {

@@ -12,7 +12,9 @@
  *     drafted tokens needs (gqa_tree.h): siblings share a position but not a slot.
  * The cache it fills is read by gqa_tree_attn (single tokens included), and, where the
  * rotary embedding is the unscaled full-width half-split one, by the decode step and
- * prefill: the key rows are then the same bits that those append.
+ * prefill: the key rows are then the same bits that those append.  gqa_prefill_attn rotates by
+ * itself, so a prompt with another embedding attends by gqa_tree_attn, GQA_MAX_TREE tokens at a time with a
+ * chain's masks.
  *
  * For token t of sequence b, every head row x of q and k, with w its norm weights:
  *   y    = x / sqrt(mean(x^2) + eps) * w          (y = x where no weights are given)
@@ -27,8 +29,9 @@
  *
  * Conventions are those of gqa_decode.h (bf16 as 16-bit storage, row-major device tensors,
  * asynchronous on `stream`, argument errors before any launch, device-side index errors as
- * GQA_DEVERR_* bits).  Nothing is allocated and no state is kept between calls besides the
- * kernels' one-time configuration per device (make a first call before capturing a graph), so
+ * GQA_DEVERR_* bits).  Nothing is allocated.  Between calls a host thread keeps what follows from the
+ * fields of the last gqa_rope_t it used (never from a CUSTOM one, whose table is read at every
+ * call), and a device the kernels' one-time configuration (make a first call before capturing a graph);
  * calls on different streams may overlap.  The kernel is launched with programmatic stream
  * serialization but reads and writes nothing before the preceding kernel has completed,
  * and never lets the next one start early.
