@@ -372,7 +372,7 @@ gqa_status_t check_desc(const gqa_plan_desc_t &d) {
     return GQA_ERR_UNSUPPORTED;
   const bool paged = d.block_size > 0;
   if (paged && d.num_cache_blocks < 1) return GQA_ERR_INVALID_ARG;
-  const long long max_blocks = (d.max_seq_len + kTile - 1) / kTile;
+  const long long max_blocks = capacity_tiles(d.max_seq_len);
   const long long num_rows = paged ? static_cast<long long>(d.num_cache_blocks) * kTile
                                    : static_cast<long long>(d.batch) * d.max_seq_len;
   if (num_rows > 0x7fffffffLL - kTile) return GQA_ERR_UNSUPPORTED;
@@ -426,7 +426,7 @@ gqa_status_t step_layout(const gqa_plan_desc_t &d, int num_sms, StepLayout *lay)
   if (st != GQA_OK) return st;
   const bool paged = d.block_size > 0;
   const long long B = d.batch, Hkv = d.num_kv_heads;
-  const long long max_blocks = (d.max_seq_len + kTile - 1) / kTile;
+  const long long max_blocks = capacity_tiles(d.max_seq_len);
   StepLayout l;
   l.G = d.num_q_heads / d.num_kv_heads;
   l.npad = l.G <= 8 ? 8 : 16;
@@ -520,7 +520,7 @@ gqa_status_t gqa_plan_create(const gqa_plan_desc_t *desc, const int32_t *seq_len
   p->G = d.num_q_heads / d.num_kv_heads;
   p->npad = npad;
   p->num_sms = sms;
-  p->max_blocks = static_cast<int>((d.max_seq_len + kTile - 1) / kTile);
+  p->max_blocks = capacity_tiles(d.max_seq_len);
   p->num_rows = d.block_size > 0 ? static_cast<long long>(d.num_cache_blocks) * kTile
                                   : static_cast<long long>(d.batch) * d.max_seq_len;
   p->W = pc.W;

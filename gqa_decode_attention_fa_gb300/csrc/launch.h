@@ -11,6 +11,9 @@ namespace gqa {
 
 cudaError_t launch_rope_table(const RopeTableParams &p, cudaStream_t stream);
 
+// Pages, or tiles, of a sequence at full length (max_seq_len >= 1, up to 2^31 - 1): the columns of a page table.
+inline int capacity_tiles(int max_seq_len) { return (max_seq_len - 1) / kTile + 1; }
+
 // Launches `kernel`, with programmatic stream serialization when `pdl` is set (it may
 // begin while the previous kernel in the stream finishes; the kernels order themselves
 // with griddepcontrol.wait), else in plain stream order.

@@ -595,7 +595,7 @@ extern "C" gqa_status_t gqa_cache_keep_rows(const gqa_keep_desc_t *desc, const g
   p.err = device_errors;
   p.max_keep = d.max_keep;
   p.max_seq = d.max_seq_len;
-  p.max_blocks = static_cast<int>((d.max_seq_len + kTile - 1LL) / kTile);
+  p.max_blocks = capacity_tiles(d.max_seq_len);
   p.num_blocks = paged ? d.num_blocks : 0;
   p.paged = paged ? 1 : 0;
   int widest = 1, sms = 0;

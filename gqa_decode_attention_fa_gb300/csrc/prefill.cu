@@ -811,7 +811,7 @@ extern "C" gqa_status_t gqa_prefill_attn(const gqa_prefill_desc_t *desc, const v
   }
   p.paged = paged ? 1 : 0;
   p.max_seq = d.max_seq_len;
-  p.max_blocks = (d.max_seq_len + kTile - 1) / kTile;
+  p.max_blocks = capacity_tiles(d.max_seq_len);
   p.num_blocks = paged ? d.num_cache_blocks : 0;
   p.eps = eps;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(kHeadDim)));

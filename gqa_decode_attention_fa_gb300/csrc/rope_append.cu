@@ -590,7 +590,7 @@ extern "C" gqa_status_t gqa_rope_append(const gqa_rope_desc_t *desc, const void 
   p.Hkv = d.num_kv_heads;
   p.paged = paged ? 1 : 0;
   p.max_seq = d.max_seq_len;
-  p.max_blocks = static_cast<int>((d.max_seq_len + kTile - 1LL) / kTile);
+  p.max_blocks = capacity_tiles(d.max_seq_len);
   p.num_blocks = paged ? d.num_cache_blocks : 0;
   p.rotary = rope->rotary_dim;
   p.eps = eps;

@@ -1108,7 +1108,7 @@ gqa_status_t tree_check(const gqa_tree_desc_t &d) {
   if (st != GQA_OK) return st;
   if (d.tree_len > GQA_MAX_TREE) return GQA_ERR_INVALID_ARG;
   // (grid sizes, and the numbers of the batch's tiles with their gaps, are int32)
-  const long long tiles = static_cast<long long>(d.batch) * ((d.max_seq_len + kTile - 1LL) / kTile + kTrPieceCost);
+  const long long tiles = static_cast<long long>(d.batch) * (capacity_tiles(d.max_seq_len) + kTrPieceCost);
   return static_cast<long long>(d.batch) * d.num_kv_heads * tree_row_tiles(d) > 0x7fffffffLL || tiles > 0x7fffffffLL
              ? GQA_ERR_UNSUPPORTED
              : GQA_OK;
@@ -1130,7 +1130,7 @@ int tree_max_ranges(const gqa_tree_desc_t &d, int sms) {
     if (w >= 1 && 10 * w * best_rounds > 11 * best * rounds) best = w, best_rounds = rounds;
   }
   // never more than the batch at full capacity could use
-  long long most = static_cast<long long>(d.batch) * ((d.max_seq_len + kTile - 1LL) / kTile) / kTrMinTiles;
+  long long most = static_cast<long long>(d.batch) * capacity_tiles(d.max_seq_len) / kTrMinTiles;
   most = most > d.batch ? most : d.batch;
   best = best < most ? best : most;
   return static_cast<int>(best < 1 ? 1 : best);
@@ -1228,7 +1228,7 @@ extern "C" gqa_status_t gqa_tree_attn(const gqa_tree_desc_t *desc, const void *q
   p.words = (d.tree_len + 63) / 64;
   p.paged = paged ? 1 : 0;
   p.max_seq = d.max_seq_len;
-  p.max_blocks = static_cast<int>((d.max_seq_len + kTile - 1LL) / kTile);
+  p.max_blocks = capacity_tiles(d.max_seq_len);
   p.num_blocks = paged ? d.num_cache_blocks : 0;
   p.W = tree_max_ranges(d, sms);
   p.out_wide = aligned_to(out, 32) ? 1 : 0;

@@ -319,3 +319,38 @@ def test_a_captured_step_whose_growth_fails_changes_no_page():
     graph.replay()
     torch.cuda.synchronize()
     assert int(s.err) == 0 and s.lens.tolist() == [102, 103, 129]
+
+
+def test_page_tables_of_the_largest_capacity():
+    """max_seq_len = 2^31 - 1 (2^25 columns a sequence) over a small pool: every call finds the second
+    sequence's pages and gives what it gives with a table of three columns."""
+    B, T, blocks, small, large = 2, 5, 9, 192, 2 ** 31 - 1
+    narrow = i32([[4, 1, 7], [8, 0, 3]])
+    wide = torch.full((B, 2 ** 25), -1, dtype=torch.int32, device="cuda")
+    wide[:, :3] = narrow
+    ctx, counts = i32([70, 127]), i32([5, 4])
+    parents, keep, took = i32([[-1, 0, 0, 1, 2]] * B), i32([[1, 3, -1, -1, -1], [0, 2, 3, -1, -1]]), i32([2, 3])
+    mask, positions = torch.zeros(B, T, 1, dtype=torch.int64, device="cuda"), torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    binding.tree_prepare(parents, ctx, counts, mask, positions)
+    got = []
+    for cap, table in ((small, narrow), (large, wide)):
+        s = Loop(1, 64, blocks, seed=50)
+        for x in s.k + s.v:
+            x.copy_(s.rn(*x.shape))
+        q, k, v = s.rn(B, T, Hq, D), s.rn(B, T, Hkv, D), s.rn(B, T, Hkv, D)
+        rot, out, pre = s.rn(B, T, Hq, D), s.rn(B, T, Hq, D), s.rn(B, T, Hq, D)
+        paged = dict(block_size=64, num_cache_blocks=blocks, device_errors=s.err)
+        binding.prefill_attn(B, Hq, Hkv, T, cap, q, k, v, s.k[1], s.v[1], table, i32([62, 127]), s.wq, s.wk, THETA, EPS, pre, **paged)
+        binding.rope_append(B, Hq, Hkv, T, cap, q, k, v, s.k[0], s.v[0], table, ctx, positions, counts, s.wq, s.wk, binding.Rope(theta=THETA),
+                            EPS, rot, **paged)
+        binding.tree_attn(B, Hq, Hkv, T, cap, rot, s.k[0], s.v[0], table, ctx, counts, mask, out, **paged)
+        binding.cache_keep_rows(s.pools, table, ctx, keep, took, max_seq_len=cap, device_errors=s.err)
+        torch.cuda.synchronize()
+        assert int(s.err) == 0
+        got.append((out, [rot, pre] + s.k + s.v))
+    for a, b in zip(got[0][1], got[1][1]):
+        assert torch.equal(bits(a), bits(b))
+    a, b = (x[0].double() for x in got)      # the sequences may be cut otherwise: two roundings of values near each other
+    for x, y, n in zip(a, b, counts.tolist()):
+        assert float((x[:n] - y[:n]).norm() / y[:n].norm()) <= 2 * REL_L2
+        assert torch.equal(bits(x[n:].bfloat16()), bits(y[n:].bfloat16()))

@@ -244,3 +244,11 @@ def test_fields_beyond_32_bits_are_refused():
         with pytest.raises(ValueError):
             binding.tree_workspace_bytes(2, 8, 2, 4, field)
     binding._desc(binding.PagesDesc, 2, (1 << 31) - 1, 16, 0)
+
+
+def test_tree_geometry_at_the_largest_capacity():
+    """2^31 - 1 tokens a sequence over a small pool: the limit on B (ceil(max_seq_len/64) + 7) is reached at 64."""
+    big = dict(block_size=64, num_cache_blocks=1, max_seq_len=2 ** 31 - 1)
+    for batch, refused in [(64, True), (63, False)]:
+        for status in _tree(batch=batch, args=dict(ws=ODD), **big)[:1 if not refused else 2]:
+            assert (status == UNS) == refused, (batch, status)
