@@ -862,7 +862,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       tc_fence_after();
       if (warp_valid) {
         bool bad = false;
-        if (j1 * kTile > ctx)  // every softmax warp's look at V came before its P, which came before this O
+        const int o1 = (j1 - 1) * kTile - ctx + kTile;  // the node at the slot behind the piece (j1 kTile may be 2^31)
+        if (o1 > 0)  // every softmax warp's look at V came before its P, which came before this O
           bad = *reinterpret_cast<volatile uint32_t *>(&v_bad[piece & 3]) == static_cast<uint32_t>(piece + 1);
         const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // (NaN stays NaN)
         uint16_t *dst = p.out + ((static_cast<long long>(b) * p.T + t) * p.Hq + kv * p.G + g) * kHeadDim;
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
         }
         if (bad && valid)
-          add_nonfinite(p, b, t, kv, ctx, max(0, j0 * kTile - ctx), min(n, j1 * kTile - ctx), 32 * c0, 32 * c1,
+          add_nonfinite(p, b, t, kv, ctx, max(0, j0 * kTile - ctx), min(n, o1), 32 * c0, 32 * c1,
                         walk.whole ? dst : nullptr, mine + row, inv);
         if (!walk.whole && (nr == 2 || st == 0)) {
           mine[kHeadDim * kTrRows + row] = m_run;

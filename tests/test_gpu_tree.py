@@ -503,3 +503,33 @@ def test_workspace_of_a_page_table_larger_than_any_pool():
     torch.cuda.synchronize()
     call(w)
     verify(w, before)
+
+
+def test_a_context_that_ends_in_the_last_tile_of_int32():
+    """2^31 - 9 cached slots over a table that repeats three pages: the last tile ends at slot 2^31.  With
+    keys of zero every weight is alike; a node's infinity reaches those that see it and no other."""
+    T, cap = 8, 2 ** 31 - 1
+    ctx = cap - T
+    blocks = 5
+    w = make(1, 2, 1, T, [3], seed=40, parents=[[-1, 0, 0, 1, 2, 4, 4, -1]])
+    w.update(cap=cap, ctx=np.array([ctx]), ctx_d=torch.tensor([ctx], dtype=torch.int32, device="cuda"), blocks=blocks)
+    w["table"] = (torch.arange(2 ** 25, dtype=torch.int32, device="cuda") % 3)[None].contiguous()
+    w["table"][0, -1] = 4                                    # slots 2^31 - 64 on: 55 of the context, then the nodes
+    w["k"] = torch.zeros(blocks * 64, 1, D, dtype=torch.bfloat16, device="cuda")
+    w["v"] = torch.ones_like(w["k"])
+    call(w)
+    torch.cuda.synchronize()
+    base = w["out"].clone()
+    # a part's sums are whole numbers below 2^24, exact; the parts' add up to 2^31 within 152 2^-24
+    assert bool((base.float() == 1).all()) and int(w["err"]) == 0
+    row = 4 * 64 + (ctx + 2) % 64
+    w["v"][row, 0, 9] = float("inf")
+    call(w)
+    torch.cuda.synchronize()
+    sees = [bool((int(w["mask"][0, t, 0]) >> 2) & 1) for t in range(T)]
+    assert sees == [False, False, True, False, True, True, True, False]
+    for t in range(T):
+        touched = torch.zeros(2, D, dtype=torch.bool, device="cuda")
+        touched[:, 9] = sees[t]
+        assert torch.equal(torch.isfinite(w["out"][0, t]), ~touched), t
+        assert torch.equal(w["out"][0, t][~touched], base[0, t][~touched]), t
