@@ -574,7 +574,7 @@ extern "C" gqa_status_t gqa_cache_keep_rows(const gqa_keep_desc_t *desc, const g
   if (paged && d.num_blocks < 1) return GQA_ERR_INVALID_ARG;
   const long long rows = paged ? static_cast<long long>(d.num_blocks) * kTile
                                : static_cast<long long>(d.batch) * d.max_seq_len;
-  if (rows > 0x7fffffffLL) return GQA_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffffLL || d.max_keep > (1 << 30)) return GQA_ERR_UNSUPPORTED;  // (entries are counted in int32 steps)
   if (paged != (page_table != nullptr) || !start || !keep || !counts) return GQA_ERR_INVALID_ARG;
   if (!aligned_to(page_table, 4) || !aligned_to(start, 4) || !aligned_to(keep, 4) || !aligned_to(counts, 4) ||
       !aligned_to(device_errors, 4))

@@ -111,7 +111,7 @@ gqa_status_t gqa_pages_copy(const gqa_pool_t *pools, int num_pools, int num_bloc
 /* Shape of a gqa_cache_keep_rows call. */
 typedef struct gqa_keep_desc {
     int batch;       /* B, 1..GQA_MAX_BATCH */
-    int max_keep;    /* N: entries of a sequence's list (1..max_seq_len) */
+    int max_keep;    /* N: entries of a sequence's list (1..max_seq_len, at most 2^30) */
     int max_seq_len; /* per-sequence capacity in tokens (>= 1) */
     int block_size;  /* 64: paged pools; 0: contiguous pools of B * max_seq_len rows */
     int num_blocks;  /* paged: pages of each pool (>= 1); else ignored */
@@ -130,7 +130,7 @@ typedef struct gqa_keep_desc {
  * counts) or has a page outside the pool in its way (GQA_DEVERR_PAGE) moves nothing.  The slots
  * written must belong to the sequence alone (gqa_pages_resize sees to that for slots it grew).
  * Rows keep their contents: rotary positions are those they were stored with.
- * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (block_size, more than 2^31 - 1 rows), GQA_ERR_CUDA.
+ * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (block_size, more than 2^31 - 1 rows, max_keep), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_cache_keep_rows(const gqa_keep_desc_t *desc, const gqa_pool_t *pools, int num_pools,
                                  const int32_t *page_table, const int32_t *start, const int32_t *keep,

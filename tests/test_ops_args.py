@@ -252,3 +252,11 @@ def test_tree_geometry_at_the_largest_capacity():
     for batch, refused in [(64, True), (63, False)]:
         for status in _tree(batch=batch, args=dict(ws=ODD), **big)[:1 if not refused else 2]:
             assert (status == UNS) == refused, (batch, status)
+
+
+def test_keep_lists_longer_than_any_index_are_refused():
+    """Lists past 2^30 entries: the kernel counts in steps of thousands below 2^31."""
+    desc = lambda n: ctypes.byref(binding.KeepDesc(1, n, 2 ** 31 - 1, 0, 0, 0))  # noqa: E731
+    call = lambda n: binding.load().gqa_cache_keep_rows(desc(n), _pools(16), 1, None, DUMMY, DUMMY, ODD, None, None)  # noqa: E731
+    assert call((1 << 30) + 1) == UNS and call(2 ** 31 - 1) == UNS
+    assert call(1 << 30) == INV                                        # goes on to the misaligned counts
