@@ -1,5 +1,5 @@
 """Thin ctypes binding over libgqa_decode.so (include/gqa_decode.h, gqa_prefill.h, gqa_q4.h,
-gqa_rope.h, gqa_tree.h, gqa_pages.h).
+gqa_rope.h, gqa_tree.h, gqa_pages.h, gqa_q8.h).
 
 Argument marshalling only: every step of the decode path runs in the library's CUDA
 kernels.  Device tensors are torch tensors (device memory and streams come from torch);
@@ -69,6 +69,12 @@ class PagesDesc(ctypes.Structure):
 class KeepDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in (
         "batch", "max_keep", "max_seq_len", "block_size", "num_blocks", "device")]
+
+
+class Q8Desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "format", "num_tokens", "block_size", "max_seq_len",
+        "num_cache_blocks", "device", "k_stride", "v_stride")]
 
 
 class Pool(ctypes.Structure):
@@ -167,6 +173,8 @@ def load(build: bool = True):
         lib.gqa_pages_resize.argtypes = [P] * 9
         lib.gqa_pages_copy.argtypes = [P, I, I, P, P, I, I, P, P]
         lib.gqa_cache_keep_rows.argtypes = [P, P, I] + [P] * 6
+        lib.gqa_q8_append.argtypes = [P] * 12
+        lib.gqa_q8_read.argtypes = [P] * 12
         lib.gqa_status_string.argtypes = [I]
         lib.gqa_status_string.restype = ctypes.c_char_p
         for name in ("gqa_plan_create", "gqa_plan_destroy", "gqa_decode_attn", "gqa_decode_attn_host",
@@ -174,7 +182,7 @@ def load(build: bool = True):
                      "gqa_plan_device_errors", "gqa_decode_attn_static", "gqa_prefill_attn", "gqa_q4_codebook",
                      "gqa_decode_attn_q4", "gqa_rope_freqs", "gqa_rope_append", "gqa_tree_prepare",
                      "gqa_tree_workspace_bytes", "gqa_tree_attn", "gqa_pages_fork", "gqa_pages_resize",
-                     "gqa_pages_copy", "gqa_cache_keep_rows"):
+                     "gqa_pages_copy", "gqa_cache_keep_rows", "gqa_q8_append", "gqa_q8_read"):
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -304,7 +312,7 @@ def prefill_attn_workload(w, out, *, device: int = 0, device_errors=None, stream
                  num_cache_blocks=w.num_blocks, device=device, device_errors=device_errors, stream=stream)
 
 
-# ------------------------------------------------------- rotary append, draft trees, cache pages
+# ------------------------------------- rotary append, draft trees, cache pages, 8-bit caches
 
 # These calls come once a layer and step, so their wrappers keep to a few microseconds: one check
 # a tensor, and the descriptors of the geometries in use are kept (the library reads them during a
@@ -319,7 +327,8 @@ class _Torch:
     @classmethod
     def load(cls):
         import torch
-        cls.i32, cls.bf16, cls.u8 = torch.int32, torch.bfloat16, torch.uint8
+        cls.i32, cls.bf16, cls.u8, cls.f32 = torch.int32, torch.bfloat16, torch.uint8, torch.float32
+        cls.codes = {"e4m3": (torch.float8_e4m3fn, torch.uint8), "int8": (torch.int8, torch.uint8)}
         cls.word32, cls.word64 = (torch.int32, torch.uint32), (torch.int64, torch.uint64)
         cls.empty = torch.empty
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object
@@ -593,6 +602,81 @@ def cache_keep_rows(pools: CachePools, page_table, start, keep, counts, *, max_s
         _dev(start, "start", i32, (batch,), device), kp, _dev(counts, "counts", i32, (batch,), device),
         _err(device_errors, device), _on(device, stream)),
         "gqa_cache_keep_rows")
+
+
+Q8_FORMATS = {"e4m3": 0, "int8": 1}
+
+
+def _q8_cache(k_codes, v_codes, k_scale, v_scale, fmt: str, rows: int, num_kv_heads: int, device: int):
+    """Pointers of an 8-bit cache's four tensors: `rows` rows of num_kv_heads x 128 codes and num_kv_heads scales."""
+    tt = _torch()
+    if fmt not in Q8_FORMATS:
+        raise ValueError(f"fmt: one of {sorted(Q8_FORMATS)}, got {fmt!r}")
+    out = []
+    for t, name, dtype, row in ((k_codes, "k_codes", tt.codes[fmt], num_kv_heads * 128),
+                                (v_codes, "v_codes", tt.codes[fmt], num_kv_heads * 128),
+                                (k_scale, "k_scale", tt.f32, num_kv_heads), (v_scale, "v_scale", tt.f32, num_kv_heads)):
+        out.append(_dev(t, name, dtype, None, device))
+        if t.numel() != rows * row:
+            raise ValueError(f"{name}: expected {rows} rows of {row}, got shape {tuple(t.shape)}")
+    return out
+
+
+def _packed(t, name: str, tokens: int, heads: int, device: int):
+    """(pointer, stride in elements between tokens) of a packed [N, H, 128] tensor whose heads are
+    dense -- dense, or a slice of a wider projection."""
+    if t is None or t.get_device() != device or t.dtype is not _torch().bf16:
+        raise ValueError(f"{name}: expected a bfloat16 tensor on cuda:{device}")
+    if t.shape != (tokens, heads, 128):
+        raise ValueError(f"{name}: expected shape {(tokens, heads, 128)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * 128
+    st, sh, sd = t.stride()
+    if tokens == 1:
+        st = heads * 128
+    if sd != 1 or (heads > 1 and sh != 128) or st < heads * 128:
+        raise ValueError(f"{name}: heads must be dense and tokens evenly spaced, got strides {t.stride()}")
+    return t.data_ptr(), st
+
+
+def _q8_rows(call: str, batch, num_kv_heads, num_tokens, max_seq_len, k, v, names, cache, page_table, offsets, slot_start,
+             start_optional, fmt, block_size, num_cache_blocks, head_dim, device, device_errors, stream):
+    i32 = _torch().i32
+    kp, ks = _packed(k, names[0], num_tokens, num_kv_heads, device)
+    vp, vs = _packed(v, names[1], num_tokens, num_kv_heads, device)
+    rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
+    cp = _q8_cache(*cache, fmt, rows, num_kv_heads, device)
+    desc = _desc(Q8Desc, batch, 0, num_kv_heads, head_dim, Q8_FORMATS[fmt], num_tokens, block_size, max_seq_len,
+                 num_cache_blocks, device, ks, vs)
+    where = (_dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+             _dev(offsets, "offsets", i32, (batch + 1,), device, True),
+             _dev(slot_start, "slot_start", i32, (batch,), device, start_optional))
+    more = (_err(device_errors, device), _on(device, stream))
+    if call == "gqa_q8_append":
+        _check(load().gqa_q8_append(desc, kp, vp, *cp, *where, *more), call)
+    else:
+        _check(load().gqa_q8_read(desc, *cp, *where, kp, vp, *more), call)
+
+
+def q8_append(batch: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, k, v, k_codes, v_codes, k_scale, v_scale,
+              page_table, offsets, slot_start, *, fmt: str = "e4m3", block_size: int = 0, num_cache_blocks: int = 0,
+              head_dim: int = 128, device: int = 0, device_errors=None, stream=None):
+    """Quantise and store packed rows (gqa_q8_append, include/gqa_q8.h): k and v [N, H_kv, 128], the rows
+    offsets[b] .. offsets[b + 1] - 1 those of sequence b (offsets None: one row a sequence), to the slots
+    from slot_start[b] on.  fmt "e4m3" (codes float8_e4m3fn or uint8) or "int8" (int8 or uint8)."""
+    _q8_rows("gqa_q8_append", batch, num_kv_heads, num_tokens, max_seq_len, k, v, ("k", "v"),
+             (k_codes, v_codes, k_scale, v_scale), page_table, offsets, slot_start, False, fmt, block_size,
+             num_cache_blocks, head_dim, device, device_errors, stream)
+
+
+def q8_read(batch: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, k_codes, v_codes, k_scale, v_scale,
+            page_table, offsets, slot_start, k_out, v_out, *, fmt: str = "e4m3", block_size: int = 0,
+            num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0, device_errors=None, stream=None):
+    """Rows of an 8-bit cache as packed bf16 (gqa_q8_read): row offsets[b] + i of k_out and v_out [N, H_kv, 128]
+    receives slot slot_start[b] + i of sequence b (slot_start None: from slot 0 on)."""
+    _q8_rows("gqa_q8_read", batch, num_kv_heads, num_tokens, max_seq_len, k_out, v_out, ("k_out", "v_out"),
+             (k_codes, v_codes, k_scale, v_scale), page_table, offsets, slot_start, True, fmt, block_size,
+             num_cache_blocks, head_dim, device, device_errors, stream)
 
 
 def q4_codebook() -> np.ndarray:

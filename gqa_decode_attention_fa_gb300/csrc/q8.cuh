@@ -1,0 +1,55 @@
+// What the kernels over an 8-bit KV cache (include/gqa_q8.h) share: the formats, and where a
+// packed row or a slot lies.
+#pragma once
+
+#include "../../include/gqa_q8.h"
+#include <cuda_fp16.h>
+
+#include "op_args.h"
+
+namespace gqa {
+
+// Two e4m3 codes (the low 16 bits of x) as two binary16 values; exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+// Four codes, c0 in the low byte, as binary16 pairs (c0, c1) and (c2, c3); exact.  An int8 code c
+// is put, as c + 128, under the exponent of 1024: 1024 + 128 + c, less 1152.
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  if (FMT == GQA_Q8_E4M3) {
+    lo = e4m3x2_to_f16x2(x);
+    hi = e4m3x2_to_f16x2(x >> 16);
+  } else {
+    const uint32_t u = x ^ 0x80808080u;
+    lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+    hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+  }
+}
+
+// The sequence that packed row n belongs to, or -1: the last b of the batch with offsets[b] <= n, if n
+// is below offsets[b + 1] too.  Every lane of a warp calls this alike; two loads deep for up to 1024
+// sequences.
+__device__ __forceinline__ int sequence_of_row(const int32_t *offsets, int B, int n, int lane, int *first, int *end) {
+  static_assert(GQA_MAX_BATCH <= 32 * 32, "two steps of 32");
+  const int per = (B + 31) / 32;
+  const uint32_t le = __ballot_sync(0xffffffffu, lane * per < B && offsets[min(lane * per, B)] <= n);
+  if (le == 0) return -1;
+  const int base = (31 - __clz(le)) * per;
+  const int x = lane <= per && base + lane <= B ? offsets[base + lane] : 0x7fffffff;
+  const uint32_t mine = __ballot_sync(0xffffffffu, lane < per && base + lane < B && x <= n);
+  if (mine == 0) return -1;
+  const int at = 31 - __clz(mine);
+  *first = __shfl_sync(0xffffffffu, x, at);
+  *end = at < 31 ? __shfl_sync(0xffffffffu, x, at + 1) : offsets[base + 32];
+  return n < *end ? base + at : -1;
+}
+
+}  // namespace gqa
