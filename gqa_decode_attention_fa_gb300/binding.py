@@ -175,6 +175,8 @@ def load(build: bool = True):
         lib.gqa_cache_keep_rows.argtypes = [P, P, I] + [P] * 6
         lib.gqa_q8_append.argtypes = [P] * 12
         lib.gqa_q8_read.argtypes = [P] * 12
+        lib.gqa_q8_workspace_bytes.argtypes = [P, P]
+        lib.gqa_q8_attn.argtypes = [P] * 12
         lib.gqa_status_string.argtypes = [I]
         lib.gqa_status_string.restype = ctypes.c_char_p
         for name in ("gqa_plan_create", "gqa_plan_destroy", "gqa_decode_attn", "gqa_decode_attn_host",
@@ -182,7 +184,8 @@ def load(build: bool = True):
                      "gqa_plan_device_errors", "gqa_decode_attn_static", "gqa_prefill_attn", "gqa_q4_codebook",
                      "gqa_decode_attn_q4", "gqa_rope_freqs", "gqa_rope_append", "gqa_tree_prepare",
                      "gqa_tree_workspace_bytes", "gqa_tree_attn", "gqa_pages_fork", "gqa_pages_resize",
-                     "gqa_pages_copy", "gqa_cache_keep_rows", "gqa_q8_append", "gqa_q8_read"):
+                     "gqa_pages_copy", "gqa_cache_keep_rows", "gqa_q8_append", "gqa_q8_read",
+                     "gqa_q8_workspace_bytes", "gqa_q8_attn"):
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -677,6 +680,59 @@ def q8_read(batch: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, k_
     _q8_rows("gqa_q8_read", batch, num_kv_heads, num_tokens, max_seq_len, k_out, v_out, ("k_out", "v_out"),
              (k_codes, v_codes, k_scale, v_scale), page_table, offsets, slot_start, True, fmt, block_size,
              num_cache_blocks, head_dim, device, device_errors, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _q8_workspace_of(batch, num_q_heads, num_kv_heads, max_seq_len, block_size, num_cache_blocks, head_dim, device) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().gqa_q8_workspace_bytes(_desc(Q8Desc, batch, num_q_heads, num_kv_heads, head_dim, 0, 0, block_size,
+                                               max_seq_len, num_cache_blocks, device, 0, 0), ctypes.byref(n)),
+           "gqa_q8_workspace_bytes")
+    return int(n.value)
+
+
+def q8_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int, *, block_size: int = 0,
+                       num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0) -> int:
+    return _q8_workspace_of(batch, num_q_heads, num_kv_heads, max_seq_len, block_size, num_cache_blocks, head_dim, device)
+
+
+def q8_workspace(batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int, *, block_size: int = 0,
+                 num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0):
+    """A workspace for gqa_q8_attn calls of this geometry that do not overlap."""
+    tt = _torch()
+    return tt.empty(q8_workspace_bytes(batch, num_q_heads, num_kv_heads, max_seq_len, block_size=block_size,
+                                       num_cache_blocks=num_cache_blocks, head_dim=head_dim, device=device),
+                    dtype=tt.u8, device=f"cuda:{device}")
+
+
+def q8_attn(batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int, q, k_codes, v_codes, k_scale, v_scale,
+            page_table, seq_lens, out, *, fmt: str = "e4m3", block_size: int = 0, num_cache_blocks: int = 0,
+            head_dim: int = 128, workspace=None, device: int = 0, device_errors=None, stream=None):
+    """Attention of one new token a sequence over an 8-bit cache (gqa_q8_attn, include/gqa_q8.h): q and out [B, H_q,
+    128], slots 0 .. seq_lens[b] - 1.  ``workspace``: a uint8 tensor of q8_workspace_bytes; None takes one from torch's
+    allocator for this call (which knows the current stream only: give one with an explicit ``stream``)."""
+    tt = _torch()
+    i32 = tt.i32
+    rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
+    need = _q8_workspace_of(batch, num_q_heads, num_kv_heads, max_seq_len, block_size, num_cache_blocks, head_dim, device)
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("a call on an explicit stream needs a workspace")
+        workspace = tt.empty(need, dtype=tt.u8, device=f"cuda:{device}")
+    ws = _dev(workspace, "workspace", tt.u8, None, device)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace: {need} bytes needed, got {workspace.numel()}")
+    shape = (batch, num_q_heads, 128)
+    qp, op = _dev(q, "q", tt.bf16, shape, device), _dev(out, "out", tt.bf16, shape, device)
+    if qp == op:
+        raise ValueError("out: must not be q, which other CTAs still read")
+    cp = _q8_cache(k_codes, v_codes, k_scale, v_scale, fmt, rows, num_kv_heads, device)
+    _check(load().gqa_q8_attn(
+        _desc(Q8Desc, batch, num_q_heads, num_kv_heads, head_dim, Q8_FORMATS[fmt], 0, block_size, max_seq_len,
+              num_cache_blocks, device, 0, 0), qp, *cp,
+        _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+        _dev(seq_lens, "seq_lens", i32, (batch,), device), op, ws, _err(device_errors, device), _on(device, stream)),
+        "gqa_q8_attn")
 
 
 def q4_codebook() -> np.ndarray:

@@ -9,6 +9,9 @@
 
 namespace gqa {
 
+// Geometry and format checks of a call (q8_rows.cu).
+gqa_status_t q8_check(const gqa_q8_desc_t &d, bool attn);
+
 // Two e4m3 codes (the low 16 bits of x) as two binary16 values; exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
   uint32_t y;

@@ -1,0 +1,756 @@
+// Attention of one new token a sequence over an 8-bit KV cache (include/gqa_q8.h).
+//
+// out = sum_j p_j vs_j vc_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = (q . kc_j) ks_j log2(e) / sqrt(128).
+//
+// Work.  The batch's tokens, in units of 16, sequence after sequence, are cut into W ranges of equal
+// cost whatever the sequence boundaries; the lengths are read on the device.  A CTA streams a range for
+// `hg` neighbouring KV heads: its eight warps take a head each, or share a head's units in turn.  A piece
+// of a range that is a whole sequence writes its output rows, one that is cut leaves its normalised
+// output and log-sum in the workspace for q8_merge_kernel.
+//
+// A warp works alone between the ends of its pieces: a ring of stages of its own in shared memory, filled by
+// asynchronous 16-byte copies (16 tokens of K, of V and their scales a stage; rows in 16-byte chunks permuted by
+// chunk ^ (row mod 8), so that no load below meets a bank conflict; what lies beyond the
+// sequence is filled with zeros), and mma.sync with the G query heads as the N of both products, S^T = K q^T and
+// O^T += V^T P^T.  The codes become binary16 exactly (two to a conversion); the order of the 128 dims in a
+// product is free, so a lane takes 32 neighbouring bytes of a K row, and of V rows 16 neighbouring dims
+// of its four tokens.
+//   q is scaled to binary16's range by a power of two a row (exact but for elements 2^-29 below the
+// largest).  The scale of K multiplies the score, that of V the weight: x = p vs 2^(m - E), rounded to
+// binary16 (2^-12 of each weight, where the output's own rounding is 2^-9) under a power of two 2^E of its own
+// that follows the largest weight seen, so that neither p nor the scale can pass binary16's range: weights down
+// to 2^-22 of the largest keep 11 bits, those below 2^-32 are lost.  The maximum m is raised lazily, where a score
+// passes it by 8; sums are binary32.
+#include <math.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "q8.cuh"
+
+namespace gqa {
+
+struct Q8AttnParams {
+  const uint16_t *q;
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  const int32_t *page_table, *seq_lens;
+  uint16_t *out;
+  float *part;  // [W][Hkv][2] (G x 128 outputs, G log-sums) of cut pieces
+  uint32_t *err;
+  int B, Hq, Hkv, G;
+  int hg;       // KV heads of a CTA
+  int paged, max_seq, max_blocks, num_blocks;
+  int W;        // ranges the grid is sized for
+  int whole;    // a range is a sequence, W = B
+  int merge_by_sequence;
+  float scale_log2;
+};
+
+namespace {
+
+constexpr int kQaWarps = 8;
+constexpr int kQaThreads = 32 * kQaWarps;
+constexpr int kQaUnit = 16;                              // tokens of a stage
+constexpr int kQaStageBytes = 2 * kQaUnit * 128 + 2 * kQaUnit * 4;  // K, V, scales of K, of V
+constexpr int kQaMaxRanges = 640;
+constexpr float kQaRaise = 8.f;     // log2: how far a score may pass m
+constexpr float kQaMostLog2 = 14.f; // of x (binary16 holds 65504)
+constexpr float kQaFreshLog2 = 8.f; // of the largest x when E is set
+
+template <int NT>
+struct Q8Smem {
+  static constexpr int kStages = NT == 1 ? 3 : 6;
+  static constexpr int kRing = kQaWarps * kStages * kQaStageBytes;
+  static constexpr int kRow = kHeadDim + 4;  // floats of a head's row in the merge
+  static constexpr int kMerge = kQaWarps * 8 * NT * (kRow + 2) * 4;
+  static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
+};
+
+__device__ __forceinline__ int q8_units(const Q8AttnParams &p, int b) {
+  const int n = p.seq_lens[b];
+  return n > 0 && n <= p.max_seq ? (n - 1) / kQaUnit + 1 : 0;
+}
+
+// How the batch is cut: as for draft trees (tree.cu), in units of 16 tokens.  Behind each sequence but the
+// last `gap` numbers are left out, the cost of a piece's end.
+struct Q8Cut {
+  int ranges, gap, each, more;
+  bool whole;
+  int lane_first;
+
+  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int range_of(int x) const {
+    const int wide = (each + 1) * more;
+    return x < wide ? x / (each + 1) : more + (x - wide) / each;
+  }
+};
+__device__ __forceinline__ Q8Cut q8_cut(const Q8AttnParams &p, int lane) {
+  const int per = (p.B + 31) / 32, b0 = lane * per, b1 = min(p.B, b0 + per);
+  int units = 0, seqs = 0, longest = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = q8_units(p, b);
+    units += n;
+    seqs += n > 0;
+    longest = max(longest, n);
+  }
+  const int own_units = units, own_seqs = seqs;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, units, o), z = __shfl_up_sync(0xffffffffu, seqs, o);
+    if (lane >= o) units += y, seqs += z;
+  }
+  const int all = __shfl_sync(0xffffffffu, units, 31), all_seqs = __shfl_sync(0xffffffffu, seqs, 31);
+  longest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(longest)));
+  const int wph = kQaWarps / p.hg;  // a warp's unit is 1 / wph of a range's
+  Q8Cut c;
+  c.ranges = all < 1 ? 0 : max(1, min(p.W, all / (2 * wph)));
+  const int quarter = c.ranges > 0 ? all / c.ranges / 4 : 0;
+  c.gap = min(quarter, wph);
+  c.whole = c.ranges > 0 && all_seqs <= p.W && longest <= all / c.ranges + c.gap * all_seqs / c.ranges + 2 * wph;
+  if (c.whole) c.ranges = all_seqs;
+  const int total = c.whole ? all_seqs : all + c.gap * max(0, all_seqs - 1);
+  c.each = c.ranges > 0 ? total / c.ranges : 0;
+  c.more = total - c.each * c.ranges;
+  c.lane_first = c.whole ? seqs - own_seqs : units - own_units + c.gap * (seqs - own_seqs);
+  return c;
+}
+__device__ __forceinline__ int q8_span(const Q8AttnParams &p, const Q8Cut &c, int b) {
+  const int n = q8_units(p, b);
+  return n < 1 ? 0 : c.whole ? 1 : n + c.gap;
+}
+// The sequence whose numbers (or the gap behind them) hold `at`, below their end, and its first number.
+__device__ __forceinline__ void q8_find(const Q8AttnParams &p, const Q8Cut &c, int at, int *b, int *seq0) {
+  const uint32_t le = __ballot_sync(0xffffffffu, c.lane_first <= at);
+  const int owner = 31 - __clz(le);
+  const int per = (p.B + 31) / 32;
+  int s = __shfl_sync(0xffffffffu, c.lane_first, owner);
+  int x = owner * per;
+  while (x + 1 < p.B) {
+    const int nxt = s + q8_span(p, c, x);
+    if (nxt > at) break;
+    s = nxt;
+    ++x;
+  }
+  *b = x;
+  *seq0 = s;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+// D = A(16x16, row) * B(16x8, col) + D, binary16 inputs, binary32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }  // -126 .. 127
+__device__ __forceinline__ uint32_t word(const uint4 &x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
+
+// Largest over the lanes of the same t (lane = 4 g + t).
+__device__ __forceinline__ float max_over_g(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+}  // namespace
+
+// NT: the heads of a KV head in eights.
+template <int FMT, int NT>
+__global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
+  using Smem = Q8Smem<NT>;
+  constexpr int kStages = Smem::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int groups = p.Hkv / p.hg, wph = kQaWarps / p.hg;
+  const int w = static_cast<int>(blockIdx.x) / groups, h0 = (static_cast<int>(blockIdx.x) - w * groups) * p.hg;
+  const int hl = warp % p.hg, share = warp / p.hg, kv = h0 + hl;
+
+  griddep_wait();
+  if (!p.whole && p.W > 1) griddep_launch_dependents();  // q8_merge_kernel follows, and it waits
+
+  for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x)) {  // sequences without tokens
+    const int n = p.seq_lens[b];
+    if (n > 0 && n <= p.max_seq) continue;
+    if (n != 0 && tid == 0) flag_error(p.err, GQA_DEVERR_SEQLEN);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + static_cast<long long>(b) * p.Hq * kHeadDim);
+    for (int c = tid; c < p.Hq * (kHeadDim / 8); c += kQaThreads) dst[c] = make_uint4(0, 0, 0, 0);
+  }
+
+  int pos, end, b, seq0, gap = 0;  // numbers of the range still to do; the sequence at hand and its first number
+  if (p.whole) {
+    b = w;
+    pos = seq0 = 0;
+    end = q8_units(p, b);
+  } else {
+    const Q8Cut cut = q8_cut(p, lane);
+    pos = end = b = seq0 = 0;
+    gap = cut.gap;
+    if (w < cut.ranges) {
+      pos = cut.begin(w);
+      end = cut.begin(w + 1);
+      q8_find(p, cut, pos, &b, &seq0);
+      if (cut.whole) pos = seq0 = 0, end = q8_units(p, b);
+    }
+  }
+
+  const uint32_t ring = smem_addr(smem_raw) + warp * kStages * kQaStageBytes;
+  const int cp_row = lane >> 3, cp_chunk = lane & 7;
+  const long long row_bytes = static_cast<long long>(p.Hkv) * kHeadDim;
+  const uint8_t *const k_lane = p.k_codes + (static_cast<long long>(cp_row) * p.Hkv + kv) * kHeadDim + 16 * cp_chunk;
+  const uint8_t *const v_lane = p.v_codes + (static_cast<long long>(cp_row) * p.Hkv + kv) * kHeadDim + 16 * cp_chunk;
+  const float *const s_lane = (lane < 16 ? p.k_scale : p.v_scale) + static_cast<long long>(lane & 15) * p.Hkv + kv;
+  const uint32_t cp_dst0 = cp_row * 128 + ((cp_chunk ^ cp_row) << 4);        // rows cp_row and cp_row + 8
+  const uint32_t cp_dst1 = cp_row * 128 + 512 + ((cp_chunk ^ (cp_row + 4)) << 4);  // cp_row + 4 and + 12
+
+  while (pos < end) {
+    int n = p.seq_lens[b], nu = q8_units(p, b);
+    while (pos >= seq0 + nu) {  // on to the next sequence
+      seq0 += nu > 0 ? nu + gap : 0;
+      if (pos < seq0) pos = seq0;
+      if (pos >= end) break;
+      ++b;
+      n = p.seq_lens[b];
+      nu = q8_units(p, b);
+    }
+    if (pos >= end) break;
+    const int j0 = pos - seq0, j1 = min(nu, j0 + end - pos);
+    pos += j1 - j0;
+
+    // ------------------------------------------------------------- the queries, as B of the first product
+    uint32_t qf[NT][8][2];
+    float qs1[NT][2], qs2[NT][2];  // of heads 2t, 2t + 1: together 2^-shift log2(e) / sqrt(128)
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      const int head = 8 * x + g;
+      uint4 r[4];
+      const uint16_t *src = p.q + (static_cast<long long>(b) * p.Hq + kv * p.G + head) * kHeadDim + 32 * t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = head < p.G ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+      uint32_t most = 0;  // the largest finite |q|, as bf16 bits
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t y = word(r[i >> 2], i & 3), lo = y & 0x7fffu, hi = (y >> 16) & 0x7fffu;
+        most = max(most, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const int shift = most == 0 ? 0 : 14 - (static_cast<int>(most >> 7) - 127);
+      const int h1 = shift >> 1, h2 = shift - h1;
+      const float f1 = power_of_two(h1), f2 = power_of_two(h2);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t y = word(r[i >> 2], i & 3);
+        qf[x][i >> 1][i & 1] = pack_f16(bf16_lo_to_float(y) * f1 * f2, bf16_hi_to_float(y) * f1 * f2);
+      }
+      const float a1 = power_of_two(-h1) * p.scale_log2, a2 = power_of_two(-h2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qs1[x][e] = __shfl_sync(0xffffffffu, a1, (2 * t + e) * 4);
+        qs2[x][e] = __shfl_sync(0xffffffffu, a2, (2 * t + e) * 4);
+      }
+    }
+
+    // ------------------------------------------------------------- copies
+    int pg_base = -1, pg = 0;  // the lane's page id among 32 from pg_base on
+    auto issue = [&](int j, int stage) {
+      if (j < j1) {
+        const int tok = j * kQaUnit;
+        long long crow;
+        bool there = true;
+        if (p.paged) {
+          const int page = tok / kTile;
+          if (pg_base < 0 || page >= pg_base + 32) {
+            pg_base = page;
+            const int at = page + lane;
+            pg = at <= (n - 1) / kTile ? p.page_table[static_cast<long long>(b) * p.max_blocks + at] : 0;
+            if (pg < 0 || pg >= p.num_blocks) {
+              flag_error(p.err, GQA_DEVERR_PAGE);
+              pg = -1;
+            }
+          }
+          const int id = __shfl_sync(0xffffffffu, pg, page - pg_base);
+          there = id >= 0;
+          crow = (there ? static_cast<long long>(id) * kTile : 0) + (tok & (kTile - 1));
+        } else {
+          crow = static_cast<long long>(b) * p.max_seq + tok;
+        }
+        const int left = there ? n - tok : 0;  // tokens of the unit that there are
+        const uint32_t st = ring + stage * kQaStageBytes;
+        const long long at = crow * row_bytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = cp_row + 4 * i < left;
+          const long long from = in ? at + 4 * i * row_bytes : -static_cast<long long>(cp_row) * row_bytes;
+          const uint32_t dst = st + (i & 1 ? cp_dst1 : cp_dst0) + (i >> 1) * 1024;
+          cp_async16(dst, k_lane + from, in ? 16u : 0u);
+          cp_async16(dst + kQaUnit * 128, v_lane + from, in ? 16u : 0u);
+        }
+        const bool in = (lane & 15) < left;
+        cp_async4(st + 2 * kQaUnit * 128 + 4 * lane,
+                  s_lane + (in ? crow * p.Hkv : -static_cast<long long>(lane & 15) * p.Hkv), in ? 4u : 0u);
+      }
+      cp_async_commit();
+    };
+
+    float o[8][NT][4], m[NT][2], l[NT][2], ex[NT][2], lim[NT][2], wt[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][x][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[x][e] = ex[x][e] = -INFINITY;  // ex: E
+        l[x][e] = lim[x][e] = wt[x][e] = 0.f;  // lim: 2^(14 + E - m), wt: 2^((m - E) / 2)
+      }
+    }
+    auto follow = [&](int x, int e) {  // lim and wt after m or E has changed
+      const float d = m[x][e] - ex[x][e];
+      const bool none = ex[x][e] == -INFINITY;
+      lim[x][e] = none ? 0.f : fast_exp2(kQaMostLog2 - d);
+      wt[x][e] = none ? 0.f : fast_exp2(0.5f * d);
+    };
+
+    int jl = j0 + share;
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s, jl += wph) issue(jl, s);
+    int stage = 0;
+    for (int j = j0 + share; j < j1; j += wph) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      issue(jl, stage == 0 ? kStages - 1 : stage - 1);  // the stage read last
+      jl += wph;
+      const uint32_t st = ring + stage * kQaStageBytes;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+
+      float acc[NT][4];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a = st + g * 128 + (((2 * t + i) ^ g) << 4);
+        const uint4 ka = lds128(a), kb = lds128(a + 1024);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16<FMT>(word(ka, c), a0, a2);
+          codes_to_f16<FMT>(word(kb, c), a1, a3);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) mma_f16(acc[x], a0, a1, a2, a3, qf[x][4 * i + c][0], qf[x][4 * i + c][1]);
+        }
+      }
+      const uint32_t sc = st + 2 * kQaUnit * 128 + 4 * g;
+      const float ks[2] = {lds_f32(sc), lds_f32(sc + 32)}, vs[2] = {lds_f32(sc + 64), lds_f32(sc + 96)};
+      const int left = n - j * kQaUnit;
+      const bool in[2] = {g < left, g + 8 < left};
+
+      bool raise = false;
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float s = acc[x][e] * qs1[x][e & 1] * ks[e >> 1] * qs2[x][e & 1];
+          acc[x][e] = in[e >> 1] ? s : -INFINITY;
+          raise |= acc[x][e] > m[x][e & 1] + kQaRaise;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mx = fmaxf(m[x][e], max_over_g(fmaxf(acc[x][e], acc[x][e + 2])));
+            if (mx > m[x][e] + kQaRaise) {  // (a head's result does not depend on the others)
+              l[x][e] *= fast_exp2(m[x][e] - mx);
+              m[x][e] = mx;
+              follow(x, e);
+            }
+          }
+      }
+      float y[NT][4];
+      raise = false;
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mm = m[x][e & 1] == -INFINITY ? 0.f : m[x][e & 1];
+          const float pr = fast_exp2(acc[x][e] - mm);
+          l[x][e & 1] += pr;
+          y[x][e] = pr * vs[e >> 1];
+          raise |= fabsf(y[x][e]) > lim[x][e & 1];
+          acc[x][e] = pr;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float most = max_over_g(fmaxf(fabsf(y[x][e]), fabsf(y[x][e + 2])));
+            if (most > lim[x][e] && most < INFINITY) {
+              // E to the nearest power of two at which the largest x is about 2^8
+              const float fresh = floorf(m[x][e] + log2f(most) - kQaFreshLog2);
+              if (fresh > ex[x][e]) {
+                const float f = fast_exp2(ex[x][e] - fresh);
+                ex[x][e] = fresh;
+                follow(x, e);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  o[i][x][e] *= f;
+                  o[i][x][e + 2] *= f;
+                }
+              }
+            }
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          pb[x][r] = movmatrix_t(pack_f16((acc[x][2 * r] * wt[x][0]) * (vs[r] * wt[x][0]),
+                                          (acc[x][2 * r + 1] * wt[x][1]) * (vs[r] * wt[x][1])));
+      const uint32_t vb = st + kQaUnit * 128 + 2 * t * 128;
+      const uint4 v0 = lds128(vb + ((g ^ (2 * t)) << 4)), v1 = lds128(vb + 128 + ((g ^ (2 * t + 1)) << 4)),
+                  v2 = lds128(vb + 1024 + ((g ^ (2 * t)) << 4)), v3 = lds128(vb + 1152 + ((g ^ (2 * t + 1)) << 4));
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16<FMT>(__byte_perm(word(v0, c), word(v1, c), i ? 0x7362 : 0x5140), a0, a1);
+          codes_to_f16<FMT>(__byte_perm(word(v2, c), word(v3, c), i ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) mma_f16(o[2 * c + i][x], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+        }
+    }
+
+    // ------------------------------------------------------------- the piece's end
+    // Each warp's output over its own sum, then the warps of a head joined through shared memory.
+    cp_async_wait<0>();
+    __syncthreads();
+    float *const rows = reinterpret_cast<float *>(smem_raw);
+    constexpr int kHeads = 8 * NT;
+    float *const ml = rows + kQaWarps * kHeads * Smem::kRow;
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[x][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int head = 8 * x + 2 * t + e;
+        const float f = ex[x][e] == -INFINITY ? 0.f : fast_exp2(0.5f * (ex[x][e] - m[x][e]));
+        const float fl = sum != 0.f ? f / sum : 0.f;
+        float *row = rows + (warp * kHeads + head) * Smem::kRow + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float y0 = o[i][x][e] * f * fl, y1 = o[i][x][e + 2] * f * fl;
+          *reinterpret_cast<float2 *>(row + 2 * i) = sum != 0.f ? make_float2(y0, y1) : make_float2(0.f, 0.f);
+        }
+        // log2 of the sum; -infinity where nothing counts
+        if (g == 0) ml[warp * kHeads + head] = sum != 0.f ? m[x][e] + log2f(sum) : -INFINITY;
+      }
+    __syncthreads();
+    const bool whole = j0 == 0 && j1 == nu;
+    for (int c = tid; c < p.hg * p.G * (kHeadDim / 4); c += kQaThreads) {
+      const int d = 4 * (c & 31), hh = c >> 5, hq = hh / p.G, head = hh - hq * p.G;
+      float M = -INFINITY, sum = 0.f;
+      for (int s = 0; s < wph; ++s) {
+        const float x = ml[(s * p.hg + hq) * kHeads + head];
+        M = x > M || x != x ? x : M;
+      }
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float mm = M == -INFINITY ? 0.f : M;
+      for (int s = 0; s < wph; ++s) {
+        const int from = (s * p.hg + hq) * kHeads + head;
+        const float f = fast_exp2(ml[from] - mm);
+        const float4 y = *reinterpret_cast<const float4 *>(rows + from * Smem::kRow + d);
+        sum += f;
+        a.x = fmaf(f, y.x, a.x);
+        a.y = fmaf(f, y.y, a.y);
+        a.z = fmaf(f, y.z, a.z);
+        a.w = fmaf(f, y.w, a.w);
+      }
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
+      const int h = h0 + hq;
+      if (whole) {
+        *reinterpret_cast<uint2 *>(p.out + (static_cast<long long>(b) * p.Hq + h * p.G + head) * kHeadDim + d) =
+            make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+      } else {
+        float *mine = p.part + ((static_cast<long long>(w) * p.Hkv + h) * 2 + (j0 > 0 ? 0 : 1)) * p.G * (kHeadDim + 4);
+        *reinterpret_cast<float4 *>(mine + head * kHeadDim + d) = a;
+        if (d == 0) mine[p.G * kHeadDim + head] = sum != 0.f ? mm + log2f(sum) : -INFINITY;
+      }
+    }
+    __syncthreads();  // the ring is filled anew
+  }
+}
+
+// ------------------------------------------------------------------------------------ merge
+// out = sum_k 2^(s_k - M) o_k / sum_k 2^(s_k - M) over the parts k of a cut sequence (s_k: log-sum, o_k: its normalised
+// output), in the order of the ranges.  A CTA joins one (sequence, query head): warp x takes the parts x, x + 8, ...,
+// a lane four dims; the warps' sums are added in order.
+constexpr int kQaMergeWarps = 8;
+__global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
+  __shared__ float s_w[kQaMaxRanges];
+  __shared__ float4 s_o[kQaMergeWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hq = static_cast<int>(blockIdx.x) % p.Hq, index = static_cast<int>(blockIdx.x) / p.Hq;
+  const int kv = hq / p.G, head = hq - kv * p.G;
+  griddep_wait();
+  const Q8Cut all = q8_cut(p, lane);
+  if (all.whole || all.ranges < 2) return;
+  int b = 0, first = 0;
+  if (p.merge_by_sequence) {
+    b = index;
+    const int per = (p.B + 31) / 32;
+    first = __shfl_sync(0xffffffffu, all.lane_first, b / per);
+    for (int x = b / per * per; x < b; ++x) first += q8_span(p, all, x);
+  } else {
+    if (index + 1 >= all.ranges) return;
+    q8_find(p, all, all.begin(index + 1), &b, &first);
+  }
+  const int nu = q8_units(p, b);
+  if (nu == 0) return;
+  const int w0 = all.range_of(first), w1 = all.range_of(first + nu - 1);
+  if (w0 == w1 || (!p.merge_by_sequence && w0 != index)) return;  // not cut, or another boundary is its first
+  const int parts = w1 - w0 + 1;
+  const long long each = static_cast<long long>(p.G) * (kHeadDim + 4);
+  auto part = [&](int k) { return p.part + ((static_cast<long long>(w0 + k) * p.Hkv + kv) * 2 + (k == 0 ? 1 : 0)) * each; };
+  // every warp finds M by itself; the weights are made once
+  float M = -INFINITY;
+  for (int k = lane; k < parts; k += 32) {
+    const float x = __ldcg(part(k) + p.G * kHeadDim + head);
+    if (warp == 0) s_w[k] = x;
+    M = fmaxf(M, x);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (M == -INFINITY) M = 0.f;
+  __syncthreads();
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  constexpr int kAhead = 8;
+  for (int k0 = warp; k0 < parts; k0 += kAhead * kQaMergeWarps) {
+    float4 y[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + i * kQaMergeWarps;
+      y[i] = k < parts ? __ldcg(reinterpret_cast<const float4 *>(part(k) + head * kHeadDim + 4 * lane))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + i * kQaMergeWarps;
+      if (k >= parts) break;
+      const float f = fast_exp2(s_w[k] - M);
+      sum += f;
+      a.x = fmaf(f, y[i].x, a.x);
+      a.y = fmaf(f, y[i].y, a.y);
+      a.z = fmaf(f, y[i].z, a.z);
+      a.w = fmaf(f, y[i].w, a.w);
+    }
+  }
+  __shared__ float s_sum[kQaMergeWarps];
+  s_o[warp][lane] = a;
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int x = 1; x < kQaMergeWarps; ++x) {
+    const float4 y = s_o[x][lane];
+    a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+    sum += s_sum[x];
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2 *>(p.out + (static_cast<long long>(b) * p.Hq + hq) * kHeadDim + 4 * lane) =
+      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+}
+
+// --------------------------------------------------------------------------------- host side
+
+namespace {
+
+constexpr int kQaMaxDevices = 64;
+std::atomic<int> g_qa_sms[kQaMaxDevices];  // 0: the kernels are not configured on the device yet
+
+template <int FMT, int NT>
+cudaError_t qa_configure() {
+  return cudaFuncSetAttribute(q8_attn_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q8Smem<NT>::kBytes);
+}
+gqa_status_t qa_device(int device, int *sms) {
+  if (device >= kQaMaxDevices) return GQA_ERR_UNSUPPORTED;
+  *sms = g_qa_sms[device].load(std::memory_order_acquire);
+  if (*sms > 0) return GQA_OK;
+  int n = 0;
+  if (qa_configure<GQA_Q8_E4M3, 1>() != cudaSuccess || qa_configure<GQA_Q8_E4M3, 2>() != cudaSuccess ||
+      qa_configure<GQA_Q8_INT8, 1>() != cudaSuccess || qa_configure<GQA_Q8_INT8, 2>() != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  g_qa_sms[device].store(n, std::memory_order_release);
+  *sms = n;
+  return GQA_OK;
+}
+
+// How a call of this geometry is laid out over the SMs.
+struct QaLayout {
+  int hg, W;
+  bool whole;
+};
+constexpr int kQaWholeTokens = 512;
+QaLayout qa_layout(const gqa_q8_desc_t &d, int sms) {
+  QaLayout y;
+  const int G = d.num_q_heads / d.num_kv_heads;
+  y.whole = d.max_seq_len <= kQaWholeTokens;
+  y.hg = 1;
+  if (!y.whole)
+    while (y.hg < kQaWarps && d.num_kv_heads % (2 * y.hg) == 0) y.hg *= 2;
+  const long long units = d.num_kv_heads / y.hg, slots = static_cast<long long>(sms) * (G > 8 ? 1 : 2);
+  if (y.whole) {
+    y.W = d.batch;
+    return y;
+  }
+  long long best = 1, best_rounds = (units + slots - 1) / slots;
+  for (long long rounds = 1; rounds <= 3; ++rounds) {
+    const long long w = slots * rounds / units;
+    if (w >= 1 && 10 * w * best_rounds > 11 * best * rounds) best = w, best_rounds = rounds;
+  }
+  const long long most = static_cast<long long>(d.batch) * ((d.max_seq_len - 1) / kQaUnit + 1);
+  best = best < most ? best : most;
+  best = best < kQaMaxRanges ? best : kQaMaxRanges;
+  y.W = static_cast<int>(best < 1 ? 1 : best);
+  return y;
+}
+
+gqa_status_t qa_check(const gqa_q8_desc_t &d) {
+  const gqa_status_t st = q8_check(d, true);
+  if (st != GQA_OK) return st;
+  // grid sizes, and the numbers of the batch's units with their gaps, are int32
+  const long long units = static_cast<long long>(d.batch) * ((d.max_seq_len - 1) / kQaUnit + 1 + kQaWarps);
+  return units > 0x7fffffffLL || static_cast<long long>(d.batch > kQaMaxRanges ? d.batch : kQaMaxRanges) * d.num_q_heads > 0x7fffffffLL
+             ? GQA_ERR_UNSUPPORTED
+             : GQA_OK;
+}
+
+}  // namespace
+
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" gqa_status_t gqa_q8_workspace_bytes(const gqa_q8_desc_t *desc, size_t *bytes) {
+  if (!desc || !bytes) return GQA_ERR_INVALID_ARG;
+  const gqa_q8_desc_t d = *desc;
+  gqa_status_t st = qa_check(d);
+  if (st != GQA_OK) return st;
+  st = check_device(d.device);
+  if (st != GQA_OK) return st;
+  DeviceGuard guard(d.device);
+  if (!guard.ok) return GQA_ERR_CUDA;
+  int sms = 0;
+  st = qa_device(d.device, &sms);
+  if (st != GQA_OK) return st;
+  const QaLayout y = qa_layout(d, sms);
+  *bytes = y.whole || y.W < 2 ? 256
+                              : static_cast<size_t>(y.W) * 2 * d.num_q_heads * (kHeadDim + 4) * sizeof(float);
+  return GQA_OK;
+}
+
+extern "C" gqa_status_t gqa_q8_attn(const gqa_q8_desc_t *desc, const void *q, const void *k_codes, const void *v_codes,
+                                    const float *k_scale, const float *v_scale, const int32_t *page_table,
+                                    const int32_t *seq_lens, void *out, void *workspace, uint32_t *device_errors,
+                                    void *stream) {
+  if (!desc) return GQA_ERR_INVALID_ARG;
+  const gqa_q8_desc_t d = *desc;
+  gqa_status_t st = qa_check(d);
+  if (st != GQA_OK) return st;
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !seq_lens || !out || !workspace) return GQA_ERR_INVALID_ARG;
+  const bool paged = d.block_size > 0;
+  if (paged != (page_table != nullptr)) return GQA_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k_codes, 16) || !aligned_to(v_codes, 16) || !aligned_to(out, 16) ||
+      !aligned_to(workspace, 256) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4) || !aligned_to(page_table, 4) ||
+      !aligned_to(seq_lens, 4) || !aligned_to(device_errors, 4))
+    return GQA_ERR_INVALID_ARG;
+  st = check_device(d.device);
+  if (st != GQA_OK) return st;
+  DeviceGuard guard(d.device);
+  if (!guard.ok) return GQA_ERR_CUDA;
+  int sms = 0;
+  st = qa_device(d.device, &sms);
+  if (st != GQA_OK) return st;
+
+  const QaLayout y = qa_layout(d, sms);
+  Q8AttnParams p;
+  memset(&p, 0, sizeof p);
+  p.q = static_cast<const uint16_t *>(q);
+  p.k_codes = static_cast<const uint8_t *>(k_codes);
+  p.v_codes = static_cast<const uint8_t *>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<uint16_t *>(out);
+  p.part = static_cast<float *>(workspace);
+  p.err = device_errors;
+  p.B = d.batch;
+  p.Hq = d.num_q_heads;
+  p.Hkv = d.num_kv_heads;
+  p.G = d.num_q_heads / d.num_kv_heads;
+  p.hg = y.hg;
+  p.paged = paged ? 1 : 0;
+  p.max_seq = d.max_seq_len;
+  p.max_blocks = capacity_tiles(d.max_seq_len);
+  p.num_blocks = paged ? d.num_cache_blocks : 0;
+  p.W = y.W;
+  p.whole = y.whole ? 1 : 0;
+  p.merge_by_sequence = p.B <= p.W - 1;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(kHeadDim)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool wide = p.G > 8, e4m3 = d.format == GQA_Q8_E4M3;
+  auto *kernel = e4m3 ? (wide ? q8_attn_kernel<GQA_Q8_E4M3, 2> : q8_attn_kernel<GQA_Q8_E4M3, 1>)
+                      : (wide ? q8_attn_kernel<GQA_Q8_INT8, 2> : q8_attn_kernel<GQA_Q8_INT8, 1>);
+  const long long joins = static_cast<long long>(p.merge_by_sequence ? p.B : p.W - 1) * p.Hq;
+  if (launch_pdl(kernel, dim3(static_cast<unsigned>(p.W * (p.Hkv / p.hg))), dim3(kQaThreads),
+                 static_cast<size_t>(wide ? Q8Smem<2>::kBytes : Q8Smem<1>::kBytes), s, p) != cudaSuccess ||
+      (!y.whole && p.W > 1 &&
+       launch_pdl(q8_merge_kernel, dim3(static_cast<unsigned>(joins)), dim3(32 * kQaMergeWarps), 0, s, p) != cudaSuccess)) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  return GQA_OK;
+}

@@ -94,6 +94,37 @@ gqa_status_t gqa_q8_read(const gqa_q8_desc_t *desc, const void *k_codes, const v
                          const float *v_scale, const int32_t *page_table, const int32_t *offsets,
                          const int32_t *slot_start, void *k_out, void *v_out, uint32_t *device_errors, void *stream);
 
+/*
+ * gqa_q8_workspace_bytes -- size of the workspace gqa_q8_attn needs for a geometry on its device, into
+ * *bytes (num_tokens and the strides are not used).  Errors: those of gqa_q8_attn's geometry
+ * checks; GQA_ERR_CUDA.
+ */
+gqa_status_t gqa_q8_workspace_bytes(const gqa_q8_desc_t *desc, size_t *bytes);
+
+/*
+ * gqa_q8_attn -- attention of one new token a sequence over the cache, its own slot included.
+ *   q          [B, H_q, 128] bf16 device, dense   rotated queries
+ *   k_codes, v_codes, k_scale, v_scale, page_table   the cache; read only
+ *   seq_lens   [B] int32 device   slots 0 .. seq_lens[b] - 1 are attended to; 0 <= seq_lens[b] <= max_seq_len
+ *   out        [B, H_q, 128] bf16 device   softmax over these slots of q . K / sqrt(128), applied to V;
+ *              zeros for a sequence without slots (or a head whose every score is -infinity).  Must
+ *              not overlap any input.
+ *   workspace  device memory of gqa_q8_workspace_bytes bytes, 256-byte aligned; its contents need not be
+ *              set and are not kept.  Calls that may overlap (different streams, two graphs
+ *              replayed at once) need one each.
+ *   device_errors   optional device pointer to a uint32.  A seq_lens[b] outside [0, max_seq_len]
+ *              (GQA_DEVERR_SEQLEN) gives zeros; a page id outside the pool (GQA_DEVERR_PAGE) reads
+ *              that page as zeros.
+ * Slots from seq_lens[b] on have no effect whatever they hold.  A scale that is not finite, or an e4m3
+ * code that is no number, makes what depends on it infinite or NaN.  The rounding of the
+ * result does not depend on timing: the same inputs give the same bits.
+ * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (as gqa_q8_append; also H_q % H_kv != 0, H_q / H_kv >
+ * 16, B (ceil(max_seq_len / 16) + 8) or max(B, 640) H_q above 2^31 - 1), GQA_ERR_CUDA.
+ */
+gqa_status_t gqa_q8_attn(const gqa_q8_desc_t *desc, const void *q, const void *k_codes, const void *v_codes,
+                         const float *k_scale, const float *v_scale, const int32_t *page_table,
+                         const int32_t *seq_lens, void *out, void *workspace, uint32_t *device_errors, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,7 @@ the tests allow 2^-8 (1 + 2^-12) |value|, and half of the least bf16 step where 
 
 Tolerance of an output element of the attention, derived before the first run: half a bf16 step,
 2^-8 |o|, and 2^-10 sum_j p_j |v_j| for what comes before it: a score is a binary32 sum of 128 exact
-products, off by at most 128 2^-24 sum |q k| / sqrt(128) (below 2^-13 for the data here, and a weight by
+products, off by at most 128 2^-24 sum |q k| / sqrt(128) (below 2^-12 for the data here, and a weight by
 as much relatively), 2^x and the scalings add 2^-20, the weights times the scale of V are rounded to
 binary16 (half a step, 2^-11), sums of at most 2^13 weights add 2^-13."""
 import numpy as np
@@ -239,3 +239,207 @@ def test_many_sequences():
             np.testing.assert_array_equal(got[rows], ref[at[b]:at[b + 1]])
             np.testing.assert_array_equal(gf[rows], f[at[b]:at[b + 1]])
         assert err.item() == 0
+
+
+# ------------------------------------------------------------------------------- one token's attention
+
+def attend(c, q, lens, Hq):
+    """(out [B, Hq, 128], sum_j p_j |v_j|) in 64 bits over the cache's values."""
+    G = Hq // c.Hkv
+    K, V = c.dense()
+    out = np.zeros((c.B, Hq, D))
+    mag = np.zeros((c.B, Hq, D))
+    qd = q.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        rows = c.slots(b, 0, n)
+        for h in range(Hq):
+            k, v = K[rows, h // G], V[rows, h // G]
+            s = (k @ qd[b, h]) / np.sqrt(D)
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            out[b, h], mag[b, h] = p @ v, p @ np.abs(v)
+    return out, mag
+
+
+def token(c, q, lens, Hq, **more):
+    out = torch.full((c.B, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = errors()
+    ws = binding.q8_workspace(c.B, Hq, c.Hkv, c.cap, block_size=64 if c.blocks else 0, num_cache_blocks=c.blocks)
+    ws.fill_(255)
+    binding.q8_attn(c.B, Hq, c.Hkv, c.cap, q, *c.tensors, more.get("table", c.table), i32(lens), out, workspace=ws,
+                    device_errors=err, **c.layout)
+    return out, err.item()
+
+
+def near(out, ref, mag, least=0.0):
+    off = np.abs(out.double().cpu().numpy() - ref)
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + least
+    assert (off <= tol).all(), (off.max(), (off / np.maximum(tol, 1e-300)).max())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hq,Hkv,lens,paged,slack", [
+    (40, 8, [256], False, 0),
+    (40, 8, [1, 0, 15, 16, 17, 63, 64, 65, 300], True, 5),          # one CTA a sequence and head (small capacity)
+    (40, 8, [1, 0, 15, 16, 17, 63, 64, 65, 1300], True, 5),         # cut into ranges
+    (64, 8, [5000], True, 0),
+    (8, 8, [700, 900, 0, 33], False, 1),
+    (16, 1, [2000, 1, 0, 777], True, 0),                            # 16 heads a KV head, 8 warps a head
+    (18, 2, [900, 1000], False, 3),                                 # 9 heads
+    (6, 3, [600, 601, 602], True, 0),                               # KV heads that are no power of two
+    (20, 4, [3000, 10, 4000, 0, 0, 1], True, 0),
+    (32, 32, [520, 100], True, 0),
+    (15, 5, [1111], False, 2),
+    (4, 4, [0, 0], True, 600),
+])
+def test_one_token(fmt, Hq, Hkv, lens, paged, slack):
+    c = Cache(len(lens), Hkv, max(max(lens), 1) + slack, fmt, paged, seed=len(lens))
+    q = rows_of(9, len(lens), Hq)
+    out, err = token(c, q, lens, Hq)
+    ref, mag = attend(c, q, lens, Hq)
+    near(out, ref, mag)
+    assert err == 0
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert bool((out[b] == 0).all())
+    again, _ = token(c, q, lens, Hq)
+    assert torch.equal(out, again)
+
+
+def test_many_sequences_attend():
+    """More sequences than ranges; ragged, some empty."""
+    for B, cap in ((400, 700), (700, 520), (1024, 40)):
+        rng = np.random.default_rng(B)
+        lens = rng.integers(0, cap + 1, B)
+        lens[rng.random(B) < 0.2] = 0
+        c = Cache(B, 2, cap, "int8", False)
+        q = rows_of(3, B, 4)
+        out, err = token(c, q, lens, 4)
+        ref, mag = attend(c, q, lens, 4)
+        near(out, ref, mag)
+        assert err == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("cap", [400, 3000])
+def test_slots_behind_the_length_have_no_effect(fmt, cap):
+    B, Hq, Hkv = 3, 16, 4
+    c = Cache(B, Hkv, cap, fmt, True)
+    lens = [cap - 65, 1, cap - 7]
+    q = rows_of(4, B, Hq)
+    out, _ = token(c, q, lens, Hq)
+    keep = np.concatenate([c.slots(b, 0, n) for b, n in enumerate(lens)])
+    rest = torch.as_tensor(np.setdiff1d(np.arange(c.rows), keep), device="cuda")
+    c.k.view(torch.uint8)[rest] = 0x7f
+    c.v.view(torch.uint8)[rest] = 0xff
+    c.ks[rest], c.vs[rest] = float("nan"), float("inf")
+    again, err = token(c, q, lens, Hq)
+    assert err == 0 and torch.equal(out, again)
+
+
+@pytest.mark.parametrize("cap", [300, 2500])
+def test_scales_over_the_whole_range(cap):
+    """Rows of V whose scales lie many binades apart, growing, falling and mixed; a head whose weight sits
+    on a row of small values (as where a first token takes the weight); tiny and large queries."""
+    B, Hq, Hkv = 4, 8, 4
+    c = Cache(B, Hkv, cap, "e4m3", False)
+    slot = torch.arange(cap, device="cuda").float()
+    vs = c.vs.view(B, cap, Hkv)
+    vs[0] *= torch.exp2(-20 + 40 * slot / cap)[:, None]
+    vs[1] *= torch.exp2(20 - 40 * slot / cap)[:, None]
+    vs[2] *= torch.exp2(torch.randint(-10, 10, (cap, Hkv), device="cuda").float())
+    vs[3, 1:] *= 2.0 ** 10
+    c.ks.view(B, cap, Hkv)[:, :, 3] *= 2.0 ** -60
+    q = rows_of(6, B, Hq)
+    q[:, 6:] *= 2.0 ** 60
+    q[:, :2] *= 2.0 ** -40
+    c.k.view(B, cap, Hkv, D)[3, 0, 1] = q[3, 2].float().mul(100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    lens = [cap, cap - 1, cap - 17, cap]
+    out, err = token(c, q, lens, Hq)
+    ref, mag = attend(c, q, lens, Hq)
+    near(out, ref, mag)
+    assert err == 0
+
+
+@pytest.mark.parametrize("power", [-135, -100, 100, 115])
+def test_extreme_scales(power):
+    """Values near the ends of binary32's range: alike within a few binades."""
+    c = Cache(2, 2, 600, "int8", True)
+    c.vs *= 2.0 ** power
+    q = rows_of(6, 2, 4)
+    out, err = token(c, q, [600, 77], 4)
+    ref, mag = attend(c, q, [600, 77], 4)
+    near(out, ref, mag, 2.0 ** -134)
+    # (at 2^-135 a value is 2^-135 and the mean of 77 of them about 2^-138, below half of the least bf16 number, 2^-133)
+    assert err == 0 and bool((out != 0).any()) == bool((np.abs(ref) >= 2.0 ** -133).any())
+
+
+@pytest.mark.parametrize("cap", [300, 2500])
+def test_values_that_are_not_finite_reach_what_sees_them(cap):
+    B, Hq, Hkv = 3, 8, 4
+    c = Cache(B, Hkv, cap, "e4m3", False)
+    clean, _ = token(c, q := rows_of(4, B, Hq), [cap] * B, Hq)
+    c.ks.view(B, cap, Hkv)[0, 5, 1] = float("nan")
+    c.vs.view(B, cap, Hkv)[1, cap - 1, 2] = float("nan")
+    c.v.view(torch.uint8).view(B, cap, Hkv, D)[2, 17, 3, 9] = 0x7f
+    out, err = token(c, q, [cap] * B, Hq)
+    bad = torch.zeros(B, Hq, D, dtype=torch.bool, device="cuda")
+    bad[0, 2:4], bad[1, 4:6], bad[2, 6:8, 9] = True, True, True
+    assert err == 0 and bool(torch.isnan(out[bad]).all()) and torch.equal(out[~bad], clean[~bad])
+    q[0, 0, 3] = float("inf")
+    q[1, 0, 3] = float("nan")
+    out, _ = token(c, q, [cap] * B, Hq)
+    assert bool(torch.isnan(out[:2, 0]).all()) and torch.equal(out[:, 1][~bad[:, 1]], clean[:, 1][~bad[:, 1]])
+
+
+@pytest.mark.parametrize("cap", [300, 2500])
+def test_bad_lengths_and_pages(cap):
+    B, Hq, Hkv = 4, 8, 2
+    c = Cache(B, Hkv, cap, "e4m3", True)
+    q = rows_of(4, B, Hq)
+    lens = [cap, -1, cap + 1, cap]
+    table = c.table.clone()
+    table[3, 1], table[3, 2] = c.blocks, -5
+    out, err = token(c, q, lens, Hq, table=table)
+    assert err == binding.DEVERR_SEQLEN | binding.DEVERR_PAGE
+    assert bool((out[1:3] == 0).all())
+    zero = torch.as_tensor(c.slots(3, 64, 128), device="cuda")
+    for x in c.tensors:
+        x.view(torch.uint8)[zero] = 0
+    ref, mag = attend(c, q, [cap, 0, 0, cap], Hq)
+    near(out, ref, mag)
+
+
+def test_rows_beyond_four_gib():
+    """A cache whose byte offsets pass 32 bits."""
+    Hkv, cap = 8, (1 << 32) // (8 * 128) + 700
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("not enough device memory")
+    k = torch.zeros(cap, Hkv, D, dtype=torch.int8, device="cuda")
+    v, s = torch.zeros_like(k), torch.zeros(2, cap, Hkv, device="cuda")
+    c = Cache(1, Hkv, 4, "int8", False)
+    c.cap = c.rows = cap
+    c.k, c.v, c.ks, c.vs = k, v, s[0], s[1]
+    n = 600
+    x, y = rows_of(1, n, Hkv), rows_of(2, n, Hkv)
+    binding.q8_append(1, Hkv, n, cap, x, y, *c.tensors, None, i32([0, n]), i32([cap - n]), **c.layout)
+    ko, vo = torch.empty_like(x), torch.empty_like(y)
+    binding.q8_read(1, Hkv, n, cap, *c.tensors, None, i32([0, n]), i32([cap - n]), ko, vo, **c.layout)
+    kq, kf = quantised(x.double().cpu().numpy(), "int8")
+    vq, vf = quantised(y.double().cpu().numpy(), "int8")
+    kd, vd = kq * kf.astype(float)[..., None], vq * vf.astype(float)[..., None]
+    assert (np.abs(ko.double().cpu().numpy() - kd) <= 2.0 ** -8 * (1 + 2.0 ** -12) * np.abs(kd)).all()
+    q = rows_of(3, 1, Hkv) * 4
+    out, err = token(c, q, [cap], Hkv)
+    assert err == 0
+    for h in range(Hkv):
+        z = kd[:, h] @ q[0, h].double().cpu().numpy() / np.sqrt(D)
+        top = max(z.max(), 0.0)
+        p = np.exp(z - top)
+        total = p.sum() + (cap - n) * np.exp(-top)
+        ref, mag = (p @ vd[:, h]) / total, (p @ np.abs(vd[:, h])) / total
+        off = np.abs(out[0, h].double().cpu().numpy() - ref)
+        assert (off <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag).all()
