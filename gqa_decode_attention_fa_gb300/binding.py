@@ -1,5 +1,6 @@
 """Thin ctypes binding over libgqa_decode.so (include/gqa_decode.h, gqa_prefill.h, gqa_q4.h,
-gqa_rope.h, gqa_tree.h, gqa_pages.h, gqa_q8.h).
+gqa_rope.h, gqa_tree.h, gqa_pages.h, gqa_q8.h,
+gqa_packed.h).
 
 Argument marshalling only: every step of the decode path runs in the library's CUDA
 kernels.  Device tensors are torch tensors (device memory and streams come from torch);
@@ -75,6 +76,12 @@ class Q8Desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in (
         "batch", "num_q_heads", "num_kv_heads", "head_dim", "format", "num_tokens", "block_size", "max_seq_len",
         "num_cache_blocks", "device", "k_stride", "v_stride")]
+
+
+class PackedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "num_queries", "num_keys", "causal", "device", "q_stride",
+        "k_stride", "v_stride")]
 
 
 class Pool(ctypes.Structure):
@@ -177,6 +184,7 @@ def load(build: bool = True):
         lib.gqa_q8_read.argtypes = [P] * 12
         lib.gqa_q8_workspace_bytes.argtypes = [P, P]
         lib.gqa_q8_attn.argtypes = [P] * 12
+        lib.gqa_packed_attn.argtypes = [P] * 9
         lib.gqa_status_string.argtypes = [I]
         lib.gqa_status_string.restype = ctypes.c_char_p
         for name in ("gqa_plan_create", "gqa_plan_destroy", "gqa_decode_attn", "gqa_decode_attn_host",
@@ -185,7 +193,7 @@ def load(build: bool = True):
                      "gqa_decode_attn_q4", "gqa_rope_freqs", "gqa_rope_append", "gqa_tree_prepare",
                      "gqa_tree_workspace_bytes", "gqa_tree_attn", "gqa_pages_fork", "gqa_pages_resize",
                      "gqa_pages_copy", "gqa_cache_keep_rows", "gqa_q8_append", "gqa_q8_read",
-                     "gqa_q8_workspace_bytes", "gqa_q8_attn"):
+                     "gqa_q8_workspace_bytes", "gqa_q8_attn", "gqa_packed_attn"):
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -315,7 +323,7 @@ def prefill_attn_workload(w, out, *, device: int = 0, device_errors=None, stream
                  num_cache_blocks=w.num_blocks, device=device, device_errors=device_errors, stream=stream)
 
 
-# ------------------------------------- rotary append, draft trees, cache pages, 8-bit caches
+# ------------------- rotary append, draft trees, cache pages, 8-bit caches, packed prompts
 
 # These calls come once a layer and step, so their wrappers keep to a few microseconds: one check
 # a tensor, and the descriptors of the geometries in use are kept (the library reads them during a
@@ -733,6 +741,29 @@ def q8_attn(batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int, q
         _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
         _dev(seq_lens, "seq_lens", i32, (batch,), device), op, ws, _err(device_errors, device), _on(device, stream)),
         "gqa_q8_attn")
+
+
+def packed_attn(q, k, v, q_offsets, k_offsets, out, *, causal: bool = True, device: int = 0, device_errors=None,
+                stream=None):
+    """Attention over packed prompts (gqa_packed_attn, include/gqa_packed.h): q [N_q, H_q, 128], k and v [N_k, H_kv,
+    128] (slices of one projection are taken as they are), out [N_q, H_q, 128] dense; sequence b has the queries
+    q_offsets[b] .. q_offsets[b + 1] - 1 and the keys of k_offsets (None: the same), both ending at one token."""
+    tt = _torch()
+    if q.dim() != 3 or k.dim() != 3 or q_offsets.dim() != 1:
+        raise ValueError("q [N_q, H_q, 128], k and v [N_k, H_kv, 128], q_offsets [B + 1]")
+    (nq, hq, _), (nk, hkv, _) = q.shape, k.shape
+    offsets = q_offsets.shape
+    qp, qs = _packed(q, "q", nq, hq, device)
+    kp, ks = _packed(k, "k", nk, hkv, device)
+    vp, vs = _packed(v, "v", nk, hkv, device)
+    op = _dev(out, "out", tt.bf16, (nq, hq, 128), device)
+    if qp == op:
+        raise ValueError("out: must not be q, which other CTAs still read")
+    _check(load().gqa_packed_attn(
+        _desc(PackedDesc, offsets[0] - 1, hq, hkv, 128, nq, nk, int(bool(causal)), device, qs, ks, vs), qp, kp, vp,
+        _dev(q_offsets, "q_offsets", tt.i32, None, device), _dev(k_offsets, "k_offsets", tt.i32, offsets, device, True), op,
+        _err(device_errors, device), _on(device, stream)),
+        "gqa_packed_attn")
 
 
 def q4_codebook() -> np.ndarray:

@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libgqa_decode.so")
 HEADERS = [os.path.join(ROOT, "include", "gqa_decode.h"), os.path.join(ROOT, "include", "gqa_prefill.h"),
            os.path.join(ROOT, "include", "gqa_q4.h"), os.path.join(ROOT, "include", "gqa_rope.h"),
            os.path.join(ROOT, "include", "gqa_tree.h"), os.path.join(ROOT, "include", "gqa_pages.h"),
-           os.path.join(ROOT, "include", "gqa_q8.h")]
+           os.path.join(ROOT, "include", "gqa_q8.h"), os.path.join(ROOT, "include", "gqa_packed.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",

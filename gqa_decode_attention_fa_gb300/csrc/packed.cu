@@ -1,0 +1,735 @@
+// Attention over prompts packed one behind the other (include/gqa_packed.h) on the 5th-generation tensor
+// core.
+//
+// Rows.  Tt = 128 / G tokens and the G query heads of a KV head make the 128 rows of a tile, the M of
+// every MMA; a unit of work is two such tiles, neighbours in one sequence, and the 128-key tiles that the
+// later of the two sees.  Keys behind a row's last are masked by the row, those behind the unit's never
+// loaded.
+//
+// Units are numbered from the one with the most key tiles to the one with the fewest, over all sequences and
+// KV heads, and dealt to the CTAs, one an SM, to and fro; the numbering follows from the lengths, which are read on the
+// device: the units with at least D key tiles are counted in closed form for each sequence.
+//
+// A CTA: a TMA warp finds the units, tells the others and streams Q, K and V; two streams of an MMA warp and
+// four softmax warps each hold a tile, so that one stream's softmax overlaps the other's products; a warp
+// looks over the values that some rows must not see.  A stream's S = Q K^T (128 x 128) and its O += P V lie in tensor
+// memory, P over S as bf16 pairs in two halves, the first multiplied while the second is made.  A softmax thread holds a
+// row.  The maximum is raised lazily (by more than 2^8), so most tiles rescale nothing; S of a tile is issued behind P V of
+// the one before, so a thread that sees S finds O at rest.
+//   P is rounded to bf16 (2^-8 of a weight, and the sum takes the rounded ones): over the keys that adds about as
+// much to a row as the output's own rounding; a second term for what is cut would add half to the
+// products.
+#include <math.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "../../include/gqa_packed.h"
+#include "op_args.h"
+#include "pairmath.cuh"
+#include "tc05.cuh"
+
+namespace gqa {
+
+struct PackedParams {
+  const int32_t *q_offsets, *k_offsets;
+  const uint16_t *v;
+  uint16_t *out;
+  uint32_t *err;
+  long long v_stride;
+  int B, Nq, Nk, Hq, Hkv, G, Tt;
+  int causal;
+  int out_wide;  // `out` is 32-byte aligned
+  float scale_log2;
+};
+
+namespace {
+
+constexpr int kPkRows = 128;
+constexpr int kPkKeys = 128;
+constexpr int kPkMmaWarp = 8;  // and 9: a stream's each
+constexpr int kPkProducerWarp = 10;
+constexpr int kPkCheckWarp = 11;
+constexpr int kPkThreads = 32 * 12;
+constexpr int kPkKStages = 2, kPkVStages = 3;
+constexpr int kPkPanelBytes = kPkRows * kHalfRowBytes;  // 64 dims of 128 rows: 16 KiB
+constexpr int kPkTileBytes = 2 * kPkPanelBytes;
+constexpr int kPkSlots = 4;  // units told ahead
+// Tensor memory: a stream's S (128 columns; P in the first 64) and its O (128).
+constexpr uint32_t kPkTmemStream = 256, kPkTmemO = 128, kPkTmemCols = 512;
+constexpr float kPkRescaleLog2 = 8.f;
+// Registers a thread: 168 at launch; the softmax warpgroups take what the third gives up.
+constexpr int kPkRegsSoftmax = 216, kPkRegsOther = 72;
+static_assert(2 * kPkRegsSoftmax + kPkRegsOther <= 3 * 168, "registers of the launch");
+
+constexpr int kPkOffK = 2 * kPkTileBytes;
+constexpr int kPkOffV = kPkOffK + kPkKStages * kPkTileBytes;
+constexpr int kPkOffBar = kPkOffV + kPkVStages * kPkTileBytes;
+
+// A unit as the producer tells it.
+struct PackedUnit {
+  int q0, k0;      // packed rows of the unit's first query and of its sequence's first key
+  int tokens;      // queries of the unit, up to 2 Tt; 0: no unit is left
+  int see0;        // keys that the first query sees (causal: each next one sees one more), may be negative
+  int keys;        // m of the sequence
+  int nt[2];       // key tiles of each stream's tile
+  int kv;
+  uint32_t bad;    // a value that not all rows see is not finite
+};
+
+struct PackedShared {
+  uint64_t k_full[kPkKStages], k_empty[kPkKStages], v_full[kPkVStages], v_clean[kPkVStages], v_empty[kPkVStages];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain[2], q_full, q_empty;
+  uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_checked[kPkSlots];
+  PackedUnit unit[kPkSlots];
+  uint32_t tmem;
+};
+constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 6 + 2 + 3 * kPkSlots;
+constexpr int kPkSmemBytes = kPkOffBar + static_cast<int>(sizeof(PackedShared));
+static_assert(kPkSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void store_32b(uint16_t *dst, const uint32_t (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// Queries and keys of sequence b; n = 0 where the offsets of the queries, m = 0 where those of the keys are
+// not in order.
+struct PackedSeq {
+  int q0, k0, n, m;
+};
+__device__ __forceinline__ PackedSeq packed_seq(const PackedParams &p, int b) {
+  PackedSeq s;
+  s.q0 = p.q_offsets[b];
+  const int q1 = p.q_offsets[b + 1];
+  s.k0 = p.k_offsets[b];
+  const int k1 = p.k_offsets[b + 1];
+  s.n = s.q0 >= 0 && q1 >= s.q0 && q1 <= p.Nq ? q1 - s.q0 : 0;
+  s.m = s.k0 >= 0 && k1 >= s.k0 && k1 <= p.Nk ? k1 - s.k0 : 0;
+  return s;
+}
+// Units a KV head of a sequence whose key tiles are at least D.
+__device__ __forceinline__ int units_of_depth(const PackedParams &p, const PackedSeq &s, int D) {
+  const int P = 2 * p.Tt, all = (s.n + P - 1) / P;
+  if (D <= 0) return all;
+  const int need = (D - 1) * kPkKeys + 1;  // keys that the unit's last query has to see
+  if (s.m < need) return 0;
+  if (!p.causal) return all;
+  const int last = need - (s.m - s.n);  // queries, counted from the sequence's first, up to the unit's last
+  if (last <= 0) return all;
+  return last > s.n ? 0 : all - (last + P - 1) / P + 1;
+}
+
+// Finds units by their number, which grows from call to call.  Every lane of a warp alike.
+struct PackedWalk {
+  int D, upto, above;  // units a KV head with at least D key tiles, and with more
+  int base, before;    // the 32 sequences looked at, and units of exactly D tiles in those before them
+
+  __device__ __forceinline__ int count(const PackedParams &p, int d, int lane) const {
+    int c = 0;
+    for (int b = lane; b < p.B; b += 32) c += units_of_depth(p, packed_seq(p, b), d);
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+  __device__ __forceinline__ void start(const PackedParams &p, int lane) {
+    unsigned most = 0;
+    for (int b = lane; b < p.B; b += 32) most = max(most, static_cast<unsigned>(packed_seq(p, b).m));
+    D = static_cast<int>((__reduce_max_sync(0xffffffffu, most) + kPkKeys - 1) / kPkKeys) + 1;
+    upto = above = base = before = 0;
+  }
+  // The unit of number `at` (a KV head's); false if there are fewer.
+  __device__ __forceinline__ bool find(const PackedParams &p, int at, int lane, PackedSeq *seq, int *index) {
+    if (at >= upto) {
+      if (D == 0) return false;
+      int lo = 0, hi = D - 1;  // the largest depth with more than `at` units
+      const int all = count(p, 0, lane);
+      if (at >= all) return false;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (count(p, mid, lane) > at) lo = mid;
+        else hi = mid - 1;
+      }
+      D = lo;
+      upto = count(p, D, lane);
+      above = count(p, D + 1, lane);
+      base = before = 0;
+    }
+    const int want = at - above;
+    for (; base < p.B; base += 32) {
+      PackedSeq s = {0, 0, 0, 0};
+      int c = 0, deeper = 0, all = 0;
+      if (base + lane < p.B) {
+        s = packed_seq(p, base + lane);
+        deeper = units_of_depth(p, s, D + 1);
+        c = units_of_depth(p, s, D) - deeper;
+        all = units_of_depth(p, s, 0);
+      }
+      int sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, sum, 31);
+      if (want >= before + total) {
+        before += total;
+        continue;
+      }
+      const int x = want - before;
+      const int who = __ffs(__ballot_sync(0xffffffffu, sum > x)) - 1;
+      // units of a sequence get deeper with their index: those of D tiles end where the deeper ones begin
+      const int mine = all - deeper - c + (x - (sum - c));
+      *index = __shfl_sync(0xffffffffu, mine, who);
+      seq->q0 = __shfl_sync(0xffffffffu, s.q0, who);
+      seq->k0 = __shfl_sync(0xffffffffu, s.k0, who);
+      seq->n = __shfl_sync(0xffffffffu, s.n, who);
+      seq->m = __shfl_sync(0xffffffffu, s.m, who);
+      return true;
+    }
+    return false;
+  }
+};
+
+// Values of keys [from, to) of a row's sequence that are not finite, which the products left out, come to
+// the row after all.
+__device__ __noinline__ void packed_add_nonfinite(const PackedParams &p, int k0, int kv, int from, int to, uint16_t *out,
+                                                  float inv) {
+  for (int j = from; j < to; ++j) {
+    const uint16_t *v = p.v + (k0 + j) * p.v_stride + kv * kHeadDim;
+#pragma unroll 1
+    for (int d = 0; d < kHeadDim; ++d) {
+      const uint32_t y = v[d];
+      if ((y & 0x7f80u) != 0x7f80u) continue;
+      out[d] = static_cast<uint16_t>(pack_bf16(bf16_lo_to_float(out[d]) + bf16_lo_to_float(y) * inv, 0.f) & 0xffffu);
+    }
+  }
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kPkThreads, 1)
+    packed_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_addr(smem) & 1023u) != 0u) {  // a launch assumption broken: no work at all
+    if (threadIdx.x == 0) flag_error(p.err, GQA_DEVERR_LAUNCH);
+    return;
+  }
+  PackedShared &sh = *reinterpret_cast<PackedShared *>(smem + kPkOffBar);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  griddep_wait();
+  if (warp == kPkMmaWarp) {
+    tmem_alloc(smem_addr(&sh.tmem), kPkTmemCols);
+    tmem_relinquish();
+  } else if (warp == kPkMmaWarp + 1) {
+    uint64_t *bars = sh.k_full;
+    for (int i = lane; i < kPkNumBars; i += 32) {
+      uint64_t *bar = bars + i;
+      int count = 1;
+      if ((bar >= sh.k_empty && bar < sh.v_full) || (bar >= sh.v_empty && bar < sh.s_full) || bar == &sh.q_empty) count = 2;
+      if ((bar >= sh.p_full[0] && bar < sh.o_full) || (bar >= sh.o_free && bar < sh.drain)) count = 4;
+      if (bar >= sh.unit_empty && bar < sh.unit_checked) count = 11;  // every warp but the producer
+      mbar_init(smem_addr(bar), count);
+    }
+    fence_barrier_init();
+    __syncwarp();
+  } else if (warp == kPkProducerWarp && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  auto k_ptr = [&](int s) { return smem_addr(smem) + kPkOffK + s * kPkTileBytes; };
+  auto v_ptr = [&](int s) { return smem_addr(smem) + kPkOffV + s * kPkTileBytes; };
+  // The unit told as number u; false when a wait ran out.  Whoever has read a slot gives it back.
+  auto take_unit = [&](int u, PackedUnit &x) -> bool {
+    const int slot = u % kPkSlots;
+    if (!mbar_wait(smem_addr(&sh.unit_full[slot]), static_cast<uint32_t>((u / kPkSlots) & 1))) return false;
+    x = sh.unit[slot];
+    return true;
+  };
+  bool ok = true;
+
+  if (warp >= kPkMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPkRegsOther));
+    if (warp == kPkProducerWarp) {
+      // ---------------------------------------------------------------- units, TMA
+      if (blockIdx.x == 0)
+        for (int b = lane; b < p.B; b += 32) {
+          const int q0 = p.q_offsets[b], q1 = p.q_offsets[b + 1], k0 = p.k_offsets[b], k1 = p.k_offsets[b + 1];
+          if (q0 < 0 || q1 < q0 || q1 > p.Nq || k0 < 0 || k1 < k0 || k1 > p.Nk) flag_error(p.err, GQA_DEVERR_SEQLEN);
+        }
+      PackedWalk walk;
+      walk.start(p, lane);
+      int it = 0, queries = 0;  // key tiles and loads of queries so far
+      for (int u = 0; ok; ++u) {
+        const int c = static_cast<int>(blockIdx.x), W = static_cast<int>(gridDim.x);
+        const long long number = static_cast<long long>(u) * W + (u & 1 ? W - 1 - c : c);  // to and fro
+        PackedUnit x = {};
+        PackedSeq s;
+        int index = 0;
+        if (number < 0x7fffffffLL && walk.find(p, static_cast<int>(number / p.Hkv), lane, &s, &index)) {
+          const int t0 = index * 2 * p.Tt;
+          x.q0 = s.q0 + t0;
+          x.k0 = s.k0;
+          x.tokens = min(2 * p.Tt, s.n - t0);
+          x.see0 = p.causal ? t0 + 1 + s.m - s.n : s.m;
+          x.keys = s.m;
+          x.kv = static_cast<int>(number % p.Hkv);
+          for (int i = 0; i < 2; ++i) {
+            const int rows = min(p.Tt, x.tokens - i * p.Tt);  // tokens of the tile
+            const int sees = p.causal ? x.see0 + i * p.Tt + rows - 1 : s.m;
+            x.nt[i] = rows > 0 && sees > 0 ? (sees + kPkKeys - 1) / kPkKeys : 0;
+          }
+        }
+        const int slot = u % kPkSlots;
+        if (u >= kPkSlots) ok = mbar_wait(smem_addr(&sh.unit_empty[slot]), static_cast<uint32_t>((u / kPkSlots - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          sh.unit[slot] = x;
+          mbar_arrive(smem_addr(&sh.unit_full[slot]));
+        }
+        if (x.tokens == 0) break;
+        const int nt = max(x.nt[0], x.nt[1]);
+        if (nt == 0) continue;
+        if (lane == 0) {
+          for (int j = 0; j < nt && ok; ++j, ++it) {
+            const int row = x.k0 + j * kPkKeys, ks = it % kPkKStages, vs = it % kPkVStages;
+            if (it >= kPkKStages)
+              ok = mbar_wait(smem_addr(&sh.k_empty[ks]), static_cast<uint32_t>((it / kPkKStages - 1) & 1));
+            if (!ok) break;
+            const uint32_t kb = smem_addr(&sh.k_full[ks]);
+            mbar_arrive_expect_tx(kb, kPkTileBytes);
+            tma_load_3d(k_ptr(ks), &tmK, kb, 0, x.kv, row);
+            tma_load_3d(k_ptr(ks) + kPkPanelBytes, &tmK, kb, 64, x.kv, row);
+            if (j == 0) {  // the queries, once every S of the unit before has read its own
+              if (queries > 0) ok = mbar_wait(smem_addr(&sh.q_empty), static_cast<uint32_t>((queries - 1) & 1));
+              if (!ok) break;
+              const uint32_t qb = smem_addr(&sh.q_full);
+              mbar_arrive_expect_tx(qb, 2u * 2u * 64u * 2u * static_cast<uint32_t>(p.G * p.Tt));
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t qd = smem_addr(smem) + i * kPkTileBytes;
+                tma_load_3d(qd, &tmQ, qb, 0, x.kv * p.G, x.q0 + i * p.Tt);
+                tma_load_3d(qd + kPkPanelBytes, &tmQ, qb, 64, x.kv * p.G, x.q0 + i * p.Tt);
+              }
+              ++queries;
+            }
+            if (it >= kPkVStages)
+              ok = mbar_wait(smem_addr(&sh.v_empty[vs]), static_cast<uint32_t>((it / kPkVStages - 1) & 1));
+            if (!ok) break;
+            const uint32_t vb = smem_addr(&sh.v_full[vs]);
+            mbar_arrive_expect_tx(vb, kPkTileBytes);
+            tma_load_3d(v_ptr(vs), &tmV, vb, 0, x.kv, row);
+            tma_load_3d(v_ptr(vs) + kPkPanelBytes, &tmV, vb, 64, x.kv, row);
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok && lane == 0) {
+        flag_error(p.err, GQA_DEVERR_TIMEOUT);
+        // Do not leave while copies into this CTA's shared memory may still be in flight: wait out every
+        // phase that a load was issued for (tile `it` may have its K loads alone).
+        if (queries > 0) (void)mbar_wait(smem_addr(&sh.q_full), static_cast<uint32_t>((queries - 1) & 1));
+        for (int i = (it + 1 > kPkKStages ? it + 1 - kPkKStages : 0); i <= it; ++i)
+          (void)mbar_wait(smem_addr(&sh.k_full[i % kPkKStages]), static_cast<uint32_t>((i / kPkKStages) & 1));
+        for (int i = (it > kPkVStages ? it - kPkVStages : 0); i < it; ++i)
+          (void)mbar_wait(smem_addr(&sh.v_full[i % kPkVStages]), static_cast<uint32_t>((i / kPkVStages) & 1));
+      }
+    } else if (warp == kPkCheckWarp) {
+      // ---------------------------------------------------------------- values that some rows must not see
+      // Behind the first query's last key a row of V is seen by some rows of the unit or by none (the
+      // sequence's end): P is 0 there, but 0 x inf is not.  Those behind the end are cleared, and so is a
+      // value that is not finite before it, which the epilogue gives to the rows that see it.
+      int it = 0;
+      for (int u = 0; ok; ++u) {
+        PackedUnit x;
+        ok = __all_sync(0xffffffffu, take_unit(u, x));
+        if (!ok || x.tokens == 0) break;
+        const int nt = max(x.nt[0], x.nt[1]), slot = u % kPkSlots;
+        bool bad = false;
+        for (int j = 0; j < nt; ++j, ++it) {
+          const int vs = it % kPkVStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.v_full[vs]), static_cast<uint32_t>((it / kPkVStages) & 1)));
+          if (!ok) break;
+          const int r0 = max(0, max(x.see0, 0) - j * kPkKeys), r1 = x.keys - j * kPkKeys;  // rows from r0 on; the end
+          if (r0 < kPkKeys) {
+            uint4 *tile = reinterpret_cast<uint4 *>(smem + kPkOffV + vs * kPkTileBytes);
+#pragma unroll 4
+            for (int c = r0 * 16 + lane; c < kPkKeys * 16; c += 32) {  // 16-byte chunks: row, panel, chunk
+              const int row = c >> 4;
+              uint4 *at = tile + ((c & 8) << 7) + row * 8 + (c & 7);
+              if (row >= r1) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 y = *at;
+              // an exponent of all ones carries into the sign's place
+              const uint32_t ones = (((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                                     ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u)) &
+                                    0x80008000u;
+              if (ones) {
+                uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+                  if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
+                }
+                *at = make_uint4(z[0], z[1], z[2], z[3]);
+                bad = true;
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean[vs]));
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+          if (bad) sh.unit[slot].bad = 1;
+          mbar_arrive(smem_addr(&sh.unit_checked[slot]));
+          mbar_arrive(smem_addr(&sh.unit_empty[slot]));
+        }
+      }
+      if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+    } else if (lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer of a stream
+      // S_0, then for each tile the two halves of P V and the next S: S overwrites P, and the tensor pipe runs
+      // what a thread issues in order.
+      constexpr uint32_t kIdS = idesc_bf16_f32(kPkRows, kPkKeys, false, false);
+      constexpr uint32_t kIdO = idesc_bf16_f32(kPkRows, kHeadDim, false, true);
+      const int st = warp - kPkMmaWarp;
+      const uint32_t tm = tmem + st * kPkTmemStream;
+      const uint64_t qd = sdesc_sw128(smem_addr(smem) + st * kPkTileBytes, 16, 1024), kd0 = sdesc_sw128(k_ptr(0), 16, 1024),
+                     vd0 = sdesc_sw128(v_ptr(0), kPkPanelBytes, 1024);
+      int it = 0, is = 0, queries = 0, mine = 0;  // key tiles of the CTA, of the stream; units with tiles; with the stream's
+      for (int u = 0; ok; ++u) {
+        PackedUnit x;
+        ok = take_unit(u, x);
+        if (!ok || x.tokens == 0) break;
+        mbar_arrive(smem_addr(&sh.unit_empty[u % kPkSlots]));
+        const int n0 = max(x.nt[0], x.nt[1]), nt = st ? x.nt[1] : x.nt[0];
+        if (n0 == 0) continue;
+        ok = mbar_wait(smem_addr(&sh.q_full), static_cast<uint32_t>(queries++ & 1));
+        for (int j = 0; j <= nt && ok; ++j) {
+          if (j > 0) {  // P V of tile j - 1
+            const int t = it + j - 1, vs = t % kPkVStages;
+            ok = mbar_wait(smem_addr(&sh.v_clean[vs]), static_cast<uint32_t>((t / kPkVStages) & 1));
+            if (ok && j == 1 && mine > 0)  // the O of the unit before has been read
+              ok = mbar_wait(smem_addr(&sh.o_free[st]), static_cast<uint32_t>((mine - 1) & 1));
+            const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (kPkTileBytes / 16));
+            for (int half = 0; half < 2 && ok; ++half) {
+              ok = mbar_wait(smem_addr(&sh.p_full[st][half]), static_cast<uint32_t>((is - 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // 16 keys each
+                umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
+                             j > 1 || half > 0 || k > 0 ? 1u : 0u);
+            }
+            if (!ok) break;
+            umma_commit(smem_addr(&sh.v_empty[vs]));
+          }
+          if (j < nt) {
+            const int t = it + j, ks = t % kPkKStages;
+            ok = mbar_wait(smem_addr(&sh.k_full[ks]), static_cast<uint32_t>((t / kPkKStages) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (kPkTileBytes / 16));
+#pragma unroll
+            for (int k = 0; k < kHeadDim / 16; ++k)
+              umma_bf16(tm, qd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
+                        kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
+            umma_commit(smem_addr(&sh.s_full[st]));
+            umma_commit(smem_addr(&sh.k_empty[ks]));
+            ++is;
+            if (j + 1 == nt) umma_commit(smem_addr(&sh.q_empty));
+          }
+        }
+        if (!ok) break;
+        if (nt > 0) {
+          umma_commit(smem_addr(&sh.o_full[st]));
+          ++mine;
+        } else {
+          mbar_arrive(smem_addr(&sh.q_empty));
+        }
+        for (int j = nt; j < n0 && ok; ++j) {  // tiles that the other stream alone uses
+          const int t = it + j, ks = t % kPkKStages, vs = t % kPkVStages;
+          ok = mbar_wait(smem_addr(&sh.k_full[ks]), static_cast<uint32_t>((t / kPkKStages) & 1));
+          if (ok) mbar_arrive(smem_addr(&sh.k_empty[ks]));
+          if (ok) ok = mbar_wait(smem_addr(&sh.v_full[vs]), static_cast<uint32_t>((t / kPkVStages) & 1));
+          if (ok) mbar_arrive(smem_addr(&sh.v_empty[vs]));
+        }
+        it += n0;
+      }
+      if (!ok) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      if (is > 0) {  // nothing is deallocated while an MMA runs
+        umma_commit(smem_addr(&sh.drain[st]));
+        if (!mbar_wait(smem_addr(&sh.drain[st]), 0)) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax warps of a stream
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPkRegsSoftmax));
+    const int st = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int tl = row / p.G, g = row - tl * p.G;
+    const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + st * kPkTmemStream;
+    int is = 0, mine = 0;  // key tiles of the stream, units with any
+    for (int u = 0; ok; ++u) {
+      PackedUnit x;
+      ok = __all_sync(0xffffffffu, take_unit(u, x));
+      if (!ok || x.tokens == 0) break;
+      const int slot = u % kPkSlots, nt = st ? x.nt[1] : x.nt[0];
+      const int token = st * p.Tt + tl;
+      const bool valid = tl < p.Tt && token < x.tokens;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      const int sees = valid ? max(0, min(x.keys, x.see0 + (p.causal ? token : 0))) : 0;
+      const int all_see = x.see0 + (p.causal ? st * p.Tt : 0);  // keys that every row of the tile sees
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < nt; ++j, ++is) {
+        ok = mbar_wait(smem_addr(&sh.s_full[st]), static_cast<uint32_t>(is & 1));
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (!warp_valid) {  // what P holds in these rows reaches no output
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sh.p_full[st][0]));
+            mbar_arrive(smem_addr(&sh.p_full[st][1]));
+          }
+          continue;
+        }
+        tc_fence_after();
+        float sv[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tm + 32 * c, sv[c]);
+        tmem_wait_ld();
+        if ((j + 1) * kPkKeys > all_see) {
+          const int left = sees - j * kPkKeys;
+#pragma unroll
+          for (int c = 0; c < kPkKeys; ++c) sv[c >> 5][c & 31] = c < left ? sv[c >> 5][c & 31] : -INFINITY;
+        }
+        float m4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          m4[c] = max3(sv[c][0], sv[c][1], sv[c][2]);
+#pragma unroll
+          for (int e = 3; e < 31; e += 2) m4[c] = max3(m4[c], sv[c][e], sv[c][e + 1]);
+          m4[c] = fmaxf(m4[c], sv[c][31]);
+        }
+        const float m_new = max3(m_run, fmaxf(m4[0], m4[1]) * p.scale_log2, fmaxf(m4[2], m4[3]) * p.scale_log2);
+        float corr = 1.f;
+        bool resc = false;
+        if (m_new > m_run + kPkRescaleLog2) {
+          corr = fast_exp2(m_run - m_new);  // 0 before the row's first seen key
+          m_run = m_new;
+          l_run *= corr;
+          resc = j > 0;
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 32) {
+            float o[32];
+            tmem_ld32(tm + kPkTmemO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= corr;
+            tmem_st32(tm + kPkTmemO + c, o);
+          }
+        }
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen no key yet: P = 0
+        const f2 scale2 = make_f2(p.scale_log2, p.scale_log2), neg2 = make_f2(neg_m, neg_m);
+        f2 rs[4] = {{0}, {0}, {0}, {0}};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t ph[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int at = 64 * half + 2 * c;
+            float v0, v1;
+            split_f2(fma_f2(make_f2(sv[at >> 5][at & 31], sv[at >> 5][(at & 31) + 1]), scale2, neg2), v0, v1);
+            v0 = fast_exp2(v0);
+            v1 = fast_exp2(v1);
+            ph[c] = pack_bf16(v0, v1);
+            rs[c & 3] = add_f2(rs[c & 3], make_f2(bf16_lo_to_float(ph[c]), bf16_hi_to_float(ph[c])));
+          }
+          tmem_st32(tm + 32 * half, ph);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[st][half]));
+        }
+        float l0, l1;
+        split_f2(add_f2(add_f2(rs[0], rs[1]), add_f2(rs[2], rs[3])), l0, l1);
+        l_run += l0 + l1;
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------------- the unit's rows
+      if (nt > 0) {
+        ok = mbar_wait(smem_addr(&sh.o_full[st]), static_cast<uint32_t>(mine & 1));
+        ++mine;
+      }
+      ok = ok && mbar_wait(smem_addr(&sh.unit_checked[slot]), static_cast<uint32_t>((u / kPkSlots) & 1));
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const bool bad = *reinterpret_cast<volatile uint32_t *>(&sh.unit[slot].bad) != 0;
+      if (warp_valid) {
+        tc_fence_after();
+        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // (NaN stays NaN)
+        uint16_t *dst = p.out + (static_cast<long long>(x.q0 + token) * p.Hq + x.kv * p.G + g) * kHeadDim;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 32) {
+          float o[32];
+          if (nt > 0) {
+            tmem_ld32(tm + kPkTmemO + c, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = l_run != 0.f ? o[e] * inv : 0.f;
+          if (valid) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = pack_bf16(o[16 * i + 2 * e], o[16 * i + 2 * e + 1]);
+              store_32b(dst + c + 16 * i, y, p.out_wide);
+            }
+          }
+        }
+        if (bad && valid) packed_add_nonfinite(p, x.k0, x.kv, max(0, x.see0), sees, dst, inv);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (nt > 0) mbar_arrive(smem_addr(&sh.o_free[st]));
+        mbar_arrive(smem_addr(&sh.unit_empty[slot]));
+      }
+    }
+    if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+  }
+
+  // ------------------------------------------------------------------ teardown
+  __syncwarp();  // the MMA warps ran their loops on lane 0 alone
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPkMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kPkTmemCols);
+  }
+}
+
+// --------------------------------------------------------------------------------- host side
+
+namespace {
+
+constexpr int kPkMaxDevices = 64;
+std::atomic<int> g_packed_sms[kPkMaxDevices];  // 0: the kernel is not configured on the device yet
+
+gqa_status_t packed_device(int device, int *sms) {
+  if (device >= kPkMaxDevices) return GQA_ERR_UNSUPPORTED;
+  *sms = g_packed_sms[device].load(std::memory_order_acquire);
+  if (*sms > 0) return GQA_OK;
+  int n = 0;
+  if (cudaFuncSetAttribute(packed_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPkSmemBytes) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  g_packed_sms[device].store(n, std::memory_order_release);
+  *sms = n;
+  return GQA_OK;
+}
+
+// Packed rows viewed as [N][H][128] with a stride of `stride` elements; box = 64 dims x heads x tokens.
+bool packed_map(CUtensorMap *m, const void *base, int tokens, int heads, long long stride, int box_heads, int box_tokens) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  return encode_bf16_map(m, 3, base, dims, strides, box);
+}
+
+}  // namespace
+
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" gqa_status_t gqa_packed_attn(const gqa_packed_desc_t *desc, const void *q, const void *k, const void *v,
+                                        const int32_t *q_offsets, const int32_t *k_offsets, void *out,
+                                        uint32_t *device_errors, void *stream) {
+  if (!desc) return GQA_ERR_INVALID_ARG;
+  const gqa_packed_desc_t d = *desc;
+  gqa_status_t st = check_cache_geometry(d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, 1, 0, 1, 0);
+  if (st != GQA_OK) return st;
+  if (d.num_queries < 1 || d.num_keys < 1) return GQA_ERR_INVALID_ARG;
+  const long long dense_q = static_cast<long long>(d.num_q_heads) * kHeadDim, dense_k = static_cast<long long>(d.num_kv_heads) * kHeadDim;
+  if ((d.q_stride && (d.q_stride < dense_q || d.q_stride % 8)) || (d.k_stride && (d.k_stride < dense_k || d.k_stride % 8)) ||
+      (d.v_stride && (d.v_stride < dense_k || d.v_stride % 8)))
+    return GQA_ERR_INVALID_ARG;
+  if (static_cast<long long>(d.num_queries) * d.num_q_heads > 0x7fffffffLL ||
+      static_cast<long long>(d.num_keys) * d.num_kv_heads > 0x7fffffffLL || dense_q > 0x7fffffffLL)
+    return GQA_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !q_offsets || !out) return GQA_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) || !aligned_to(q_offsets, 4) ||
+      !aligned_to(k_offsets, 4) || !aligned_to(device_errors, 4))
+    return GQA_ERR_INVALID_ARG;
+  st = check_device(d.device);
+  if (st != GQA_OK) return st;
+  DeviceGuard guard(d.device);
+  if (!guard.ok) return GQA_ERR_CUDA;
+  int sms = 0;
+  st = packed_device(d.device, &sms);
+  if (st != GQA_OK) return st;
+
+  PackedParams p;
+  memset(&p, 0, sizeof p);
+  p.q_offsets = q_offsets;
+  p.k_offsets = k_offsets ? k_offsets : q_offsets;
+  p.v = static_cast<const uint16_t *>(v);
+  p.v_stride = d.v_stride ? d.v_stride : dense_k;
+  p.out = static_cast<uint16_t *>(out);
+  p.err = device_errors;
+  p.B = d.batch;
+  p.Nq = d.num_queries;
+  p.Nk = d.num_keys;
+  p.Hq = d.num_q_heads;
+  p.Hkv = d.num_kv_heads;
+  p.G = d.num_q_heads / d.num_kv_heads;
+  p.Tt = kPkRows / p.G;
+  p.causal = d.causal ? 1 : 0;
+  p.out_wide = aligned_to(out, 32) ? 1 : 0;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(kHeadDim)));
+  CUtensorMap tq, tk, tv;
+  if (!packed_map(&tq, q, p.Nq, p.Hq, d.q_stride ? d.q_stride : dense_q, p.G, p.Tt) ||
+      !packed_map(&tk, k, p.Nk, p.Hkv, d.k_stride ? d.k_stride : dense_k, 1, kPkKeys) ||
+      !packed_map(&tv, v, p.Nk, p.Hkv, p.v_stride, 1, kPkKeys))
+    return GQA_ERR_CUDA;
+  // units at most: every sequence ends one
+  const long long units = (static_cast<long long>(p.Nq) / (2 * p.Tt) + p.B) * p.Hkv;
+  if (launch_pdl(packed_attn_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kPkThreads),
+                 static_cast<size_t>(kPkSmemBytes), static_cast<cudaStream_t>(stream), tq, tk, tv, p) != cudaSuccess) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  return GQA_OK;
+}

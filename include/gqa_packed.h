@@ -1,0 +1,71 @@
+/*
+ * gqa_packed.h -- attention over prompts of different lengths, packed one behind the other
+ * (libgqa_decode.so).
+ *
+ * The queries of B sequences lie in one [N_q, H_q, 128] tensor, their keys and values in [N_k, H_kv, 128]
+ * tensors, without padding.  Sequence b has n_b queries and m_b keys.  The two end at the same token:
+ * query i stands at position i + m_b - n_b and sees, if causal, the keys j <= i + m_b - n_b (none where
+ * that is negative), else all m_b.  With m_b = n_b that is a whole prompt; with m_b > n_b the chunk of a
+ * prompt that goes on over a prefix (rows that gqa_q8_read has brought back from a cache, for one).
+ *
+ * Conventions are those of gqa_decode.h (bf16 as 16-bit storage, bf16 tensors 16-byte and int32 ones
+ * 4-byte aligned, asynchronous on `stream`, argument errors before any launch, device-side index
+ * errors as GQA_DEVERR_* bits).  Nothing is allocated, no workspace is needed and no state is kept between
+ * calls besides the kernel's one-time configuration per device (make a first call before capturing
+ * a graph).  The kernel is launched with programmatic stream serialization but reads and writes nothing
+ * before the preceding kernel has completed, and never lets the next one start early.
+ */
+#ifndef GQA_PACKED_H_
+#define GQA_PACKED_H_
+
+#include "gqa_decode.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Shapes and layout of one call. */
+typedef struct gqa_packed_desc {
+    int batch;        /* B, 1..GQA_MAX_BATCH */
+    int num_q_heads;  /* H_q */
+    int num_kv_heads; /* H_kv; H_q % H_kv == 0 and G = H_q / H_kv <= 16 */
+    int head_dim;     /* d; must be 128 */
+    int num_queries;  /* N_q >= 1 */
+    int num_keys;     /* N_k >= 1 */
+    int causal;       /* non-zero: the mask above; 0: every query sees all its sequence's keys */
+    int device;       /* CUDA device ordinal the call runs on */
+    int q_stride;     /* elements between the rows of consecutive tokens of q, k and v: */
+    int k_stride;     /*   0 for dense (H * 128), else a multiple of 8 >= H * 128, as in one */
+    int v_stride;     /*   [N, (H_q + 2 H_kv) * 128] projection that holds all three */
+} gqa_packed_desc_t;
+
+/*
+ * gqa_packed_attn -- softmax(q . K / sqrt(128)) V over each sequence's own keys.
+ *   q          [N_q, H_q, 128] bf16 device   rotated queries; a token's heads are dense
+ *   k, v       [N_k, H_kv, 128] bf16 device   query head h reads KV head h / G
+ *   q_offsets  [B + 1] int32 device, ascending, 0 <= q_offsets[0], q_offsets[B] <= N_q: rows q_offsets[b] ..
+ *              q_offsets[b + 1] - 1 are sequence b's queries
+ *   k_offsets  [B + 1] int32 device, likewise over N_k; NULL for q_offsets
+ *   out        [N_q, H_q, 128] bf16 device, dense; zeros for a query that sees no key (or whose
+ *              every score is -infinity); rows that belong to no sequence are left as they were.  Must
+ *              not overlap any input.
+ *   device_errors   optional device pointer to a uint32.  A sequence whose q_offsets descend, are negative or
+ *              pass N_q (GQA_DEVERR_SEQLEN) is left out: its rows stay as they were; one whose k_offsets
+ *              do (GQA_DEVERR_SEQLEN) counts as one without keys.
+ * Keys and values that a query does not see have no effect on it whatever they hold (NaN and infinities
+ * included).  A value that is not finite makes that dim of every query that sees it infinite or NaN, however
+ * small its weight.  The rounding of the result does not depend on timing or on the other sequences of
+ * the batch: the same inputs give the same bits.
+ * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, bad sizes or strides), GQA_ERR_UNSUPPORTED
+ * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, B > GQA_MAX_BATCH, more than 2^31 - 1 rows N_q H_q or
+ * N_k H_kv), GQA_ERR_CUDA.
+ */
+gqa_status_t gqa_packed_attn(const gqa_packed_desc_t *desc, const void *q, const void *k, const void *v,
+                             const int32_t *q_offsets, const int32_t *k_offsets, void *out, uint32_t *device_errors,
+                             void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GQA_PACKED_H_ */
