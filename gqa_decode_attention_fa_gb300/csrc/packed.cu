@@ -10,15 +10,14 @@
 // KV heads, and dealt to the CTAs, one an SM, to and fro; the numbering follows from the lengths, which are read on the
 // device: the units with at least D key tiles are counted in closed form for each sequence.
 //
-// A CTA: a TMA warp finds the units, tells the others and streams Q, K and V; two streams of an MMA warp and
-// four softmax warps each hold a tile, so that one stream's softmax overlaps the other's products; a warp
-// looks over the values that some rows must not see.  A stream's S = Q K^T (128 x 128) and its O += P V lie in tensor
+// A CTA: a TMA warp finds the units, tells the others and streams Q, K and V; two streams of four softmax
+// warps hold a tile each and an MMA warp serves them in turn, so that one stream's softmax overlaps the other's
+// products; a warp looks over the values that some rows must not see.  A stream's S = Q K^T (128 x 128) and its O += P V lie in tensor
 // memory, P over S as bf16 pairs in two halves, the first multiplied while the second is made.  A softmax thread holds a
 // row.  The maximum is raised lazily (by more than 2^8), so most tiles rescale nothing; S of a tile is issued behind P V of
 // the one before, so a thread that sees S finds O at rest.
-//   P is rounded to bf16 (2^-8 of a weight, and the sum takes the rounded ones): over the keys that adds about as
-// much to a row as the output's own rounding; a second term for what is cut would add half to the
-// products.
+//   P is rounded to bf16 (at most 2^-8 of a weight): over the keys that adds about as much to a row as the
+// output's own rounding; a second term for what is cut would add half to the products.
 #include <math.h>
 #include <string.h>
 
@@ -47,7 +46,7 @@ namespace {
 
 constexpr int kPkRows = 128;
 constexpr int kPkKeys = 128;
-constexpr int kPkMmaWarp = 8;  // and 9: a stream's each
+constexpr int kPkMmaWarp = 8;
 constexpr int kPkProducerWarp = 10;
 constexpr int kPkCheckWarp = 11;
 constexpr int kPkThreads = 32 * 12;
@@ -79,12 +78,12 @@ struct PackedUnit {
 
 struct PackedShared {
   uint64_t k_full[kPkKStages], k_empty[kPkKStages], v_full[kPkVStages], v_clean[kPkVStages], v_empty[kPkVStages];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain[2], q_full, q_empty;
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, q_full, q_empty;
   uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_checked[kPkSlots];
   PackedUnit unit[kPkSlots];
   uint32_t tmem;
 };
-constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 6 + 2 + 3 * kPkSlots;
+constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 2 + 3 * kPkSlots;
 constexpr int kPkSmemBytes = kPkOffBar + static_cast<int>(sizeof(PackedShared));
 static_assert(kPkSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
@@ -237,9 +236,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     for (int i = lane; i < kPkNumBars; i += 32) {
       uint64_t *bar = bars + i;
       int count = 1;
-      if ((bar >= sh.k_empty && bar < sh.v_full) || (bar >= sh.v_empty && bar < sh.s_full) || bar == &sh.q_empty) count = 2;
-      if ((bar >= sh.p_full[0] && bar < sh.o_full) || (bar >= sh.o_free && bar < sh.drain)) count = 4;
-      if (bar >= sh.unit_empty && bar < sh.unit_checked) count = 11;  // every warp but the producer
+      if ((bar >= sh.p_full[0] && bar < sh.o_full) || (bar >= sh.o_free && bar < &sh.drain)) count = 4;
+      if (bar >= sh.unit_empty && bar < sh.unit_checked) count = 10;  // softmax, MMA and check warps
       mbar_init(smem_addr(bar), count);
     }
     fence_barrier_init();
@@ -407,80 +405,76 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         }
       }
       if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
-    } else if (lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer of a stream
-      // S_0, then for each tile the two halves of P V and the next S: S overwrites P, and the tensor pipe runs
-      // what a thread issues in order.
+    } else if (warp == kPkMmaWarp && lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      // For each key tile, of stream 0 and then of stream 1: P V of the tile before, in two halves, and S, which
+      // overwrites P; the tensor pipe runs what a thread issues in order.  One thread for both streams
+      // keeps them half a tile apart: with an issuer each they fell into step, the tensor core idle while both
+      // made their P (two chunks of 6000 tokens over prefixes 1616 us).  A commit holds the pipe up, so
+      // there is one to a stream and tile, and the softmax warps that see it give the tiles back.
       constexpr uint32_t kIdS = idesc_bf16_f32(kPkRows, kPkKeys, false, false);
       constexpr uint32_t kIdO = idesc_bf16_f32(kPkRows, kHeadDim, false, true);
-      const int st = warp - kPkMmaWarp;
-      const uint32_t tm = tmem + st * kPkTmemStream;
-      const uint64_t qd = sdesc_sw128(smem_addr(smem) + st * kPkTileBytes, 16, 1024), kd0 = sdesc_sw128(k_ptr(0), 16, 1024),
+      const uint64_t qd0 = sdesc_sw128(smem_addr(smem), 16, 1024), kd0 = sdesc_sw128(k_ptr(0), 16, 1024),
                      vd0 = sdesc_sw128(v_ptr(0), kPkPanelBytes, 1024);
-      int it = 0, is = 0, queries = 0, mine = 0;  // key tiles of the CTA, of the stream; units with tiles; with the stream's
+      int it = 0, queries = 0;                  // key tiles, units with tiles
+      uint32_t phase_p[2] = {0, 0}, mine[2] = {0, 0};  // P made so far (mod 2), units of a stream with tiles
+      bool issued = false;
       for (int u = 0; ok; ++u) {
         PackedUnit x;
         ok = take_unit(u, x);
         if (!ok || x.tokens == 0) break;
         mbar_arrive(smem_addr(&sh.unit_empty[u % kPkSlots]));
-        const int n0 = max(x.nt[0], x.nt[1]), nt = st ? x.nt[1] : x.nt[0];
+        const int n0 = max(x.nt[0], x.nt[1]);
         if (n0 == 0) continue;
         ok = mbar_wait(smem_addr(&sh.q_full), static_cast<uint32_t>(queries++ & 1));
-        for (int j = 0; j <= nt && ok; ++j) {
-          if (j > 0) {  // P V of tile j - 1
-            const int t = it + j - 1, vs = t % kPkVStages;
-            ok = mbar_wait(smem_addr(&sh.v_clean[vs]), static_cast<uint32_t>((t / kPkVStages) & 1));
-            if (ok && j == 1 && mine > 0)  // the O of the unit before has been read
-              ok = mbar_wait(smem_addr(&sh.o_free[st]), static_cast<uint32_t>((mine - 1) & 1));
-            const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (kPkTileBytes / 16));
-            for (int half = 0; half < 2 && ok; ++half) {
-              ok = mbar_wait(smem_addr(&sh.p_full[st][half]), static_cast<uint32_t>((is - 1) & 1));
+        for (int j = 0; j <= n0 && ok; ++j) {
+          const int tv = it + j - 1, vs = tv % kPkVStages, tk = it + j, ks = tk % kPkKStages;
+          if (j > 0) ok = mbar_wait(smem_addr(&sh.v_clean[vs]), static_cast<uint32_t>((tv / kPkVStages) & 1));
+          if (ok && j < n0) ok = mbar_wait(smem_addr(&sh.k_full[ks]), static_cast<uint32_t>((tk / kPkKStages) & 1));
+          if (!ok) break;
+          const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (kPkTileBytes / 16));
+          const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (kPkTileBytes / 16));
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const uint32_t tm = tmem + st * kPkTmemStream;
+            const int nt = x.nt[st];
+            if (j > 0 && j <= nt) {
+              if (j == 1 && mine[st] > 0)  // the O of the unit before has been read
+                ok = ok && mbar_wait(smem_addr(&sh.o_free[st]), (mine[st] - 1) & 1);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                ok = ok && mbar_wait(smem_addr(&sh.p_full[st][half]), phase_p[st]);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // 16 keys each
+                  umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
+                               j > 1 || half > 0 || k > 0 ? 1u : 0u);
+              }
               if (!ok) break;
+              phase_p[st] ^= 1;
+              if (j == nt) {
+                umma_commit(smem_addr(&sh.o_full[st]));
+                ++mine[st];
+              }
+            }
+            if (j < nt) {
               tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)  // 16 keys each
-                umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
-                             j > 1 || half > 0 || k > 0 ? 1u : 0u);
+              for (int k = 0; k < kHeadDim / 16; ++k)
+                umma_bf16(tm, qd0 + st * (kPkTileBytes / 16) + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
+                          kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
+              umma_commit(smem_addr(&sh.s_full[st]));
+              issued = true;
             }
-            if (!ok) break;
-            umma_commit(smem_addr(&sh.v_empty[vs]));
           }
-          if (j < nt) {
-            const int t = it + j, ks = t % kPkKStages;
-            ok = mbar_wait(smem_addr(&sh.k_full[ks]), static_cast<uint32_t>((t / kPkKStages) & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (kPkTileBytes / 16));
-#pragma unroll
-            for (int k = 0; k < kHeadDim / 16; ++k)
-              umma_bf16(tm, qd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
-                        kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
-            umma_commit(smem_addr(&sh.s_full[st]));
-            umma_commit(smem_addr(&sh.k_empty[ks]));
-            ++is;
-            if (j + 1 == nt) umma_commit(smem_addr(&sh.q_empty));
-          }
-        }
-        if (!ok) break;
-        if (nt > 0) {
-          umma_commit(smem_addr(&sh.o_full[st]));
-          ++mine;
-        } else {
-          mbar_arrive(smem_addr(&sh.q_empty));
-        }
-        for (int j = nt; j < n0 && ok; ++j) {  // tiles that the other stream alone uses
-          const int t = it + j, ks = t % kPkKStages, vs = t % kPkVStages;
-          ok = mbar_wait(smem_addr(&sh.k_full[ks]), static_cast<uint32_t>((t / kPkKStages) & 1));
-          if (ok) mbar_arrive(smem_addr(&sh.k_empty[ks]));
-          if (ok) ok = mbar_wait(smem_addr(&sh.v_full[vs]), static_cast<uint32_t>((t / kPkVStages) & 1));
-          if (ok) mbar_arrive(smem_addr(&sh.v_empty[vs]));
         }
         it += n0;
       }
       if (!ok) flag_error(p.err, GQA_DEVERR_TIMEOUT);
-      if (is > 0) {  // nothing is deallocated while an MMA runs
-        umma_commit(smem_addr(&sh.drain[st]));
-        if (!mbar_wait(smem_addr(&sh.drain[st]), 0)) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      if (issued) {  // nothing is deallocated while an MMA runs
+        umma_commit(smem_addr(&sh.drain));
+        if (!mbar_wait(smem_addr(&sh.drain), 0)) flag_error(p.err, GQA_DEVERR_TIMEOUT);
       }
     }
   } else {
@@ -490,7 +484,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const int tl = row / p.G, g = row - tl * p.G;
     const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + st * kPkTmemStream;
-    int is = 0, mine = 0;  // key tiles of the stream, units with any
+    int is = 0, it0 = 0, mine = 0;  // key tiles of the stream, of the CTA before the unit; units with any of the stream's
     for (int u = 0; ok; ++u) {
       PackedUnit x;
       ok = __all_sync(0xffffffffu, take_unit(u, x));
@@ -501,12 +495,21 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const int sees = valid ? max(0, min(x.keys, x.see0 + (p.causal ? token : 0))) : 0;
       const int all_see = x.see0 + (p.causal ? st * p.Tt : 0);  // keys that every row of the tile sees
+      // The unit's tiles are given back by the stream that has S and P V of a tile behind the other's: the later one, if
+      // it has any tile (it has at least as many as the other then).
+      const int n0 = max(x.nt[0], x.nt[1]);
+      const bool gives = (warp & 3) == 0 && lane == 0 && st == (x.nt[1] > 0 ? 1 : 0);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nt; ++j, ++is) {
         ok = mbar_wait(smem_addr(&sh.s_full[st]), static_cast<uint32_t>(is & 1));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
+        }
+        if (gives) {
+          mbar_arrive(smem_addr(&sh.k_empty[(it0 + j) % kPkKStages]));
+          if (j > 0) mbar_arrive(smem_addr(&sh.v_empty[(it0 + j - 1) % kPkVStages]));
+          if (j + 1 == nt) mbar_arrive(smem_addr(&sh.q_empty));
         }
         if (!warp_valid) {  // what P holds in these rows reaches no output
           __syncwarp();
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
             v0 = fast_exp2(v0);
             v1 = fast_exp2(v1);
             ph[c] = pack_bf16(v0, v1);
-            rs[c & 3] = add_f2(rs[c & 3], make_f2(bf16_lo_to_float(ph[c]), bf16_hi_to_float(ph[c])));
+            rs[c & 3] = add_f2(rs[c & 3], make_f2(v0, v1));
           }
           tmem_st32(tm + 32 * half, ph);
           tmem_wait_st();
@@ -585,7 +588,9 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       if (nt > 0) {
         ok = mbar_wait(smem_addr(&sh.o_full[st]), static_cast<uint32_t>(mine & 1));
         ++mine;
+        if (ok && gives) mbar_arrive(smem_addr(&sh.v_empty[(it0 + nt - 1) % kPkVStages]));
       }
+      it0 += n0;
       ok = ok && mbar_wait(smem_addr(&sh.unit_checked[slot]), static_cast<uint32_t>((u / kPkSlots) & 1));
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
