@@ -87,6 +87,12 @@ constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 2 + 3 *
 constexpr int kPkSmemBytes = kPkOffBar + static_cast<int>(sizeof(PackedShared));
 static_assert(kPkSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
+// True in one lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -405,13 +411,15 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         }
       }
       if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
-    } else if (warp == kPkMmaWarp && lane == 0) {
+    } else if (warp == kPkMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
       // For each key tile, of stream 0 and then of stream 1: P V of the tile before, in two halves, and S, which
       // overwrites P; the tensor pipe runs what a thread issues in order.  One thread for both streams
       // keeps them half a tile apart: with an issuer each they fell into step, the tensor core idle while both
       // made their P (two chunks of 6000 tokens over prefixes 1616 us).  A commit holds the pipe up, so
       // there is one to a stream and tile, and the softmax warps that see it give the tiles back.
+      //   The whole warp walks, on values that are known to be alike in its lanes, so that descriptors are made in
+      // uniform registers; one lane issues.
       constexpr uint32_t kIdS = idesc_bf16_f32(kPkRows, kPkKeys, false, false);
       constexpr uint32_t kIdO = idesc_bf16_f32(kPkRows, kHeadDim, false, true);
       const uint64_t qd0 = sdesc_sw128(smem_addr(smem), 16, 1024), kd0 = sdesc_sw128(k_ptr(0), 16, 1024),
@@ -421,10 +429,12 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       bool issued = false;
       for (int u = 0; ok; ++u) {
         PackedUnit x;
-        ok = take_unit(u, x);
-        if (!ok || x.tokens == 0) break;
-        mbar_arrive(smem_addr(&sh.unit_empty[u % kPkSlots]));
-        const int n0 = max(x.nt[0], x.nt[1]);
+        ok = __all_sync(0xffffffffu, take_unit(u, x));
+        const int tokens = __reduce_max_sync(0xffffffffu, x.tokens);
+        if (!ok || tokens == 0) break;
+        const int tiles[2] = {__reduce_max_sync(0xffffffffu, x.nt[0]), __reduce_max_sync(0xffffffffu, x.nt[1])};
+        if (elect_one()) mbar_arrive(smem_addr(&sh.unit_empty[u % kPkSlots]));
+        const int n0 = max(tiles[0], tiles[1]);
         if (n0 == 0) continue;
         ok = mbar_wait(smem_addr(&sh.q_full), static_cast<uint32_t>(queries++ & 1));
         for (int j = 0; j <= n0 && ok; ++j) {
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             const uint32_t tm = tmem + st * kPkTmemStream;
-            const int nt = x.nt[st];
+            const int nt = tiles[st];
             if (j > 0 && j <= nt) {
               if (j == 1 && mine[st] > 0)  // the O of the unit before has been read
                 ok = ok && mbar_wait(smem_addr(&sh.o_free[st]), (mine[st] - 1) & 1);
@@ -446,34 +456,39 @@ __global__ void __launch_bounds__(kPkThreads, 1)
                 ok = ok && mbar_wait(smem_addr(&sh.p_full[st][half]), phase_p[st]);
                 if (!ok) break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // 16 keys each
-                  umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
-                               j > 1 || half > 0 || k > 0 ? 1u : 0u);
+                  for (int k = 0; k < 4; ++k)  // 16 keys each
+                    umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
+                                 j > 1 || half > 0 || k > 0 ? 1u : 0u);
+                  if (half == 1 && j == nt) umma_commit(smem_addr(&sh.o_full[st]));
+                }
+                __syncwarp();
               }
               if (!ok) break;
               phase_p[st] ^= 1;
-              if (j == nt) {
-                umma_commit(smem_addr(&sh.o_full[st]));
-                ++mine[st];
-              }
+              if (j == nt) ++mine[st];
             }
             if (j < nt) {
               tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < kHeadDim / 16; ++k)
-                umma_bf16(tm, qd0 + st * (kPkTileBytes / 16) + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
-                          kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
-              umma_commit(smem_addr(&sh.s_full[st]));
+                for (int k = 0; k < kHeadDim / 16; ++k)
+                  umma_bf16(tm, qd0 + st * (kPkTileBytes / 16) + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
+                            kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
+                umma_commit(smem_addr(&sh.s_full[st]));
+              }
+              __syncwarp();
               issued = true;
             }
           }
         }
         it += n0;
       }
-      if (!ok) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+      __syncwarp();
       if (issued) {  // nothing is deallocated while an MMA runs
-        umma_commit(smem_addr(&sh.drain));
+        if (elect_one()) umma_commit(smem_addr(&sh.drain));
         if (!mbar_wait(smem_addr(&sh.drain), 0)) flag_error(p.err, GQA_DEVERR_TIMEOUT);
       }
     }
