@@ -10,7 +10,7 @@
 // KV heads, and dealt to the CTAs, one an SM, to and fro; the numbering follows from the lengths, which are read on the
 // device: the units with at least D key tiles are counted in closed form for each sequence.
 //
-// A CTA: a TMA warp finds the units, tells the others and streams Q, K and V; two streams of four softmax
+// A CTA: a warp finds the units and tells the others, a TMA warp streams Q, K and V; two streams of four softmax
 // warps hold a tile each and an MMA warp serves them in turn, so that one stream's softmax overlaps the other's
 // products; a warp looks over the values that some rows must not see.  A stream's S = Q K^T (128 x 128) and its O += P V lie in tensor
 // memory, P over S as bf16 pairs in two halves, the first multiplied while the second is made.  A softmax thread holds a
@@ -47,6 +47,7 @@ namespace {
 constexpr int kPkRows = 128;
 constexpr int kPkKeys = 128;
 constexpr int kPkMmaWarp = 8;
+constexpr int kPkUnitWarp = 9;
 constexpr int kPkProducerWarp = 10;
 constexpr int kPkCheckWarp = 11;
 constexpr int kPkThreads = 32 * 12;
@@ -58,14 +59,24 @@ constexpr int kPkSlots = 4;  // units told ahead
 constexpr uint32_t kPkTmemStream = 256, kPkTmemO = 128, kPkTmemCols = 512;
 constexpr float kPkRescaleLog2 = 8.f;
 // Registers a thread: 168 at launch; the softmax warpgroups take what the third gives up.
-constexpr int kPkRegsSoftmax = 216, kPkRegsOther = 72;
+constexpr int kPkRegsSoftmax = 200, kPkRegsOther = 104;
 static_assert(2 * kPkRegsSoftmax + kPkRegsOther <= 3 * 168, "registers of the launch");
 
 constexpr int kPkOffK = 2 * kPkTileBytes;
 constexpr int kPkOffV = kPkOffK + kPkKStages * kPkTileBytes;
 constexpr int kPkOffBar = kPkOffV + kPkVStages * kPkTileBytes;
 
-// A unit as the producer tells it.
+// A place in a ring of N stages and the parity of its barriers' phase.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == N) at = 0, phase ^= 1u;
+  }
+};
+
+// A unit as it is told.
 struct PackedUnit {
   int q0, k0;      // packed rows of the unit's first query and of its sequence's first key
   int tokens;      // queries of the unit, up to 2 Tt; 0: no unit is left
@@ -78,12 +89,12 @@ struct PackedUnit {
 
 struct PackedShared {
   uint64_t k_full[kPkKStages], k_empty[kPkKStages], v_full[kPkVStages], v_clean[kPkVStages], v_empty[kPkVStages];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, q_full, q_empty;
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, q_full[2], q_empty[2];
   uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_checked[kPkSlots];
   PackedUnit unit[kPkSlots];
   uint32_t tmem;
 };
-constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 2 + 3 * kPkSlots;
+constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 4 + 3 * kPkSlots;
 constexpr int kPkSmemBytes = kPkOffBar + static_cast<int>(sizeof(PackedShared));
 static_assert(kPkSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
@@ -115,7 +126,8 @@ struct PackedSeq {
   int q0, k0, n, m;
 };
 __device__ __forceinline__ PackedSeq packed_seq(const PackedParams &p, int b) {
-  PackedSeq s;
+  PackedSeq s = {0, 0, 0, 0};
+  if (b >= p.B) return s;
   s.q0 = p.q_offsets[b];
   const int q1 = p.q_offsets[b + 1];
   s.k0 = p.k_offsets[b];
@@ -124,61 +136,79 @@ __device__ __forceinline__ PackedSeq packed_seq(const PackedParams &p, int b) {
   s.m = s.k0 >= 0 && k1 >= s.k0 && k1 <= p.Nk ? k1 - s.k0 : 0;
   return s;
 }
-// Units a KV head of a sequence whose key tiles are at least D.
-__device__ __forceinline__ int units_of_depth(const PackedParams &p, const PackedSeq &s, int D) {
-  const int P = 2 * p.Tt, all = (s.n + P - 1) / P;
+__device__ __forceinline__ int units_of(const PackedParams &p, const PackedSeq &s) {
+  return static_cast<int>(static_cast<unsigned>(s.n + 2 * p.Tt - 1) / static_cast<unsigned>(2 * p.Tt));
+}
+// Units a KV head of a sequence of `all` units whose key tiles are at least D.
+__device__ __forceinline__ int units_of_depth(const PackedParams &p, const PackedSeq &s, int all, int D) {
   if (D <= 0) return all;
   const int need = (D - 1) * kPkKeys + 1;  // keys that the unit's last query has to see
   if (s.m < need) return 0;
   if (!p.causal) return all;
   const int last = need - (s.m - s.n);  // queries, counted from the sequence's first, up to the unit's last
   if (last <= 0) return all;
-  return last > s.n ? 0 : all - (last + P - 1) / P + 1;
+  return last > s.n ? 0 : all - static_cast<int>(static_cast<unsigned>(last - 1) / static_cast<unsigned>(2 * p.Tt));
 }
 
-// Finds units by their number, which grows from call to call.  Every lane of a warp alike.
+// Finds units by their number, which grows from call to call.  Every lane of a warp alike; the lanes keep
+// the first 32 sequences.
 struct PackedWalk {
+  PackedSeq mine;
+  int mine_all;
+  int all;             // units a KV head
+  bool by_depth;       // numbered by their key tiles, else by their sequences
   int D, upto, above;  // units a KV head with at least D key tiles, and with more
   int base, before;    // the 32 sequences looked at, and units of exactly D tiles in those before them
 
   __device__ __forceinline__ int count(const PackedParams &p, int d, int lane) const {
-    int c = 0;
-    for (int b = lane; b < p.B; b += 32) c += units_of_depth(p, packed_seq(p, b), d);
+    int c = units_of_depth(p, mine, mine_all, d);
+    for (int b = 32 + lane; b < p.B; b += 32) {
+      const PackedSeq s = packed_seq(p, b);
+      c += units_of_depth(p, s, units_of(p, s), d);
+    }
     return __reduce_add_sync(0xffffffffu, c);
   }
-  __device__ __forceinline__ void start(const PackedParams &p, int lane) {
-    unsigned most = 0;
-    for (int b = lane; b < p.B; b += 32) most = max(most, static_cast<unsigned>(packed_seq(p, b).m));
-    D = static_cast<int>((__reduce_max_sync(0xffffffffu, most) + kPkKeys - 1) / kPkKeys) + 1;
-    upto = above = base = before = 0;
+  // ctas: where one round takes all units their order does not matter.
+  __device__ __forceinline__ void start(const PackedParams &p, int lane, int ctas) {
+    mine = packed_seq(p, lane);
+    mine_all = units_of(p, mine);
+    unsigned most = static_cast<unsigned>(mine.m);
+    for (int b = 32 + lane; b < p.B; b += 32) most = max(most, static_cast<unsigned>(packed_seq(p, b).m));
+    all = count(p, 0, lane);
+    by_depth = static_cast<long long>(all) * p.Hkv > ctas;
+    D = by_depth ? static_cast<int>((__reduce_max_sync(0xffffffffu, most) + kPkKeys - 1) / kPkKeys) + 1 : 0;
+    upto = by_depth ? 0 : all;
+    above = base = before = 0;
   }
   // The unit of number `at` (a KV head's); false if there are fewer.
   __device__ __forceinline__ bool find(const PackedParams &p, int at, int lane, PackedSeq *seq, int *index) {
+    if (at >= all) return false;
     if (at >= upto) {
-      if (D == 0) return false;
-      int lo = 0, hi = D - 1;  // the largest depth with more than `at` units
-      const int all = count(p, 0, lane);
-      if (at >= all) return false;
+      // the largest depth with more than `at` units: down in growing steps, then between the last two
+      int hi = D - 1, lo = hi, step = 1, c = count(p, lo, lane), c_hi = upto;
+      while (c <= at) {
+        hi = lo - 1;
+        c_hi = c;
+        lo = max(0, lo - step);
+        step *= 2;
+        c = count(p, lo, lane);
+      }
       while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (count(p, mid, lane) > at) lo = mid;
-        else hi = mid - 1;
+        const int mid = (lo + hi + 1) / 2, x = count(p, mid, lane);
+        if (x > at) lo = mid, c = x;
+        else hi = mid - 1, c_hi = x;
       }
       D = lo;
-      upto = count(p, D, lane);
-      above = count(p, D + 1, lane);
+      upto = c;
+      above = c_hi;  // the count at lo + 1, where the search ended
       base = before = 0;
     }
     const int want = at - above;
     for (; base < p.B; base += 32) {
-      PackedSeq s = {0, 0, 0, 0};
-      int c = 0, deeper = 0, all = 0;
-      if (base + lane < p.B) {
-        s = packed_seq(p, base + lane);
-        deeper = units_of_depth(p, s, D + 1);
-        c = units_of_depth(p, s, D) - deeper;
-        all = units_of_depth(p, s, 0);
-      }
+      const PackedSeq s = base == 0 ? mine : packed_seq(p, base + lane);
+      const int mine_units = base == 0 ? mine_all : units_of(p, s);
+      const int deeper = by_depth ? units_of_depth(p, s, mine_units, D + 1) : 0;
+      const int c = units_of_depth(p, s, mine_units, D) - deeper;
       int sum = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -193,8 +223,8 @@ struct PackedWalk {
       const int x = want - before;
       const int who = __ffs(__ballot_sync(0xffffffffu, sum > x)) - 1;
       // units of a sequence get deeper with their index: those of D tiles end where the deeper ones begin
-      const int mine = all - deeper - c + (x - (sum - c));
-      *index = __shfl_sync(0xffffffffu, mine, who);
+      const int i = mine_units - deeper - c + (x - (sum - c));
+      *index = __shfl_sync(0xffffffffu, i, who);
       seq->q0 = __shfl_sync(0xffffffffu, s.q0, who);
       seq->k0 = __shfl_sync(0xffffffffu, s.k0, who);
       seq->n = __shfl_sync(0xffffffffu, s.n, who);
@@ -237,13 +267,13 @@ __global__ void __launch_bounds__(kPkThreads, 1)
   if (warp == kPkMmaWarp) {
     tmem_alloc(smem_addr(&sh.tmem), kPkTmemCols);
     tmem_relinquish();
-  } else if (warp == kPkMmaWarp + 1) {
+  } else if (warp == kPkCheckWarp) {
     uint64_t *bars = sh.k_full;
     for (int i = lane; i < kPkNumBars; i += 32) {
       uint64_t *bar = bars + i;
       int count = 1;
       if ((bar >= sh.p_full[0] && bar < sh.o_full) || (bar >= sh.o_free && bar < &sh.drain)) count = 4;
-      if (bar >= sh.unit_empty && bar < sh.unit_checked) count = 10;  // softmax, MMA and check warps
+      if (bar >= sh.unit_empty && bar < sh.unit_checked) count = 11;  // every warp but the one that finds them
       mbar_init(smem_addr(bar), count);
     }
     fence_barrier_init();
@@ -260,29 +290,28 @@ __global__ void __launch_bounds__(kPkThreads, 1)
 
   auto k_ptr = [&](int s) { return smem_addr(smem) + kPkOffK + s * kPkTileBytes; };
   auto v_ptr = [&](int s) { return smem_addr(smem) + kPkOffV + s * kPkTileBytes; };
-  // The unit told as number u; false when a wait ran out.  Whoever has read a slot gives it back.
-  auto take_unit = [&](int u, PackedUnit &x) -> bool {
-    const int slot = u % kPkSlots;
-    if (!mbar_wait(smem_addr(&sh.unit_full[slot]), static_cast<uint32_t>((u / kPkSlots) & 1))) return false;
-    x = sh.unit[slot];
+  // The unit told in a slot; false when a wait ran out.  Whoever has read a slot gives it back.
+  auto take_unit = [&](const Ring<kPkSlots> &slot, PackedUnit &x) -> bool {
+    if (!mbar_wait(smem_addr(&sh.unit_full[slot.at]), slot.phase)) return false;
+    x = sh.unit[slot.at];
     return true;
   };
   bool ok = true;
 
   if (warp >= kPkMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPkRegsOther));
-    if (warp == kPkProducerWarp) {
-      // ---------------------------------------------------------------- units, TMA
+    if (warp == kPkUnitWarp) {
+      // ---------------------------------------------------------------- units, ahead of the others
       if (blockIdx.x == 0)
         for (int b = lane; b < p.B; b += 32) {
           const int q0 = p.q_offsets[b], q1 = p.q_offsets[b + 1], k0 = p.k_offsets[b], k1 = p.k_offsets[b + 1];
           if (q0 < 0 || q1 < q0 || q1 > p.Nq || k0 < 0 || k1 < k0 || k1 > p.Nk) flag_error(p.err, GQA_DEVERR_SEQLEN);
         }
+      const int c = static_cast<int>(blockIdx.x), W = static_cast<int>(gridDim.x);
       PackedWalk walk;
-      walk.start(p, lane);
-      int it = 0, queries = 0;  // key tiles and loads of queries so far
-      for (int u = 0; ok; ++u) {
-        const int c = static_cast<int>(blockIdx.x), W = static_cast<int>(gridDim.x);
+      walk.start(p, lane, W);
+      Ring<kPkSlots> slot;
+      for (int u = 0; ok; ++u, slot.step()) {
         const long long number = static_cast<long long>(u) * W + (u & 1 ? W - 1 - c : c);  // to and fro
         PackedUnit x = {};
         PackedSeq s;
@@ -295,85 +324,97 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           x.see0 = p.causal ? t0 + 1 + s.m - s.n : s.m;
           x.keys = s.m;
           x.kv = static_cast<int>(number % p.Hkv);
+#pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int rows = min(p.Tt, x.tokens - i * p.Tt);  // tokens of the tile
             const int sees = p.causal ? x.see0 + i * p.Tt + rows - 1 : s.m;
             x.nt[i] = rows > 0 && sees > 0 ? (sees + kPkKeys - 1) / kPkKeys : 0;
           }
         }
-        const int slot = u % kPkSlots;
-        if (u >= kPkSlots) ok = mbar_wait(smem_addr(&sh.unit_empty[slot]), static_cast<uint32_t>((u / kPkSlots - 1) & 1));
+        if (u >= kPkSlots) ok = mbar_wait(smem_addr(&sh.unit_empty[slot.at]), slot.phase ^ 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          sh.unit[slot] = x;
-          mbar_arrive(smem_addr(&sh.unit_full[slot]));
+          sh.unit[slot.at] = x;
+          mbar_arrive(smem_addr(&sh.unit_full[slot.at]));
         }
         if (x.tokens == 0) break;
-        const int nt = max(x.nt[0], x.nt[1]);
-        if (nt == 0) continue;
-        if (lane == 0) {
-          for (int j = 0; j < nt && ok; ++j, ++it) {
-            const int row = x.k0 + j * kPkKeys, ks = it % kPkKStages, vs = it % kPkVStages;
-            if (it >= kPkKStages)
-              ok = mbar_wait(smem_addr(&sh.k_empty[ks]), static_cast<uint32_t>((it / kPkKStages - 1) & 1));
+      }
+      if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
+    } else if (warp == kPkProducerWarp) {
+      // ---------------------------------------------------------------- TMA
+      if (lane == 0) {
+        int it = 0, queries[2] = {0, 0};  // key tiles and loads of a stream's queries so far
+        Ring<kPkKStages> ks;
+        Ring<kPkVStages> vs;
+        Ring<kPkSlots> slot;
+        for (; ok; slot.step()) {
+          PackedUnit x;
+          ok = take_unit(slot, x);
+          if (!ok || x.tokens == 0) break;
+          mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
+          const int nt = max(x.nt[0], x.nt[1]);
+          for (int j = 0; j < nt; ++j, ++it, ks.step(), vs.step()) {
+            const int row = x.k0 + j * kPkKeys;
+            if (it >= kPkKStages) ok = mbar_wait(smem_addr(&sh.k_empty[ks.at]), ks.phase ^ 1u);
             if (!ok) break;
-            const uint32_t kb = smem_addr(&sh.k_full[ks]);
+            const uint32_t kb = smem_addr(&sh.k_full[ks.at]), kd = k_ptr(ks.at);
             mbar_arrive_expect_tx(kb, kPkTileBytes);
-            tma_load_3d(k_ptr(ks), &tmK, kb, 0, x.kv, row);
-            tma_load_3d(k_ptr(ks) + kPkPanelBytes, &tmK, kb, 64, x.kv, row);
-            if (j == 0) {  // the queries, once every S of the unit before has read its own
-              if (queries > 0) ok = mbar_wait(smem_addr(&sh.q_empty), static_cast<uint32_t>((queries - 1) & 1));
-              if (!ok) break;
-              const uint32_t qb = smem_addr(&sh.q_full);
-              mbar_arrive_expect_tx(qb, 2u * 2u * 64u * 2u * static_cast<uint32_t>(p.G * p.Tt));
+            tma_load_3d(kd, &tmK, kb, 0, x.kv, row);
+            tma_load_3d(kd + kPkPanelBytes, &tmK, kb, 64, x.kv, row);
+            if (j == 0) {  // a stream's queries, once every S of the stream has read those before
+#pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t qd = smem_addr(smem) + i * kPkTileBytes;
+                if (!ok || x.nt[i] == 0) continue;
+                if (queries[i] > 0) ok = mbar_wait(smem_addr(&sh.q_empty[i]), static_cast<uint32_t>((queries[i] - 1) & 1));
+                if (!ok) continue;
+                const uint32_t qb = smem_addr(&sh.q_full[i]), qd = smem_addr(smem) + i * kPkTileBytes;
+                mbar_arrive_expect_tx(qb, 2u * 64u * 2u * static_cast<uint32_t>(p.G * p.Tt));
                 tma_load_3d(qd, &tmQ, qb, 0, x.kv * p.G, x.q0 + i * p.Tt);
                 tma_load_3d(qd + kPkPanelBytes, &tmQ, qb, 64, x.kv * p.G, x.q0 + i * p.Tt);
+                ++queries[i];
               }
-              ++queries;
+              if (!ok) break;
             }
-            if (it >= kPkVStages)
-              ok = mbar_wait(smem_addr(&sh.v_empty[vs]), static_cast<uint32_t>((it / kPkVStages - 1) & 1));
+            if (it >= kPkVStages) ok = mbar_wait(smem_addr(&sh.v_empty[vs.at]), vs.phase ^ 1u);
             if (!ok) break;
-            const uint32_t vb = smem_addr(&sh.v_full[vs]);
+            const uint32_t vb = smem_addr(&sh.v_full[vs.at]), vd = v_ptr(vs.at);
             mbar_arrive_expect_tx(vb, kPkTileBytes);
-            tma_load_3d(v_ptr(vs), &tmV, vb, 0, x.kv, row);
-            tma_load_3d(v_ptr(vs) + kPkPanelBytes, &tmV, vb, 64, x.kv, row);
+            tma_load_3d(vd, &tmV, vb, 0, x.kv, row);
+            tma_load_3d(vd + kPkPanelBytes, &tmV, vb, 64, x.kv, row);
           }
         }
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      if (!ok && lane == 0) {
-        flag_error(p.err, GQA_DEVERR_TIMEOUT);
-        // Do not leave while copies into this CTA's shared memory may still be in flight: wait out every
-        // phase that a load was issued for (tile `it` may have its K loads alone).
-        if (queries > 0) (void)mbar_wait(smem_addr(&sh.q_full), static_cast<uint32_t>((queries - 1) & 1));
-        for (int i = (it + 1 > kPkKStages ? it + 1 - kPkKStages : 0); i <= it; ++i)
-          (void)mbar_wait(smem_addr(&sh.k_full[i % kPkKStages]), static_cast<uint32_t>((i / kPkKStages) & 1));
-        for (int i = (it > kPkVStages ? it - kPkVStages : 0); i < it; ++i)
-          (void)mbar_wait(smem_addr(&sh.v_full[i % kPkVStages]), static_cast<uint32_t>((i / kPkVStages) & 1));
+        if (!ok) {
+          flag_error(p.err, GQA_DEVERR_TIMEOUT);
+          // Do not leave while copies into this CTA's shared memory may still be in flight: wait out every
+          // phase that a load was issued for (tile `it` may have its K loads alone).
+          for (int i = 0; i < 2; ++i)
+            if (queries[i] > 0) (void)mbar_wait(smem_addr(&sh.q_full[i]), static_cast<uint32_t>((queries[i] - 1) & 1));
+          for (int i = (it + 1 > kPkKStages ? it + 1 - kPkKStages : 0); i <= it; ++i)
+            (void)mbar_wait(smem_addr(&sh.k_full[i % kPkKStages]), static_cast<uint32_t>((i / kPkKStages) & 1));
+          for (int i = (it > kPkVStages ? it - kPkVStages : 0); i < it; ++i)
+            (void)mbar_wait(smem_addr(&sh.v_full[i % kPkVStages]), static_cast<uint32_t>((i / kPkVStages) & 1));
+        }
       }
     } else if (warp == kPkCheckWarp) {
       // ---------------------------------------------------------------- values that some rows must not see
       // Behind the first query's last key a row of V is seen by some rows of the unit or by none (the
       // sequence's end): P is 0 there, but 0 x inf is not.  Those behind the end are cleared, and so is a
       // value that is not finite before it, which the epilogue gives to the rows that see it.
-      int it = 0;
-      for (int u = 0; ok; ++u) {
+      Ring<kPkVStages> vs;
+      Ring<kPkSlots> slot;
+      for (; ok; slot.step()) {
         PackedUnit x;
-        ok = __all_sync(0xffffffffu, take_unit(u, x));
+        ok = __all_sync(0xffffffffu, take_unit(slot, x));
         if (!ok || x.tokens == 0) break;
-        const int nt = max(x.nt[0], x.nt[1]), slot = u % kPkSlots;
+        const int nt = max(x.nt[0], x.nt[1]);
         bool bad = false;
-        for (int j = 0; j < nt; ++j, ++it) {
-          const int vs = it % kPkVStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.v_full[vs]), static_cast<uint32_t>((it / kPkVStages) & 1)));
+        for (int j = 0; j < nt; ++j, vs.step()) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.v_full[vs.at]), vs.phase));
           if (!ok) break;
           const int r0 = max(0, max(x.see0, 0) - j * kPkKeys), r1 = x.keys - j * kPkKeys;  // rows from r0 on; the end
           if (r0 < kPkKeys) {
-            uint4 *tile = reinterpret_cast<uint4 *>(smem + kPkOffV + vs * kPkTileBytes);
+            uint4 *tile = reinterpret_cast<uint4 *>(smem + kPkOffV + vs.at * kPkTileBytes);
 #pragma unroll 4
             for (int c = r0 * 16 + lane; c < kPkKeys * 16; c += 32) {  // 16-byte chunks: row, panel, chunk
               const int row = c >> 4;
@@ -401,13 +442,13 @@ __global__ void __launch_bounds__(kPkThreads, 1)
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean[vs]));
+          if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean[vs.at]));
         }
         bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) {
-          if (bad) sh.unit[slot].bad = 1;
-          mbar_arrive(smem_addr(&sh.unit_checked[slot]));
-          mbar_arrive(smem_addr(&sh.unit_empty[slot]));
+          if (bad) sh.unit[slot.at].bad = 1;
+          mbar_arrive(smem_addr(&sh.unit_checked[slot.at]));
+          mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
         }
       }
       if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
@@ -424,32 +465,34 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       constexpr uint32_t kIdO = idesc_bf16_f32(kPkRows, kHeadDim, false, true);
       const uint64_t qd0 = sdesc_sw128(smem_addr(smem), 16, 1024), kd0 = sdesc_sw128(k_ptr(0), 16, 1024),
                      vd0 = sdesc_sw128(v_ptr(0), kPkPanelBytes, 1024);
-      int it = 0, queries = 0;                  // key tiles, units with tiles
-      uint32_t phase_p[2] = {0, 0}, mine[2] = {0, 0};  // P made so far (mod 2), units of a stream with tiles
+      //   The walk runs on across the units: a unit's first S comes before the last P V of the unit before.
+      Ring<kPkKStages> ks;                                 // of the tile at hand
+      Ring<kPkVStages> vs;                                 // of the tile before
+      Ring<kPkSlots> slot;
+      int pj = 0, pn[2] = {0, 0};                          // the tile before: its place in its unit, that unit's tiles
+      uint32_t phase_p[2] = {0, 0}, phase_q[2] = {0, 0};   // P made, queries loaded so far (mod 2)
+      uint32_t mine[2] = {0, 0};                           // units of a stream whose P V is all issued
       bool issued = false;
-      for (int u = 0; ok; ++u) {
+      for (; ok; slot.step()) {
         PackedUnit x;
-        ok = __all_sync(0xffffffffu, take_unit(u, x));
-        const int tokens = __reduce_max_sync(0xffffffffu, x.tokens);
-        if (!ok || tokens == 0) break;
+        ok = __all_sync(0xffffffffu, take_unit(slot, x));
+        if (!ok) break;
+        const bool end = __reduce_max_sync(0xffffffffu, x.tokens) == 0;
         const int tiles[2] = {__reduce_max_sync(0xffffffffu, x.nt[0]), __reduce_max_sync(0xffffffffu, x.nt[1])};
-        if (elect_one()) mbar_arrive(smem_addr(&sh.unit_empty[u % kPkSlots]));
-        const int n0 = max(tiles[0], tiles[1]);
-        if (n0 == 0) continue;
-        ok = mbar_wait(smem_addr(&sh.q_full), static_cast<uint32_t>(queries++ & 1));
-        for (int j = 0; j <= n0 && ok; ++j) {
-          const int tv = it + j - 1, vs = tv % kPkVStages, tk = it + j, ks = tk % kPkKStages;
-          if (j > 0) ok = mbar_wait(smem_addr(&sh.v_clean[vs]), static_cast<uint32_t>((tv / kPkVStages) & 1));
-          if (ok && j < n0) ok = mbar_wait(smem_addr(&sh.k_full[ks]), static_cast<uint32_t>((tk / kPkKStages) & 1));
+        if (!end && elect_one()) mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
+        const int n0 = max(max(tiles[0], tiles[1]), end ? 1 : 0);  // (the last P V is issued at the end)
+        for (int j = 0; j < n0; ++j) {
+          const bool pv = pj < max(pn[0], pn[1]);
+          const uint64_t vd = vd0 + static_cast<uint64_t>(vs.at * (kPkTileBytes / 16));
+          const uint64_t kd = kd0 + static_cast<uint64_t>(ks.at * (kPkTileBytes / 16));
+          if (pv) ok = mbar_wait(smem_addr(&sh.v_clean[vs.at]), vs.phase);
+          if (ok && !end) ok = mbar_wait(smem_addr(&sh.k_full[ks.at]), ks.phase);
           if (!ok) break;
-          const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (kPkTileBytes / 16));
-          const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (kPkTileBytes / 16));
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             const uint32_t tm = tmem + st * kPkTmemStream;
-            const int nt = tiles[st];
-            if (j > 0 && j <= nt) {
-              if (j == 1 && mine[st] > 0)  // the O of the unit before has been read
+            if (pj < pn[st]) {
+              if (pj == 0 && mine[st] > 0)  // the O of the unit before has been read
                 ok = ok && mbar_wait(smem_addr(&sh.o_free[st]), (mine[st] - 1) & 1);
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
@@ -460,16 +503,21 @@ __global__ void __launch_bounds__(kPkThreads, 1)
 #pragma unroll
                   for (int k = 0; k < 4; ++k)  // 16 keys each
                     umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
-                                 j > 1 || half > 0 || k > 0 ? 1u : 0u);
-                  if (half == 1 && j == nt) umma_commit(smem_addr(&sh.o_full[st]));
+                                 pj > 0 || half > 0 || k > 0 ? 1u : 0u);
+                  if (half == 1 && pj + 1 == pn[st]) umma_commit(smem_addr(&sh.o_full[st]));
                 }
                 __syncwarp();
               }
               if (!ok) break;
               phase_p[st] ^= 1;
-              if (j == nt) ++mine[st];
+              if (pj + 1 == pn[st]) ++mine[st];
             }
-            if (j < nt) {
+            if (j < tiles[st]) {
+              if (j == 0) {
+                ok = mbar_wait(smem_addr(&sh.q_full[st]), phase_q[st]);
+                if (!ok) break;
+                phase_q[st] ^= 1;
+              }
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
@@ -482,8 +530,14 @@ __global__ void __launch_bounds__(kPkThreads, 1)
               issued = true;
             }
           }
+          if (!ok) break;
+          pj = j;
+          pn[0] = tiles[0];
+          pn[1] = tiles[1];
+          if (pv) vs.step();
+          ks.step();
         }
-        it += n0;
+        if (end) break;
       }
       if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
       __syncwarp();
@@ -499,12 +553,15 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const int tl = row / p.G, g = row - tl * p.G;
     const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + st * kPkTmemStream;
-    int is = 0, it0 = 0, mine = 0;  // key tiles of the stream, of the CTA before the unit; units with any of the stream's
-    for (int u = 0; ok; ++u) {
-      PackedUnit x;
-      ok = __all_sync(0xffffffffu, take_unit(u, x));
+    uint32_t phase_s = 0, phase_o = 0;
+    int it = 0;  // the CTA's key tiles before the unit
+    Ring<kPkSlots> slot;
+    for (; ok; slot.step()) {
+      ok = mbar_wait(smem_addr(&sh.unit_full[slot.at]), slot.phase);
+      const PackedUnit &x = sh.unit[slot.at];
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok || x.tokens == 0) break;
-      const int slot = u % kPkSlots, nt = st ? x.nt[1] : x.nt[0];
+      const int nt = x.nt[st];
       const int token = st * p.Tt + tl;
       const bool valid = tl < p.Tt && token < x.tokens;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
@@ -512,20 +569,19 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       const int all_see = x.see0 + (p.causal ? st * p.Tt : 0);  // keys that every row of the tile sees
       // The unit's tiles are given back by the stream that has S and P V of a tile behind the other's: the later one, if
       // it has any tile (it has at least as many as the other then).
-      const int n0 = max(x.nt[0], x.nt[1]);
       const bool gives = (warp & 3) == 0 && lane == 0 && st == (x.nt[1] > 0 ? 1 : 0);
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < nt; ++j, ++is) {
-        ok = mbar_wait(smem_addr(&sh.s_full[st]), static_cast<uint32_t>(is & 1));
+      for (int j = 0; j < nt; ++j, phase_s ^= 1u) {
+        ok = mbar_wait(smem_addr(&sh.s_full[st]), phase_s);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         if (gives) {
-          mbar_arrive(smem_addr(&sh.k_empty[(it0 + j) % kPkKStages]));
-          if (j > 0) mbar_arrive(smem_addr(&sh.v_empty[(it0 + j - 1) % kPkVStages]));
-          if (j + 1 == nt) mbar_arrive(smem_addr(&sh.q_empty));
+          mbar_arrive(smem_addr(&sh.k_empty[(it + j) % kPkKStages]));
+          if (j > 0) mbar_arrive(smem_addr(&sh.v_empty[(it + j - 1) % kPkVStages]));
         }
+        if ((warp & 3) == 0 && lane == 0 && j + 1 == nt) mbar_arrive(smem_addr(&sh.q_empty[st]));
         if (!warp_valid) {  // what P holds in these rows reaches no output
           __syncwarp();
           if (lane == 0) {
@@ -601,48 +657,51 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's rows
       if (nt > 0) {
-        ok = mbar_wait(smem_addr(&sh.o_full[st]), static_cast<uint32_t>(mine & 1));
-        ++mine;
-        if (ok && gives) mbar_arrive(smem_addr(&sh.v_empty[(it0 + nt - 1) % kPkVStages]));
+        ok = mbar_wait(smem_addr(&sh.o_full[st]), phase_o);
+        phase_o ^= 1u;
+        if (ok && gives) mbar_arrive(smem_addr(&sh.v_empty[(it + nt - 1) % kPkVStages]));
       }
-      it0 += n0;
-      ok = ok && mbar_wait(smem_addr(&sh.unit_checked[slot]), static_cast<uint32_t>((u / kPkSlots) & 1));
+      it += max(x.nt[0], x.nt[1]);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      const bool bad = *reinterpret_cast<volatile uint32_t *>(&sh.unit[slot].bad) != 0;
       if (warp_valid) {
-        tc_fence_after();
         const float inv = l_run != 0.f ? 1.f / l_run : 0.f;  // (NaN stays NaN)
         uint16_t *dst = p.out + (static_cast<long long>(x.q0 + token) * p.Hq + x.kv * p.G + g) * kHeadDim;
+        tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 32) {
-          float o[32];
-          if (nt > 0) {
-            tmem_ld32(tm + kPkTmemO + c, o);
-            tmem_wait_ld();
+        for (int c = 0; c < kHeadDim; c += 64) {
+          float o[2][32];
+          tmem_ld32(tm + kPkTmemO + c, o[0]);  // (not used where there was no tile)
+          tmem_ld32(tm + kPkTmemO + c + 32, o[1]);
+          tmem_wait_ld();
+          if (c > 0 && nt > 0) {  // the next unit's P V may come
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.o_free[st]));
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = l_run != 0.f ? o[e] * inv : 0.f;
           if (valid) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
               uint32_t y[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = pack_bf16(o[16 * i + 2 * e], o[16 * i + 2 * e + 1]);
+              for (int e = 0; e < 8; ++e)
+                y[e] = l_run != 0.f ? pack_bf16(o[i >> 1][16 * (i & 1) + 2 * e] * inv, o[i >> 1][16 * (i & 1) + 2 * e + 1] * inv)
+                                    : 0u;
               store_32b(dst + c + 16 * i, y, p.out_wide);
             }
           }
         }
-        if (bad && valid) packed_add_nonfinite(p, x.k0, x.kv, max(0, x.see0), sees, dst, inv);
+        ok = mbar_wait(smem_addr(&sh.unit_checked[slot.at]), slot.phase);
+        const bool bad = *reinterpret_cast<volatile uint32_t *>(&sh.unit[slot.at].bad) != 0;
+        if (bad && valid && ok) packed_add_nonfinite(p, x.k0, x.kv, max(0, x.see0), sees, dst, inv);
+      } else if (nt > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.o_free[st]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (nt > 0) mbar_arrive(smem_addr(&sh.o_free[st]));
-        mbar_arrive(smem_addr(&sh.unit_empty[slot]));
-      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
     }
     if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
   }
