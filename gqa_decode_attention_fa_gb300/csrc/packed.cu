@@ -83,6 +83,7 @@ struct PackedUnit {
   int see0;        // keys that the first query sees (causal: each next one sees one more), may be negative
   int keys;        // m of the sequence
   int nt[2];       // key tiles of each stream's tile
+  int steps[2];    // of the last one, sixteens of keys that some row sees
   int kv;
   uint32_t bad;    // a value that not all rows see is not finite
 };
@@ -90,11 +91,11 @@ struct PackedUnit {
 struct PackedShared {
   uint64_t k_full[kPkKStages], k_empty[kPkKStages], v_full[kPkVStages], v_clean[kPkVStages], v_empty[kPkVStages];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, q_full[2], q_empty[2];
-  uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_checked[kPkSlots];
+  uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_checked[kPkSlots][2];
   PackedUnit unit[kPkSlots];
   uint32_t tmem;
 };
-constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 4 + 3 * kPkSlots;
+constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 4 + 4 * kPkSlots;
 constexpr int kPkSmemBytes = kPkOffBar + static_cast<int>(sizeof(PackedShared));
 static_assert(kPkSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       uint64_t *bar = bars + i;
       int count = 1;
       if ((bar >= sh.p_full[0] && bar < sh.o_full) || (bar >= sh.o_free && bar < &sh.drain)) count = 4;
-      if (bar >= sh.unit_empty && bar < sh.unit_checked) count = 11;  // every warp but the one that finds them
+      if (bar >= sh.unit_empty && bar < sh.unit_checked[0]) count = 11;  // every warp but the one that finds them
       mbar_init(smem_addr(bar), count);
     }
     fence_barrier_init();
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
             const int rows = min(p.Tt, x.tokens - i * p.Tt);  // tokens of the tile
             const int sees = p.causal ? x.see0 + i * p.Tt + rows - 1 : s.m;
             x.nt[i] = rows > 0 && sees > 0 ? (sees + kPkKeys - 1) / kPkKeys : 0;
+            x.steps[i] = x.nt[i] > 0 ? ((sees - 1) % kPkKeys) / 16 + 1 : 0;
           }
         }
         if (u >= kPkSlots) ok = mbar_wait(smem_addr(&sh.unit_empty[slot.at]), slot.phase ^ 1u);
@@ -398,9 +400,10 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       }
     } else if (warp == kPkCheckWarp) {
       // ---------------------------------------------------------------- values that some rows must not see
-      // Behind the first query's last key a row of V is seen by some rows of the unit or by none (the
-      // sequence's end): P is 0 there, but 0 x inf is not.  Those behind the end are cleared, and so is a
-      // value that is not finite before it, which the epilogue gives to the rows that see it.
+      // Behind the first query's last key a row of V is seen by some rows of the unit or by none: P is 0
+      // there, but 0 x inf is not.  Up to the last step of 16 keys that is multiplied, rows behind the
+      // sequence's end are cleared, and so is a value before it that is not finite, which the epilogue gives to
+      // the rows that see it.
       Ring<kPkVStages> vs;
       Ring<kPkSlots> slot;
       for (; ok; slot.step()) {
@@ -408,48 +411,56 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         ok = __all_sync(0xffffffffu, take_unit(slot, x));
         if (!ok || x.tokens == 0) break;
         const int nt = max(x.nt[0], x.nt[1]);
-        bool bad = false;
+        if (lane == 0) {
+          if (x.nt[0] == 0) mbar_arrive(smem_addr(&sh.unit_checked[slot.at][0]));
+          if (x.nt[1] == 0) mbar_arrive(smem_addr(&sh.unit_checked[slot.at][1]));
+        }
         for (int j = 0; j < nt; ++j, vs.step()) {
           ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.v_full[vs.at]), vs.phase));
           if (!ok) break;
-          const int r0 = max(0, max(x.see0, 0) - j * kPkKeys), r1 = x.keys - j * kPkKeys;  // rows from r0 on; the end
-          if (r0 < kPkKeys) {
+          // rows from r0 on, to r2; the sequence's end
+          const int r0 = max(0, max(x.see0, 0) - j * kPkKeys), r1 = x.keys - j * kPkKeys;
+          const int r2 = j + 1 < nt ? kPkKeys : 16 * (x.nt[1] == nt ? x.steps[1] : x.steps[0]);
+          if (r0 < r2) {
             uint4 *tile = reinterpret_cast<uint4 *>(smem + kPkOffV + vs.at * kPkTileBytes);
-#pragma unroll 4
-            for (int c = r0 * 16 + lane; c < kPkKeys * 16; c += 32) {  // 16-byte chunks: row, panel, chunk
-              const int row = c >> 4;
-              uint4 *at = tile + ((c & 8) << 7) + row * 8 + (c & 7);
-              if (row >= r1) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 y = *at;
-              // an exponent of all ones carries into the sign's place
-              const uint32_t ones = (((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-                                     ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u)) &
-                                    0x80008000u;
-              if (ones) {
-                uint32_t z[4] = {y.x, y.y, y.z, y.w};
+            auto at = [&](int c) { return tile + ((c & 8) << 7) + (c >> 4) * 8 + (c & 7); };  // chunk: row, panel, 16 bytes
+            bool bad = false;
+            const int c1 = 16 * min(r1, r2);
+            constexpr int kAhead = 8;
+            for (int c0 = 16 * r0 + lane; c0 < c1; c0 += 32 * kAhead) {
+              uint4 y[kAhead];
+              uint32_t ones = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
-                  if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
-                }
-                *at = make_uint4(z[0], z[1], z[2], z[3]);
+              for (int i = 0; i < kAhead; ++i) y[i] = c0 + 32 * i < c1 ? *at(c0 + 32 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < kAhead; ++i)  // an exponent of all ones carries into the sign's place
+                ones |= ((y[i].x & 0x7f807f80u) + 0x00800080u) | ((y[i].y & 0x7f807f80u) + 0x00800080u) |
+                        ((y[i].z & 0x7f807f80u) + 0x00800080u) | ((y[i].w & 0x7f807f80u) + 0x00800080u);
+              if (ones & 0x80008000u) {
                 bad = true;
+#pragma unroll 1
+                for (int c = c0; c < min(c1, c0 + 32 * kAhead); c += 32) {
+                  uint32_t *z = reinterpret_cast<uint32_t *>(at(c));
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+                    if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
+                  }
+                }
               }
             }
+            for (int c = 16 * max(r0, r1) + lane; c < 16 * r2; c += 32) *at(c) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
+            if (__any_sync(0xffffffffu, bad) && lane == 0) sh.unit[slot.at].bad = 1;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.v_clean[vs.at]));
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sh.v_clean[vs.at]));
+            if (j + 1 == x.nt[0]) mbar_arrive(smem_addr(&sh.unit_checked[slot.at][0]));
+            if (j + 1 == x.nt[1]) mbar_arrive(smem_addr(&sh.unit_checked[slot.at][1]));
+          }
         }
-        bad = __any_sync(0xffffffffu, bad);
-        if (lane == 0) {
-          if (bad) sh.unit[slot.at].bad = 1;
-          mbar_arrive(smem_addr(&sh.unit_checked[slot.at]));
-          mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
-        }
+        if (lane == 0) mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
       }
       if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
     } else if (warp == kPkMmaWarp) {
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       Ring<kPkKStages> ks;                                 // of the tile at hand
       Ring<kPkVStages> vs;                                 // of the tile before
       Ring<kPkSlots> slot;
-      int pj = 0, pn[2] = {0, 0};                          // the tile before: its place in its unit, that unit's tiles
+      int pj = 0, pn[2] = {0, 0}, ps[2] = {0, 0};          // the tile before: its place in its unit, that unit's tiles, the last one's steps
       uint32_t phase_p[2] = {0, 0}, phase_q[2] = {0, 0};   // P made, queries loaded so far (mod 2)
       uint32_t mine[2] = {0, 0};                           // units of a stream whose P V is all issued
       bool issued = false;
@@ -479,63 +490,90 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         if (!ok) break;
         const bool end = __reduce_max_sync(0xffffffffu, x.tokens) == 0;
         const int tiles[2] = {__reduce_max_sync(0xffffffffu, x.nt[0]), __reduce_max_sync(0xffffffffu, x.nt[1])};
+        const int steps[2] = {__reduce_max_sync(0xffffffffu, x.steps[0]), __reduce_max_sync(0xffffffffu, x.steps[1])};
         if (!end && elect_one()) mbar_arrive(smem_addr(&sh.unit_empty[slot.at]));
         const int n0 = max(max(tiles[0], tiles[1]), end ? 1 : 0);  // (the last P V is issued at the end)
-        for (int j = 0; j < n0; ++j) {
+        // O += P V of the tile before, the sixteens of keys below `steps`
+        auto issue_pv = [&](int st, uint64_t vd, int place, int steps, bool last) -> bool {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait(smem_addr(&sh.p_full[st][half]), phase_p[st])) return false;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t tm = tmem + st * kPkTmemStream;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (4 * half + k < steps)
+                  umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
+                               place > 0 || half > 0 || k > 0 ? 1u : 0u);
+              if (half == 1 && last) umma_commit(smem_addr(&sh.o_full[st]));
+            }
+            __syncwarp();
+          }
+          phase_p[st] ^= 1;
+          return true;
+        };
+        auto issue_s = [&](int st, uint64_t kd) {
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kHeadDim / 16; ++k)
+              umma_bf16(tmem + st * kPkTmemStream, qd0 + st * (kPkTileBytes / 16) + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
+                        kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
+            umma_commit(smem_addr(&sh.s_full[st]));
+          }
+          __syncwarp();
+        };
+        auto o_free = [&](int st) {  // the O of the unit before has been read
+          return mine[st] == 0 || mbar_wait(smem_addr(&sh.o_free[st]), (mine[st] - 1) & 1);
+        };
+        const int both = min(tiles[0], tiles[1]);
+        for (int j = 0; j < n0;) {
           const bool pv = pj < max(pn[0], pn[1]);
           const uint64_t vd = vd0 + static_cast<uint64_t>(vs.at * (kPkTileBytes / 16));
           const uint64_t kd = kd0 + static_cast<uint64_t>(ks.at * (kPkTileBytes / 16));
           if (pv) ok = mbar_wait(smem_addr(&sh.v_clean[vs.at]), vs.phase);
-          if (ok && !end) ok = mbar_wait(smem_addr(&sh.k_full[ks.at]), ks.phase);
           if (!ok) break;
+          if (j == 0 || j >= both) {
+            // The unit's first tile, before which come the last P V of the unit before, or one that a stream uses alone.
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const uint32_t tm = tmem + st * kPkTmemStream;
-            if (pj < pn[st]) {
-              if (pj == 0 && mine[st] > 0)  // the O of the unit before has been read
-                ok = ok && mbar_wait(smem_addr(&sh.o_free[st]), (mine[st] - 1) & 1);
+            for (int st = 0; st < 2; ++st)
+              if (ok && pj < pn[st]) {
+                const bool last = pj + 1 == pn[st];
+                if (pj == 0) ok = o_free(st);
+                ok = ok && issue_pv(st, vd, pj, last ? ps[st] : kPkKeys / 16, last);
+                if (last) ++mine[st];
+              }
+            if (ok && !end) ok = mbar_wait(smem_addr(&sh.k_full[ks.at]), ks.phase);
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                ok = ok && mbar_wait(smem_addr(&sh.p_full[st][half]), phase_p[st]);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)  // 16 keys each
-                    umma_bf16_ts(tm + kPkTmemO, tm + 32 * half + 8 * k, vd + 128 * (4 * half + k), kIdO,
-                                 pj > 0 || half > 0 || k > 0 ? 1u : 0u);
-                  if (half == 1 && pj + 1 == pn[st]) umma_commit(smem_addr(&sh.o_full[st]));
+            for (int st = 0; st < 2; ++st)
+              if (ok && j < tiles[st]) {
+                if (j == 0) {
+                  ok = mbar_wait(smem_addr(&sh.q_full[st]), phase_q[st]);
+                  phase_q[st] ^= 1;
                 }
-                __syncwarp();
+                tc_fence_after();
+                if (ok) issue_s(st, kd);
+                issued = true;
               }
-              if (!ok) break;
-              phase_p[st] ^= 1;
-              if (pj + 1 == pn[st]) ++mine[st];
-            }
-            if (j < tiles[st]) {
-              if (j == 0) {
-                ok = mbar_wait(smem_addr(&sh.q_full[st]), phase_q[st]);
-                if (!ok) break;
-                phase_q[st] ^= 1;
-              }
-              tc_fence_after();
-              if (elect_one()) {
+          } else {  // both streams have P V and S of a tile in the middle
+            ok = mbar_wait(smem_addr(&sh.k_full[ks.at]), ks.phase);
 #pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k)
-                  umma_bf16(tm, qd0 + st * (kPkTileBytes / 16) + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3),
-                            kd + (k >> 2) * (kPkPanelBytes / 16) + 2 * (k & 3), kIdS, k > 0 ? 1u : 0u);
-                umma_commit(smem_addr(&sh.s_full[st]));
-              }
-              __syncwarp();
-              issued = true;
+            for (int st = 0; st < 2; ++st) {
+              if (j == 1) ok = ok && o_free(st);
+              ok = ok && issue_pv(st, vd, j - 1, kPkKeys / 16, false);
+              if (!ok) break;
+              issue_s(st, kd);
             }
           }
           if (!ok) break;
           pj = j;
           pn[0] = tiles[0];
           pn[1] = tiles[1];
+          ps[0] = steps[0];
+          ps[1] = steps[1];
           if (pv) vs.step();
           ks.step();
+          ++j;
         }
         if (end) break;
       }
@@ -693,7 +731,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
             }
           }
         }
-        ok = mbar_wait(smem_addr(&sh.unit_checked[slot.at]), slot.phase);
+        ok = mbar_wait(smem_addr(&sh.unit_checked[slot.at][st]), slot.phase);
         const bool bad = *reinterpret_cast<volatile uint32_t *>(&sh.unit[slot.at].bad) != 0;
         if (bad && valid && ok) packed_add_nonfinite(p, x.k0, x.kv, max(0, x.see0), sees, dst, inv);
       } else if (nt > 0) {
