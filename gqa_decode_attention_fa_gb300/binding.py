@@ -621,16 +621,15 @@ Q8_FORMATS = {"e4m3": 0, "int8": 1}
 def _q8_cache(k_codes, v_codes, k_scale, v_scale, fmt: str, rows: int, num_kv_heads: int, device: int):
     """Pointers of an 8-bit cache's four tensors: `rows` rows of num_kv_heads x 128 codes and num_kv_heads scales."""
     tt = _torch()
-    if fmt not in Q8_FORMATS:
+    codes, n = tt.codes.get(fmt), rows * num_kv_heads
+    if codes is None:
         raise ValueError(f"fmt: one of {sorted(Q8_FORMATS)}, got {fmt!r}")
-    out = []
-    for t, name, dtype, row in ((k_codes, "k_codes", tt.codes[fmt], num_kv_heads * 128),
-                                (v_codes, "v_codes", tt.codes[fmt], num_kv_heads * 128),
-                                (k_scale, "k_scale", tt.f32, num_kv_heads), (v_scale, "v_scale", tt.f32, num_kv_heads)):
-        out.append(_dev(t, name, dtype, None, device))
-        if t.numel() != rows * row:
-            raise ValueError(f"{name}: expected {rows} rows of {row}, got shape {tuple(t.shape)}")
-    return out
+    ptrs = (_dev(k_codes, "k_codes", codes, None, device), _dev(v_codes, "v_codes", codes, None, device),
+            _dev(k_scale, "k_scale", tt.f32, None, device), _dev(v_scale, "v_scale", tt.f32, None, device))
+    if not (k_scale.numel() == n == v_scale.numel() and k_codes.numel() == n * 128 == v_codes.numel()):
+        shapes = [tuple(t.shape) for t in (k_codes, v_codes, k_scale, v_scale)]
+        raise ValueError(f"cache: expected {rows} rows of {num_kv_heads} x 128 codes and {num_kv_heads} scales, got shapes {shapes}")
+    return ptrs
 
 
 def _packed(t, name: str, tokens: int, heads: int, device: int):
@@ -650,34 +649,24 @@ def _packed(t, name: str, tokens: int, heads: int, device: int):
     return t.data_ptr(), st
 
 
-def _q8_rows(call: str, batch, num_kv_heads, num_tokens, max_seq_len, k, v, names, cache, page_table, offsets, slot_start,
-             start_optional, fmt, block_size, num_cache_blocks, head_dim, device, device_errors, stream):
-    i32 = _torch().i32
-    kp, ks = _packed(k, names[0], num_tokens, num_kv_heads, device)
-    vp, vs = _packed(v, names[1], num_tokens, num_kv_heads, device)
-    rows = num_cache_blocks * 64 if block_size else batch * max_seq_len
-    cp = _q8_cache(*cache, fmt, rows, num_kv_heads, device)
-    desc = _desc(Q8Desc, batch, 0, num_kv_heads, head_dim, Q8_FORMATS[fmt], num_tokens, block_size, max_seq_len,
-                 num_cache_blocks, device, ks, vs)
-    where = (_dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
-             _dev(offsets, "offsets", i32, (batch + 1,), device, True),
-             _dev(slot_start, "slot_start", i32, (batch,), device, start_optional))
-    more = (_err(device_errors, device), _on(device, stream))
-    if call == "gqa_q8_append":
-        _check(load().gqa_q8_append(desc, kp, vp, *cp, *where, *more), call)
-    else:
-        _check(load().gqa_q8_read(desc, *cp, *where, kp, vp, *more), call)
-
-
 def q8_append(batch: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, k, v, k_codes, v_codes, k_scale, v_scale,
               page_table, offsets, slot_start, *, fmt: str = "e4m3", block_size: int = 0, num_cache_blocks: int = 0,
               head_dim: int = 128, device: int = 0, device_errors=None, stream=None):
     """Quantise and store packed rows (gqa_q8_append, include/gqa_q8.h): k and v [N, H_kv, 128], the rows
     offsets[b] .. offsets[b + 1] - 1 those of sequence b (offsets None: one row a sequence), to the slots
     from slot_start[b] on.  fmt "e4m3" (codes float8_e4m3fn or uint8) or "int8" (int8 or uint8)."""
-    _q8_rows("gqa_q8_append", batch, num_kv_heads, num_tokens, max_seq_len, k, v, ("k", "v"),
-             (k_codes, v_codes, k_scale, v_scale), page_table, offsets, slot_start, False, fmt, block_size,
-             num_cache_blocks, head_dim, device, device_errors, stream)
+    i32 = _torch().i32
+    kp, ks = _packed(k, "k", num_tokens, num_kv_heads, device)
+    vp, vs = _packed(v, "v", num_tokens, num_kv_heads, device)
+    kc, vc, kf, vf = _q8_cache(k_codes, v_codes, k_scale, v_scale, fmt,
+                               num_cache_blocks * 64 if block_size else batch * max_seq_len, num_kv_heads, device)
+    _check(load().gqa_q8_append(
+        _desc(Q8Desc, batch, 0, num_kv_heads, head_dim, Q8_FORMATS[fmt], num_tokens, block_size, max_seq_len,
+              num_cache_blocks, device, ks, vs), kp, vp, kc, vc, kf, vf,
+        _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+        _dev(offsets, "offsets", i32, (batch + 1,), device, True), _dev(slot_start, "slot_start", i32, (batch,), device),
+        _err(device_errors, device), _on(device, stream)),
+        "gqa_q8_append")
 
 
 def q8_read(batch: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, k_codes, v_codes, k_scale, v_scale,
@@ -685,9 +674,19 @@ def q8_read(batch: int, num_kv_heads: int, num_tokens: int, max_seq_len: int, k_
             num_cache_blocks: int = 0, head_dim: int = 128, device: int = 0, device_errors=None, stream=None):
     """Rows of an 8-bit cache as packed bf16 (gqa_q8_read): row offsets[b] + i of k_out and v_out [N, H_kv, 128]
     receives slot slot_start[b] + i of sequence b (slot_start None: from slot 0 on)."""
-    _q8_rows("gqa_q8_read", batch, num_kv_heads, num_tokens, max_seq_len, k_out, v_out, ("k_out", "v_out"),
-             (k_codes, v_codes, k_scale, v_scale), page_table, offsets, slot_start, True, fmt, block_size,
-             num_cache_blocks, head_dim, device, device_errors, stream)
+    i32 = _torch().i32
+    kp, ks = _packed(k_out, "k_out", num_tokens, num_kv_heads, device)
+    vp, vs = _packed(v_out, "v_out", num_tokens, num_kv_heads, device)
+    kc, vc, kf, vf = _q8_cache(k_codes, v_codes, k_scale, v_scale, fmt,
+                               num_cache_blocks * 64 if block_size else batch * max_seq_len, num_kv_heads, device)
+    _check(load().gqa_q8_read(
+        _desc(Q8Desc, batch, 0, num_kv_heads, head_dim, Q8_FORMATS[fmt], num_tokens, block_size, max_seq_len,
+              num_cache_blocks, device, ks, vs), kc, vc, kf, vf,
+        _dev(page_table, "page_table", i32, (batch, (max_seq_len + 63) // 64), device, True),
+        _dev(offsets, "offsets", i32, (batch + 1,), device, True),
+        _dev(slot_start, "slot_start", i32, (batch,), device, True), kp, vp,
+        _err(device_errors, device), _on(device, stream)),
+        "gqa_q8_read")
 
 
 @functools.lru_cache(maxsize=1024)

@@ -12,11 +12,11 @@ namespace gqa {
 // Geometry and format checks of a call (q8_rows.cu).
 gqa_status_t q8_check(const gqa_q8_desc_t &d, bool attn);
 
-// Two e4m3 codes (the low 16 bits of x) as two binary16 values; exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}\n" : "=r"(y) : "r"(x));
-  return y;
+// Four e4m3 codes as binary16 pairs; exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t y;
@@ -28,8 +28,7 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
 template <int FMT>
 __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
   if (FMT == GQA_Q8_E4M3) {
-    lo = e4m3x2_to_f16x2(x);
-    hi = e4m3x2_to_f16x2(x >> 16);
+    e4m3x4_to_f16(x, lo, hi);
   } else {
     const uint32_t u = x ^ 0x80808080u;
     lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);

@@ -106,7 +106,7 @@ __device__ __forceinline__ Q8Cut q8_cut(const Q8AttnParams &p, int lane) {
   Q8Cut c;
   c.ranges = all < 1 ? 0 : max(1, min(p.W, all / (2 * wph)));
   const int quarter = c.ranges > 0 ? all / c.ranges / 4 : 0;
-  c.gap = min(quarter, wph);
+  c.gap = min(quarter, 3 * wph);
   c.whole = c.ranges > 0 && all_seqs <= p.W && longest <= all / c.ranges + c.gap * all_seqs / c.ranges + 2 * wph;
   if (c.whole) c.ranges = all_seqs;
   const int total = c.whole ? all_seqs : all + c.gap * max(0, all_seqs - 1);
@@ -136,6 +136,7 @@ __device__ __forceinline__ void q8_find(const Q8AttnParams &p, const Q8Cut &c, i
   *seq0 = s;
 }
 
+// Of 16 (or 4) bytes the first `bytes` copied, the others zero.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -197,14 +198,6 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
   griddep_wait();
   if (!p.whole && p.W > 1) griddep_launch_dependents();  // q8_merge_kernel follows, and it waits
 
-  for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x)) {  // sequences without tokens
-    const int n = p.seq_lens[b];
-    if (n > 0 && n <= p.max_seq) continue;
-    if (n != 0 && tid == 0) flag_error(p.err, GQA_DEVERR_SEQLEN);
-    uint4 *dst = reinterpret_cast<uint4 *>(p.out + static_cast<long long>(b) * p.Hq * kHeadDim);
-    for (int c = tid; c < p.Hq * (kHeadDim / 8); c += kQaThreads) dst[c] = make_uint4(0, 0, 0, 0);
-  }
-
   int pos, end, b, seq0, gap = 0;  // numbers of the range still to do; the sequence at hand and its first number
   if (p.whole) {
     b = w;
@@ -225,9 +218,9 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
   const uint32_t ring = smem_addr(smem_raw) + warp * kStages * kQaStageBytes;
   const int cp_row = lane >> 3, cp_chunk = lane & 7;
   const long long row_bytes = static_cast<long long>(p.Hkv) * kHeadDim;
-  const uint8_t *const k_lane = p.k_codes + (static_cast<long long>(cp_row) * p.Hkv + kv) * kHeadDim + 16 * cp_chunk;
-  const uint8_t *const v_lane = p.v_codes + (static_cast<long long>(cp_row) * p.Hkv + kv) * kHeadDim + 16 * cp_chunk;
-  const float *const s_lane = (lane < 16 ? p.k_scale : p.v_scale) + static_cast<long long>(lane & 15) * p.Hkv + kv;
+  const uint8_t *const k_lane = p.k_codes + static_cast<long long>(kv) * kHeadDim + 16 * cp_chunk;
+  const uint8_t *const v_lane = p.v_codes + static_cast<long long>(kv) * kHeadDim + 16 * cp_chunk;
+  const float *const s_lane = (lane < 16 ? p.k_scale : p.v_scale) + kv;
   const uint32_t cp_dst0 = cp_row * 128 + ((cp_chunk ^ cp_row) << 4);        // rows cp_row and cp_row + 8
   const uint32_t cp_dst1 = cp_row * 128 + 512 + ((cp_chunk ^ (cp_row + 4)) << 4);  // cp_row + 4 and + 12
 
@@ -245,40 +238,14 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
     const int j0 = pos - seq0, j1 = min(nu, j0 + end - pos);
     pos += j1 - j0;
 
-    // ------------------------------------------------------------- the queries, as B of the first product
-    uint32_t qf[NT][8][2];
-    float qs1[NT][2], qs2[NT][2];  // of heads 2t, 2t + 1: together 2^-shift log2(e) / sqrt(128)
+    // The queries are asked for ahead of the copies, which they would wait behind.
+    const uint16_t *const q_row = p.q + (static_cast<long long>(b) * p.Hq + kv * p.G + g) * kHeadDim + 32 * t;
+    uint4 raw[NT][4];
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      const int head = 8 * x + g;
-      uint4 r[4];
-      const uint16_t *src = p.q + (static_cast<long long>(b) * p.Hq + kv * p.G + head) * kHeadDim + 32 * t;
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        r[i] = head < p.G ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
-      uint32_t most = 0;  // the largest finite |q|, as bf16 bits
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t y = word(r[i >> 2], i & 3), lo = y & 0x7fffu, hi = (y >> 16) & 0x7fffu;
-        most = max(most, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-      }
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-      const int shift = most == 0 ? 0 : 14 - (static_cast<int>(most >> 7) - 127);
-      const int h1 = shift >> 1, h2 = shift - h1;
-      const float f1 = power_of_two(h1), f2 = power_of_two(h2);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t y = word(r[i >> 2], i & 3);
-        qf[x][i >> 1][i & 1] = pack_f16(bf16_lo_to_float(y) * f1 * f2, bf16_hi_to_float(y) * f1 * f2);
-      }
-      const float a1 = power_of_two(-h1) * p.scale_log2, a2 = power_of_two(-h2);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        qs1[x][e] = __shfl_sync(0xffffffffu, a1, (2 * t + e) * 4);
-        qs2[x][e] = __shfl_sync(0xffffffffu, a2, (2 * t + e) * 4);
-      }
-    }
+        raw[x][i] = 8 * x + g < p.G ? reinterpret_cast<const uint4 *>(q_row + 8 * x * kHeadDim)[i] : make_uint4(0, 0, 0, 0);
 
     // ------------------------------------------------------------- copies
     int pg_base = -1, pg = 0;  // the lane's page id among 32 from pg_base on
@@ -304,25 +271,67 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
         } else {
           crow = static_cast<long long>(b) * p.max_seq + tok;
         }
-        const int left = there ? n - tok : 0;  // tokens of the unit that there are
+        const int left = there ? n - tok : 0;  // tokens of the unit that there are; the others' rows are zero
         const uint32_t st = ring + stage * kQaStageBytes;
-        const long long at = crow * row_bytes;
+        const uint8_t *const kp = k_lane + crow * row_bytes, *const vp = v_lane + crow * row_bytes;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool in = cp_row + 4 * i < left;
-          const long long from = in ? at + 4 * i * row_bytes : -static_cast<long long>(cp_row) * row_bytes;
-          const uint32_t dst = st + (i & 1 ? cp_dst1 : cp_dst0) + (i >> 1) * 1024;
-          cp_async16(dst, k_lane + from, in ? 16u : 0u);
-          cp_async16(dst + kQaUnit * 128, v_lane + from, in ? 16u : 0u);
+          const int row = cp_row + 4 * i;
+          const long long from = max(0, min(row, left - 1)) * row_bytes;
+          const uint32_t dst = st + (i & 1 ? cp_dst1 : cp_dst0) + (i >> 1) * 1024, bytes = row < left ? 16u : 0u;
+          cp_async16(dst, kp + from, bytes);
+          cp_async16(dst + kQaUnit * 128, vp + from, bytes);
         }
-        const bool in = (lane & 15) < left;
-        cp_async4(st + 2 * kQaUnit * 128 + 4 * lane,
-                  s_lane + (in ? crow * p.Hkv : -static_cast<long long>(lane & 15) * p.Hkv), in ? 4u : 0u);
+        const int row = lane & 15;
+        cp_async4(st + 2 * kQaUnit * 128 + 4 * lane, s_lane + (crow + max(0, min(row, left - 1))) * p.Hkv, row < left ? 4u : 0u);
       }
       cp_async_commit();
     };
 
-    float o[8][NT][4], m[NT][2], l[NT][2], ex[NT][2], lim[NT][2], wt[NT][2];
+    int jl = j0 + share;
+#pragma unroll 1
+    for (int s = 0; s < kStages - 1; ++s, jl += wph) issue(jl, s);  // on their way while the queries are made
+
+    // ------------------------------------------------------------- the queries, as B of the first product
+    uint32_t qf[NT][8][2];
+    float qs1[NT][2], qs2[NT][2];  // of heads 2t, 2t + 1: together 2^-shift log2(e) / sqrt(128)
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      const int head = 8 * x + g;
+      const uint4 (&r)[4] = raw[x];
+      uint32_t most = 0;  // the largest |q|, as bf16 bits
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        most = __vmaxu2(most, __vmaxu2(__vmaxu2(r[i].x & 0x7fff7fffu, r[i].y & 0x7fff7fffu),
+                                       __vmaxu2(r[i].z & 0x7fff7fffu, r[i].w & 0x7fff7fffu)));
+      most = max(most & 0xffffu, most >> 16);
+      if (most >= 0x7f80u) {  // the largest finite one
+        most = 0;
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t y = head < p.G ? q_row[8 * x * kHeadDim + i] & 0x7fffu : 0u;
+          if (y < 0x7f80u) most = max(most, y);
+        }
+      }
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const int shift = most == 0 ? 0 : min(126, 14 - (static_cast<int>(most >> 7) - 127));
+      const float f = power_of_two(shift);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t y = word(r[i >> 2], i & 3);
+        qf[x][i >> 1][i & 1] = pack_f16(bf16_lo_to_float(y) * f, bf16_hi_to_float(y) * f);
+      }
+      const int h1 = shift >> 1;
+      const float a1 = power_of_two(-h1) * p.scale_log2, a2 = power_of_two(h1 - shift);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qs1[x][e] = __shfl_sync(0xffffffffu, a1, (2 * t + e) * 4);
+        qs2[x][e] = __shfl_sync(0xffffffffu, a2, (2 * t + e) * 4);
+      }
+    }
+
+    float o[8][NT][4], m[NT][2], top[NT][2], l[NT][2], ex[NT][2], lim[NT][2], wt[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -331,7 +340,8 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
         for (int e = 0; e < 4; ++e) o[i][x][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[x][e] = ex[x][e] = -INFINITY;  // ex: E
+        m[x][e] = 0.f;                         // 0 until a score is finite
+        top[x][e] = ex[x][e] = -INFINITY;      // m + 8; E
         l[x][e] = lim[x][e] = wt[x][e] = 0.f;  // lim: 2^(14 + E - m), wt: 2^((m - E) / 2)
       }
     }
@@ -342,9 +352,6 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
       wt[x][e] = none ? 0.f : fast_exp2(0.5f * d);
     };
 
-    int jl = j0 + share;
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s, jl += wph) issue(jl, s);
     int stage = 0;
     for (int j = j0 + share; j < j1; j += wph) {
       cp_async_wait<kStages - 2>();
@@ -374,27 +381,34 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
       }
       const uint32_t sc = st + 2 * kQaUnit * 128 + 4 * g;
       const float ks[2] = {lds_f32(sc), lds_f32(sc + 32)}, vs[2] = {lds_f32(sc + 64), lds_f32(sc + 96)};
-      const int left = n - j * kQaUnit;
-      const bool in[2] = {g < left, g + 8 < left};
-
       bool raise = false;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float s = acc[x][e] * qs1[x][e & 1] * ks[e >> 1] * qs2[x][e & 1];
-          acc[x][e] = in[e >> 1] ? s : -INFINITY;
-          raise |= acc[x][e] > m[x][e & 1] + kQaRaise;
+          acc[x][e] = acc[x][e] * qs1[x][e & 1] * ks[e >> 1] * qs2[x][e & 1];
         }
+      if (const int left = n - j * kQaUnit; left < kQaUnit) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (g + 8 * (e >> 1) >= left) acc[x][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) raise |= acc[x][e] > top[x][e & 1];
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float mx = fmaxf(m[x][e], max_over_g(fmaxf(acc[x][e], acc[x][e + 2])));
-            if (mx > m[x][e] + kQaRaise) {  // (a head's result does not depend on the others)
-              l[x][e] *= fast_exp2(m[x][e] - mx);
+            const float mx = max_over_g(fmaxf(acc[x][e], acc[x][e + 2]));
+            if (mx > top[x][e]) {  // (a head's result does not depend on the others)
+              l[x][e] *= top[x][e] == -INFINITY ? 0.f : fast_exp2(m[x][e] - mx);
               m[x][e] = mx;
+              top[x][e] = mx + kQaRaise;
               follow(x, e);
             }
           }
@@ -405,8 +419,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float mm = m[x][e & 1] == -INFINITY ? 0.f : m[x][e & 1];
-          const float pr = fast_exp2(acc[x][e] - mm);
+          const float pr = fast_exp2(acc[x][e] - m[x][e & 1]);
           l[x][e & 1] += pr;
           y[x][e] = pr * vs[e >> 1];
           raise |= fabsf(y[x][e]) > lim[x][e & 1];
@@ -518,6 +531,14 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
     }
     __syncthreads();  // the ring is filled anew
   }
+
+  for (int b = static_cast<int>(blockIdx.x); b < p.B; b += static_cast<int>(gridDim.x)) {  // sequences without tokens
+    const int n = p.seq_lens[b];
+    if (n > 0 && n <= p.max_seq) continue;
+    if (n != 0 && tid == 0) flag_error(p.err, GQA_DEVERR_SEQLEN);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + static_cast<long long>(b) * p.Hq * kHeadDim);
+    for (int c = tid; c < p.Hq * (kHeadDim / 8); c += kQaThreads) dst[c] = make_uint4(0, 0, 0, 0);
+  }
 }
 
 // ------------------------------------------------------------------------------------ merge
@@ -531,7 +552,7 @@ __global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __gr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hq = static_cast<int>(blockIdx.x) % p.Hq, index = static_cast<int>(blockIdx.x) / p.Hq;
   const int kv = hq / p.G, head = hq - kv * p.G;
-  griddep_wait();
+  // What to join follows from the lengths, which the attention kernel has waited for before it let this one start.
   const Q8Cut all = q8_cut(p, lane);
   if (all.whole || all.ranges < 2) return;
   int b = 0, first = 0;
@@ -551,7 +572,19 @@ __global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __gr
   const int parts = w1 - w0 + 1;
   const long long each = static_cast<long long>(p.G) * (kHeadDim + 4);
   auto part = [&](int k) { return p.part + ((static_cast<long long>(w0 + k) * p.Hkv + kv) * 2 + (k == 0 ? 1 : 0)) * each; };
-  // every warp finds M by itself; the weights are made once
+  constexpr int kAhead = 8;
+  float4 y[kAhead];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + i * kQaMergeWarps;
+      y[i] = k < parts ? __ldcg(reinterpret_cast<const float4 *>(part(k) + head * kHeadDim + 4 * lane))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  griddep_wait();  // the attention kernel's partials
+  fetch(warp);
+  // every warp finds M by itself
   float M = -INFINITY;
   for (int k = lane; k < parts; k += 32) {
     const float x = __ldcg(part(k) + p.G * kHeadDim + head);
@@ -564,15 +597,8 @@ __global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __gr
   __syncthreads();
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  constexpr int kAhead = 8;
   for (int k0 = warp; k0 < parts; k0 += kAhead * kQaMergeWarps) {
-    float4 y[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int k = k0 + i * kQaMergeWarps;
-      y[i] = k < parts ? __ldcg(reinterpret_cast<const float4 *>(part(k) + head * kHeadDim + 4 * lane))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    if (k0 > warp) fetch(k0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int k = k0 + i * kQaMergeWarps;
@@ -639,7 +665,7 @@ QaLayout qa_layout(const gqa_q8_desc_t &d, int sms) {
   y.whole = d.max_seq_len <= kQaWholeTokens;
   y.hg = 1;
   if (!y.whole)
-    while (y.hg < kQaWarps && d.num_kv_heads % (2 * y.hg) == 0) y.hg *= 2;
+    while (y.hg < kQaWarps && d.num_kv_heads % (2 * y.hg) == 0 && d.num_kv_heads / y.hg > 8) y.hg *= 2;
   const long long units = d.num_kv_heads / y.hg, slots = static_cast<long long>(sms) * (G > 8 ? 1 : 2);
   if (y.whole) {
     y.W = d.batch;
