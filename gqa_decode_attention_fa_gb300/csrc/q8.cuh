@@ -37,21 +37,17 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
 }
 
 // The sequence that packed row n belongs to, or -1: the last b of the batch with offsets[b] <= n, if n
-// is below offsets[b + 1] too.  Every lane of a warp calls this alike; two loads deep for up to 1024
-// sequences.
-__device__ __forceinline__ int sequence_of_row(const int32_t *offsets, int B, int n, int lane, int *first, int *end) {
-  static_assert(GQA_MAX_BATCH <= 32 * 32, "two steps of 32");
-  const int per = (B + 31) / 32;
-  const uint32_t le = __ballot_sync(0xffffffffu, lane * per < B && offsets[min(lane * per, B)] <= n);
-  if (le == 0) return -1;
-  const int base = (31 - __clz(le)) * per;
-  const int x = lane <= per && base + lane <= B ? offsets[base + lane] : 0x7fffffff;
-  const uint32_t mine = __ballot_sync(0xffffffffu, lane < per && base + lane < B && x <= n);
-  if (mine == 0) return -1;
-  const int at = 31 - __clz(mine);
-  *first = __shfl_sync(0xffffffffu, x, at);
-  *end = at < 31 ? __shfl_sync(0xffffffffu, x, at + 1) : offsets[base + 32];
-  return n < *end ? base + at : -1;
+// is below offsets[b + 1] too.
+__device__ __forceinline__ int sequence_of_row(const int32_t *offsets, int B, int n, int *first, int *end) {
+  int b = 0, above = B;
+  while (above - b > 1) {
+    const int mid = (b + above) / 2;
+    if (offsets[mid] <= n) b = mid;
+    else above = mid;
+  }
+  *first = offsets[b];
+  *end = offsets[b + 1];
+  return *first <= n && n < *end ? b : -1;
 }
 
 }  // namespace gqa

@@ -1,16 +1,20 @@
 // Rows of an 8-bit KV cache (include/gqa_q8.h): quantised as they are appended, and read back.
 //
-// A warp takes one token, or a part of its 2 H_kv rows (K heads, then V heads): 16 lanes to a row of
-// 128 bf16 values when appending, 8 lanes to a row of 128 codes when reading, 16 bytes a lane either way, all of a
-// part's loads on their way before the first is used.
+// The rows of all tokens are numbered, a token's 2 H_kv (K heads, then V heads) behind each other.  A warp takes 16 of
+// them (4 where there are few), eight lanes to a row and 16 of its values to a lane, all of its loads on their way
+// before the first is used; a lane finds one row's place in the cache.
 //
-// Quantising: scale = max |x| / Q.  The level next to x / scale, ties to even, follows from the
-// quotient cut to binary32 with its last bit set where anything was cut (so that a quotient next to
-// the border of two levels stays on its side): q = x (1 / scale) improved once, and the sign of its
-// exact remainder x - q scale.  Rows so small that the remainder would underflow are scaled by 2^80
-// with their scale.
+// Quantising.  scale = max |x| / Q (1 + d), |d| <= 2^-24.  The codes change at quotients x / scale on the borders
+// of levels, which have few bits (5 for e4m3, 8 for int8), as x and max |x| have (8): x Q / max |x| is either
+// on a border or at least 2^-16 of it away.  So any quotient within 2^-17 gives the right code, but on
+// the borders, where the sign of d decides, the same one for the row, and where d is 0 the tie is a tie.
+// q = x (1 / scale) in two terms, multiplied by 1 - 2^-21 sign(d), falls on the right side, or on
+// the border itself (checked for all significands of x and max |x|).  Rows below 2^-60, whose scale may have lost bits, are
+// divided exactly: q cut to binary32 with its last bit set where anything was cut.
+//   The append is bound by its arithmetic and the way to a row's place rather than by HBM.
 #include <string.h>
 
+#include "pairmath.cuh"
 #include "q8.cuh"
 
 namespace gqa {
@@ -25,7 +29,6 @@ struct Q8RowsParams {
   long long k_stride, v_stride;
   int B, N, Hkv;
   int paged, max_seq, max_blocks, num_blocks;
-  int parts;  // warps a token
 };
 
 namespace {
@@ -33,25 +36,45 @@ namespace {
 constexpr int kRowWarps = 8;
 
 // Where packed row n lives in the cache: its row, -1 if nothing is to be done, -2 if its page id is
-// outside the pool.  Every lane alike.
-__device__ __forceinline__ long long q8_cache_row(const Q8RowsParams &p, int n, int lane) {
+// outside the pool.
+__device__ __forceinline__ long long q8_cache_row(const Q8RowsParams &p, int n) {
   int b = n, first = n, end = n + 1;
-  if (p.offsets) b = sequence_of_row(p.offsets, p.B, n, lane, &first, &end);
+  if (p.offsets) b = sequence_of_row(p.offsets, p.B, n, &first, &end);
   if (b < 0 || first < 0 || end > p.N) return -1;  // (flagged by the first CTA, or no sequence's row)
   const int start = p.slot_start ? p.slot_start[b] : 0;
   if (start < 0 || static_cast<long long>(start) + (end - first) > p.max_seq) {
-    if (lane == 0) flag_error(p.err, start < 0 ? GQA_DEVERR_POSITION : GQA_DEVERR_SEQLEN);
+    flag_error(p.err, start < 0 ? GQA_DEVERR_POSITION : GQA_DEVERR_SEQLEN);
     return -1;
   }
   const int slot = start + (n - first);
   if (!p.paged) return static_cast<long long>(b) * p.max_seq + slot;
   const int pg = p.page_table[static_cast<long long>(b) * p.max_blocks + slot / kTile];
   if (pg < 0 || pg >= p.num_blocks) {
-    if (lane == 0) flag_error(p.err, GQA_DEVERR_PAGE);
+    flag_error(p.err, GQA_DEVERR_PAGE);
     return -2;
   }
   return static_cast<long long>(pg) * kTile + (slot & (kTile - 1));
 }
+
+// The rows of a warp, R of them: lane r % R knows the r-th one's token and place in it, and finds its place in the cache.
+template <int R>
+struct Q8Rows {
+  int n, r;  // token and row of the token; n = -1 behind the last one
+
+  __device__ __forceinline__ Q8Rows(const Q8RowsParams &p, int lane) {
+    const uint32_t rows = 2u * p.Hkv;  // N rows < 2^32
+    const uint64_t all = static_cast<uint64_t>(blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * R + (lane % R);
+    const uint32_t at = static_cast<uint32_t>(all), t = at / rows;
+    n = all < static_cast<uint64_t>(rows) * p.N ? static_cast<int>(t) : -1;
+    r = static_cast<int>(at - t * rows);
+  }
+  // The row of codes, or -1 or -2 as above.
+  __device__ __forceinline__ long long find(const Q8RowsParams &p) const {
+    if (n < 0) return -1;
+    const long long crow = q8_cache_row(p, n);
+    return crow < 0 ? crow : crow * p.Hkv + (r < p.Hkv ? r : r - p.Hkv);
+  }
+};
 
 // Sequences whose offsets are not in order, flagged once a call.
 __device__ __forceinline__ void q8_check_offsets(const Q8RowsParams &p) {
@@ -72,109 +95,126 @@ __device__ __forceinline__ float quotient(float a, float s, float inv) {
   return __int_as_float(bits);
 }
 
-// The codes of a row: the lane's 8 values (bf16 pairs), the row's 16 lanes alike in `largest` (max |x| as bits).
+// The codes of a lane's 16 values (bf16 pairs); `largest` is max |x| of the row as bits.
 template <int FMT>
-__device__ __forceinline__ uint2 quantise8(const uint4 &raw, uint32_t largest, float *scale) {
+__device__ __forceinline__ uint4 quantise16(const uint4 (&raw)[2], uint32_t largest, float *scale) {
   constexpr float kMost = FMT == GQA_Q8_E4M3 ? 448.f : 127.f;
-  float s = __fdiv_rn(__uint_as_float(largest << 16), kMost);
+  const float most = __uint_as_float(largest << 16);
+  float s = __fdiv_rn(most, kMost);
   const bool usable = largest - 1u < 0x7f7fu;  // not zero, finite
   *scale = usable ? s : largest == 0 ? 0.f : __uint_as_float(0x7fc00000u);
-  if (!usable) return make_uint2(0, 0);
-  float up = 1.f;
-  if (largest < 0x2180u) up = 0x1p80f;  // below 2^-60
-  s *= up;
+  if (!usable) return make_uint4(0, 0, 0, 0);
+  const bool small = largest < 0x2180u;  // below 2^-60
+  if (small) s *= 0x1p80f;
   const float inv = __frcp_rn(s);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const float d = fmaf(s, kMost, -most);  // its sign is that of the scale's rounding
+  float e = fmaf(-inv, s, 1.f);
+  if (d != 0.f) e -= copysignf(0x1p-21f, d);
+  const f2 hi = make_f2(inv, inv), lo = make_f2(inv * e, inv * e);
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float x0 = bf16_lo_to_float(w[i]) * up, x1 = bf16_hi_to_float(w[i]) * up;
-    const float q0 = quotient(fabsf(x0), s, inv), q1 = quotient(fabsf(x1), s, inv);
-    if (FMT == GQA_Q8_E4M3) {
-      uint16_t y;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(copysignf(q1, x1)), "f"(copysignf(q0, x0)));
-      c[i] = y;
-    } else {  // added to 1.5 2^23 the quotient is rounded to a whole number, ties to even, in the low bits
-      const uint32_t y0 = __float_as_uint(copysignf(fminf(q0, kMost), x0) + 12582912.f);
-      const uint32_t y1 = __float_as_uint(copysignf(fminf(q1, kMost), x1) + 12582912.f);
-      c[i] = __byte_perm(y0, y1, 0x0040);
+    const uint4 &x = raw[i >> 1];
+    const uint32_t w[2] = {i & 1 ? x.z : x.x, i & 1 ? x.w : x.y};
+    f2 q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f2 a = make_f2(bf16_lo_to_float(w[k]), bf16_hi_to_float(w[k]));
+      q[k] = fma_f2(a, hi, mul_f2(a, lo));
     }
+    if (small) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float a0 = bf16_lo_to_float(w[k]) * 0x1p80f, a1 = bf16_hi_to_float(w[k]) * 0x1p80f;
+        q[k] = make_f2(copysignf(fminf(quotient(fabsf(a0), s, inv), kMost), a0),
+                       copysignf(fminf(quotient(fabsf(a1), s, inv), kMost), a1));
+      }
+    }
+    uint32_t y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float q0, q1;
+      if (FMT == GQA_Q8_E4M3) {
+        split_f2(q[k], q0, q1);
+        uint16_t z;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(z) : "f"(q1), "f"(q0));
+        y[k] = z;
+      } else {  // added to 1.5 2^23 the quotient is rounded to a whole number, ties to even, in the low bits
+        split_f2(add_f2(q[k], make_f2(12582912.f, 12582912.f)), q0, q1);
+        y[k] = __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x0040);
+      }
+    }
+    c[i] = __byte_perm(y[0], y[1], 0x5410);
   }
-  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+  return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 }  // namespace
 
-// U pairs of rows a warp, those from 2 U part on.
+// U groups of four rows a warp.
 template <int FMT, int U>
 __global__ void __launch_bounds__(32 * kRowWarps) q8_append_kernel(const Q8RowsParams p) {
   griddep_wait();
   q8_check_offsets(p);
-  const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
-  const long long at = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int n = static_cast<int>(at / p.parts), part = static_cast<int>(at - static_cast<long long>(n) * p.parts);
-  if (n >= p.N) return;
-  const int r0 = 2 * U * part + half, rows = 2 * p.Hkv;
-  uint4 x[U];
+  const int lane = threadIdx.x & 31, sub = lane >> 3, ql = lane & 7;
+  const Q8Rows<4 * U> mine(p, lane);
+  uint4 x[U][2];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = r0 + 2 * u;
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
+    const int n = __shfl_sync(0xffffffffu, mine.n, 4 * u + sub), r = __shfl_sync(0xffffffffu, mine.r, 4 * u + sub);
+    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+    if (n >= 0) {
       const uint16_t *src = r < p.Hkv ? p.k + n * p.k_stride + static_cast<long long>(r) * kHeadDim
                                       : p.v + n * p.v_stride + static_cast<long long>(r - p.Hkv) * kHeadDim;
-      x[u] = *reinterpret_cast<const uint4 *>(src + 8 * hl);
+      x[u][0] = reinterpret_cast<const uint4 *>(src + 16 * ql)[0];
+      x[u][1] = reinterpret_cast<const uint4 *>(src + 16 * ql)[1];
     }
   }
-  const long long crow = q8_cache_row(p, n, lane);
-  if (crow < 0) return;
+  const long long found = mine.find(p);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = r0 + 2 * u;
-    uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
-                          __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
+    const long long to = __shfl_sync(0xffffffffu, found, 4 * u + sub);
+    const bool is_k = __shfl_sync(0xffffffffu, mine.r, 4 * u + sub) < p.Hkv;
+    uint32_t m = 0;
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = 0; i < 2; ++i)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[u][i].x & 0x7fff7fffu, x[u][i].y & 0x7fff7fffu),
+                               __vmaxu2(x[u][i].z & 0x7fff7fffu, x[u][i].w & 0x7fff7fffu)));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     float scale;
-    const uint2 c = quantise8<FMT>(x[u], max(m & 0xffffu, m >> 16), &scale);
-    if (r < rows) {
-      const int h = r < p.Hkv ? r : r - p.Hkv;
-      const long long to = crow * p.Hkv + h;
-      *reinterpret_cast<uint2 *>((r < p.Hkv ? p.k_codes : p.v_codes) + to * kHeadDim + 8 * hl) = c;
-      if (hl == 0) (r < p.Hkv ? p.k_scale : p.v_scale)[to] = scale;
+    const uint4 c = quantise16<FMT>(x[u], max(m & 0xffffu, m >> 16), &scale);
+    if (to >= 0) {
+      *reinterpret_cast<uint4 *>((is_k ? p.k_codes : p.v_codes) + to * kHeadDim + 16 * ql) = c;
+      if (ql == 0) (is_k ? p.k_scale : p.v_scale)[to] = scale;
     }
   }
 }
 
-// U groups of four rows a warp, those from 4 U part on.
 template <int FMT, int U>
 __global__ void __launch_bounds__(32 * kRowWarps) q8_read_kernel(const Q8RowsParams p) {
   griddep_wait();
   q8_check_offsets(p);
   const int lane = threadIdx.x & 31, sub = lane >> 3, ql = lane & 7;
-  const long long at = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int n = static_cast<int>(at / p.parts), part = static_cast<int>(at - static_cast<long long>(n) * p.parts);
-  if (n >= p.N) return;
-  const long long crow = q8_cache_row(p, n, lane);
-  if (crow == -1) return;
-  const int r0 = 4 * U * part + sub, rows = 2 * p.Hkv;
+  const Q8Rows<4 * U> mine(p, lane);
+  const long long found = mine.find(p);
   uint4 x[U];
   float s[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = r0 + 4 * u;
+    const long long from = __shfl_sync(0xffffffffu, found, 4 * u + sub);
+    const bool is_k = __shfl_sync(0xffffffffu, mine.r, 4 * u + sub) < p.Hkv;
     x[u] = make_uint4(0, 0, 0, 0);
     s[u] = 0.f;
-    if (r < rows && crow >= 0) {
-      const long long from = crow * p.Hkv + (r < p.Hkv ? r : r - p.Hkv);
-      x[u] = *reinterpret_cast<const uint4 *>((r < p.Hkv ? p.k_codes : p.v_codes) + from * kHeadDim + 16 * ql);
-      s[u] = (r < p.Hkv ? p.k_scale : p.v_scale)[from];
+    if (from >= 0) {
+      x[u] = *reinterpret_cast<const uint4 *>((is_k ? p.k_codes : p.v_codes) + from * kHeadDim + 16 * ql);
+      s[u] = (is_k ? p.k_scale : p.v_scale)[from];
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = r0 + 4 * u;
-    if (r >= rows) break;
+    const int n = __shfl_sync(0xffffffffu, mine.n, 4 * u + sub), r = __shfl_sync(0xffffffffu, mine.r, 4 * u + sub);
+    const bool ours = __shfl_sync(0xffffffffu, found, 4 * u + sub) != -1;
     const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
     uint32_t y[8];
 #pragma unroll
@@ -187,10 +227,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) q8_read_kernel(const Q8RowsPar
         y[2 * i + e] = pack_bf16(f.x * s[u], f.y * s[u]);
       }
     }
-    uint16_t *dst = r < p.Hkv ? p.k_out + n * p.k_stride + static_cast<long long>(r) * kHeadDim
-                              : p.v_out + n * p.v_stride + static_cast<long long>(r - p.Hkv) * kHeadDim;
-    reinterpret_cast<uint4 *>(dst + 16 * ql)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    reinterpret_cast<uint4 *>(dst + 16 * ql)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    if (ours) {
+      uint16_t *dst = r < p.Hkv ? p.k_out + n * p.k_stride + static_cast<long long>(r) * kHeadDim
+                                : p.v_out + n * p.v_stride + static_cast<long long>(r - p.Hkv) * kHeadDim;
+      reinterpret_cast<uint4 *>(dst + 16 * ql)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      reinterpret_cast<uint4 *>(dst + 16 * ql)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
   }
 }
 
@@ -247,17 +289,15 @@ gqa_status_t q8_rows_params(const gqa_q8_desc_t &d, const void *k, const void *v
   return check_device(d.device);
 }
 
-// Launches `few` (a pair or a group of rows a warp) where the rows are few, else `many` (kMany of them).
+// Launches `few` (4 rows a warp) where the rows are few, else `many` (16).
 template <typename Kernel>
-gqa_status_t q8_launch_rows(Q8RowsParams &p, int device, Kernel *few, Kernel *many, int rows_few, int rows_many,
-                            void *stream) {
+gqa_status_t q8_launch_rows(const Q8RowsParams &p, int device, Kernel *few, Kernel *many, void *stream) {
   DeviceGuard guard(device);
   if (!guard.ok) return GQA_ERR_CUDA;
-  const bool small = static_cast<long long>(p.N) * p.Hkv <= 2048;
-  const int per = small ? rows_few : rows_many;
-  p.parts = (2 * p.Hkv + per - 1) / per;
-  const long long ctas = (static_cast<long long>(p.N) * p.parts + kRowWarps - 1) / kRowWarps;
-  if (launch_pdl(small ? few : many, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRowWarps), 0,
+  const long long rows = 2LL * p.N * p.Hkv;
+  const bool small = rows <= 4096;
+  const long long per = kRowWarps * (small ? 4 : 16);
+  if (launch_pdl(small ? few : many, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(32 * kRowWarps), 0,
                  static_cast<cudaStream_t>(stream), p) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
@@ -284,9 +324,9 @@ extern "C" gqa_status_t gqa_q8_append(const gqa_q8_desc_t *desc, const void *k, 
   p.k = static_cast<const uint16_t *>(k);
   p.v = static_cast<const uint16_t *>(v);
   return d.format == GQA_Q8_E4M3 ? q8_launch_rows(p, d.device, q8_append_kernel<GQA_Q8_E4M3, 1>,
-                                                  q8_append_kernel<GQA_Q8_E4M3, 4>, 2, 8, stream)
+                                                  q8_append_kernel<GQA_Q8_E4M3, 4>, stream)
                                  : q8_launch_rows(p, d.device, q8_append_kernel<GQA_Q8_INT8, 1>,
-                                                  q8_append_kernel<GQA_Q8_INT8, 4>, 2, 8, stream);
+                                                  q8_append_kernel<GQA_Q8_INT8, 4>, stream);
 }
 
 extern "C" gqa_status_t gqa_q8_read(const gqa_q8_desc_t *desc, const void *k_codes, const void *v_codes,
@@ -302,7 +342,7 @@ extern "C" gqa_status_t gqa_q8_read(const gqa_q8_desc_t *desc, const void *k_cod
   p.k_out = static_cast<uint16_t *>(k_out);
   p.v_out = static_cast<uint16_t *>(v_out);
   return d.format == GQA_Q8_E4M3 ? q8_launch_rows(p, d.device, q8_read_kernel<GQA_Q8_E4M3, 1>,
-                                                  q8_read_kernel<GQA_Q8_E4M3, 4>, 4, 16, stream)
+                                                  q8_read_kernel<GQA_Q8_E4M3, 4>, stream)
                                  : q8_launch_rows(p, d.device, q8_read_kernel<GQA_Q8_INT8, 1>,
-                                                  q8_read_kernel<GQA_Q8_INT8, 4>, 4, 16, stream);
+                                                  q8_read_kernel<GQA_Q8_INT8, 4>, stream);
 }
