@@ -57,8 +57,7 @@ typedef struct gqa_packed_desc {
  * small its weight.  The rounding of the result does not depend on timing or on the other sequences of
  * the batch: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, bad sizes or strides), GQA_ERR_UNSUPPORTED
- * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, B > GQA_MAX_BATCH, more than 2^31 - 1 rows N_q H_q or
- * N_k H_kv), GQA_ERR_CUDA.
+ * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, more than 2^31 - 1 rows N_q H_q or N_k H_kv), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_packed_attn(const gqa_packed_desc_t *desc, const void *q, const void *k, const void *v,
                              const int32_t *q_offsets, const int32_t *k_offsets, void *out, uint32_t *device_errors,

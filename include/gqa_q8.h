@@ -72,8 +72,8 @@ typedef struct gqa_q8_desc {
  * Every slot written must belong to its sequence alone (no shared page: gqa_pages.h).
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, page_table given for a contiguous cache
  * or missing for a paged one, bad sizes, strides or format, NULL offsets with N != B),
- * GQA_ERR_UNSUPPORTED (head_dim != 128, B > GQA_MAX_BATCH, block_size other than 0 or 64, more than 2^31 - 1
- * cache rows, or rows N H_kv), GQA_ERR_CUDA.
+ * GQA_ERR_UNSUPPORTED (head_dim != 128, block_size other than 0 or 64, more than 2^31 - 1 cache rows or rows
+ * N H_kv), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_q8_append(const gqa_q8_desc_t *desc, const void *k, const void *v, void *k_codes, void *v_codes,
                            float *k_scale, float *v_scale, const int32_t *page_table, const int32_t *offsets,
