@@ -85,17 +85,17 @@ struct PackedUnit {
   int nt[2];       // key tiles of each stream's tile
   int steps[2];    // of the last one, sixteens of keys that some row sees
   int kv;
-  uint32_t bad;    // a value that not all rows see is not finite
+  uint32_t bad;    // a value that not all rows see, or none does, is not finite (known once unit_looked says so)
 };
 
 struct PackedShared {
   uint64_t k_full[kPkKStages], k_empty[kPkKStages], v_full[kPkVStages], v_clean[kPkVStages], v_empty[kPkVStages];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, q_full[2], q_empty[2];
-  uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_checked[kPkSlots][2];
+  uint64_t unit_full[kPkSlots], unit_empty[kPkSlots], unit_looked[kPkSlots], unit_checked[kPkSlots][2];
   PackedUnit unit[kPkSlots];
   uint32_t tmem;
 };
-constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 4 + 4 * kPkSlots;
+constexpr int kPkNumBars = 2 * kPkKStages + 3 * kPkVStages + 2 + 4 + 5 + 4 + 5 * kPkSlots;
 constexpr int kPkSmemBytes = kPkOffBar + static_cast<int>(sizeof(PackedShared));
 static_assert(kPkSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       uint64_t *bar = bars + i;
       int count = 1;
       if ((bar >= sh.p_full[0] && bar < sh.o_full) || (bar >= sh.o_free && bar < &sh.drain)) count = 4;
-      if (bar >= sh.unit_empty && bar < sh.unit_checked[0]) count = 11;  // every warp but the one that finds them
+      if (bar >= sh.unit_empty && bar < sh.unit_looked) count = 11;  // every warp but the one that finds them
       mbar_init(smem_addr(bar), count);
     }
     fence_barrier_init();
@@ -341,6 +341,33 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           mbar_arrive(smem_addr(&sh.unit_full[slot.at]));
         }
         if (x.tokens == 0) break;
+        // Behind the first query's last key a row of V is seen by some rows of the unit or, from the sequence's end to the last
+        // sixteen that is multiplied, by none: P is 0 there, but 0 x inf is not.  Looked at here, ahead of time and in global
+        // memory: shared memory is the MMAs' (a warp that looked at the tiles there took up to 5900 cycles a unit).
+        const int later = x.nt[1] > 0 ? 1 : 0;
+        const int first = max(x.see0, 0);
+        const int last = min(x.nt[later] > 0 ? (x.nt[later] - 1) * kPkKeys + 16 * x.steps[later] : 0, p.Nk - x.k0);
+        bool bad = false;
+        constexpr int kAhead = 8;
+        for (int r = first + (lane >> 4); r < last; r += 2 * kAhead) {
+          uint4 y[kAhead];
+          uint32_t most = 0;
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            y[i] = r + 2 * i < last ? __ldg(reinterpret_cast<const uint4 *>(p.v + (x.k0 + r + 2 * i) * p.v_stride +
+                                                                            x.kv * kHeadDim + 8 * (lane & 15)))
+                                    : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            most = __vmaxu2(most, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
+                                           __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
+          bad |= max(most & 0xffffu, most >> 16) >= 0x7f80u;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+          if (bad) sh.unit[slot.at].bad = 1;
+          mbar_arrive(smem_addr(&sh.unit_looked[slot.at]));
+        }
       }
       if (!ok && lane == 0) flag_error(p.err, GQA_DEVERR_TIMEOUT);
     } else if (warp == kPkProducerWarp) {
@@ -400,10 +427,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       }
     } else if (warp == kPkCheckWarp) {
       // ---------------------------------------------------------------- values that some rows must not see
-      // Behind the first query's last key a row of V is seen by some rows of the unit or by none: P is 0
-      // there, but 0 x inf is not.  Up to the last step of 16 keys that is multiplied, rows behind the
-      // sequence's end are cleared, and so is a value before it that is not finite, which the epilogue gives to
-      // the rows that see it.
+      // Where such a value was found, rows of V behind the sequence's end are cleared in the tiles, and so is a
+      // value before it that is not finite, which the epilogue gives to the rows that see it.
       Ring<kPkVStages> vs;
       Ring<kPkSlots> slot;
       for (; ok; slot.step()) {
@@ -421,37 +446,28 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           // rows from r0 on, to r2; the sequence's end
           const int r0 = max(0, max(x.see0, 0) - j * kPkKeys), r1 = x.keys - j * kPkKeys;
           const int r2 = j + 1 < nt ? kPkKeys : 16 * (x.nt[1] == nt ? x.steps[1] : x.steps[0]);
+          bool bad = false;
           if (r0 < r2) {
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.unit_looked[slot.at]), slot.phase));
+            if (!ok) break;
+            bad = *reinterpret_cast<volatile uint32_t *>(&sh.unit[slot.at].bad) != 0;
+          }
+          if (bad) {
             uint4 *tile = reinterpret_cast<uint4 *>(smem + kPkOffV + vs.at * kPkTileBytes);
             auto at = [&](int c) { return tile + ((c & 8) << 7) + (c >> 4) * 8 + (c & 7); };  // chunk: row, panel, 16 bytes
-            bool bad = false;
-            const int c1 = 16 * min(r1, r2);
-            constexpr int kAhead = 8;
-            for (int c0 = 16 * r0 + lane; c0 < c1; c0 += 32 * kAhead) {
-              uint4 y[kAhead];
-              uint32_t ones = 0;
+            for (int c = 16 * r0 + lane; c < 16 * r2; c += 32) {
+              if (c >= 16 * r1) {
+                *at(c) = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint32_t *z = reinterpret_cast<uint32_t *>(at(c));
 #pragma unroll
-              for (int i = 0; i < kAhead; ++i) y[i] = c0 + 32 * i < c1 ? *at(c0 + 32 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < kAhead; ++i)  // an exponent of all ones carries into the sign's place
-                ones |= ((y[i].x & 0x7f807f80u) + 0x00800080u) | ((y[i].y & 0x7f807f80u) + 0x00800080u) |
-                        ((y[i].z & 0x7f807f80u) + 0x00800080u) | ((y[i].w & 0x7f807f80u) + 0x00800080u);
-              if (ones & 0x80008000u) {
-                bad = true;
-#pragma unroll 1
-                for (int c = c0; c < min(c1, c0 + 32 * kAhead); c += 32) {
-                  uint32_t *z = reinterpret_cast<uint32_t *>(at(c));
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
-                    if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
-                  }
-                }
+              for (int k = 0; k < 4; ++k) {
+                if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+                if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
               }
             }
-            for (int c = 16 * max(r0, r1) + lane; c < 16 * r2; c += 32) *at(c) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
-            if (__any_sync(0xffffffffu, bad) && lane == 0) sh.unit[slot.at].bad = 1;
           }
           __syncwarp();
           if (lane == 0) {

@@ -665,7 +665,8 @@ QaLayout qa_layout(const gqa_q8_desc_t &d, int sms) {
   y.whole = d.max_seq_len <= kQaWholeTokens;
   y.hg = 1;
   if (!y.whole)
-    while (y.hg < kQaWarps && d.num_kv_heads % (2 * y.hg) == 0 && d.num_kv_heads / y.hg > 8) y.hg *= 2;
+    while (y.hg < kQaWarps && d.num_kv_heads % (2 * y.hg) == 0 && d.num_kv_heads / y.hg > (d.num_kv_heads < 32 ? 8 : 4))
+      y.hg *= 2;
   const long long units = d.num_kv_heads / y.hg, slots = static_cast<long long>(sms) * (G > 8 ? 1 : 2);
   if (y.whole) {
     y.W = d.batch;
