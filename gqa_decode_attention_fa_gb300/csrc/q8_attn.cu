@@ -658,11 +658,20 @@ struct QaLayout {
   int hg, W;
   bool whole;
 };
-constexpr int kQaWholeTokens = 512;
+// A CTA to a sequence and KV head, its eight warps sharing the tokens, and nothing to join, where no sequence can be
+// long: 5 ns a token against 4 to 8 us for cuts, their ends and the merge.  (8 KV heads, us whole / cut: one sequence of
+// 700 tokens 8.4 / 9.3, of 1500 13.0 / 9.3; 16 sequences of up to 1500 12.6 / 17.6, of up to 2500 18.3 / 21.3, of up to 4500
+// 29.5 / 30.3; 200 of up to 2500 108 / 115.)
+constexpr int kQaWholeTokens = 1024;
+constexpr int kQaWholeTokensMany = 2560, kQaMany = 128;  // where there are as many sequences and heads
+// KV heads of a CTA where sequences are cut: one, so that few parts are to be joined, but in wide caches, whose rows are
+// better read, and whose scales lie 32 bytes to eight heads (8 KV heads, 8 x 32k tokens: 92.6 us with 1, 93.0 with 2, 93.6
+// with 4, 99 with 8; one 128k sequence 52 / 56 / 59 / 69; 16 KV heads, 2 x 30k: 50 / 50 / 51 / 55; 32, 4 x 8k: 66 / 60 / 54 / 52).
 QaLayout qa_layout(const gqa_q8_desc_t &d, int sms) {
   QaLayout y;
   const int G = d.num_q_heads / d.num_kv_heads;
-  y.whole = d.max_seq_len <= kQaWholeTokens;
+  y.whole = d.max_seq_len <= kQaWholeTokens ||
+            (d.max_seq_len <= kQaWholeTokensMany && static_cast<long long>(d.batch) * d.num_kv_heads >= kQaMany);
   y.hg = 1;
   if (!y.whole)
     while (y.hg < kQaWarps && d.num_kv_heads % (2 * y.hg) == 0 && d.num_kv_heads / y.hg > (d.num_kv_heads < 32 ? 8 : 4))

@@ -85,6 +85,10 @@ def i32(x):
     return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
 
 
+def offsets_of(lengths):
+    return np.concatenate([[0], np.cumsum(lengths)])
+
+
 def errors():
     return torch.zeros(1, dtype=torch.int32, device="cuda")
 
@@ -320,6 +324,34 @@ def test_many_sequences_attend():
         ref, mag = attend(c, q, lens, 4)
         near(out, ref, mag)
         assert err == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,cap,top,wide", [
+    (700, 4, 2, 6000, 100, 3),       # more sequences than ranges, most of them short
+    (90, 4, 1, 30000, 60, 900),
+    (40, 64, 16, 9000, 50, 1000),    # KV heads in twos, in fours, in eights
+    (10, 32, 32, 9000, 300, 500),
+    (6, 64, 64, 5000, 300, 500),
+    (5, 48, 3, 4000, 200, 1500),     # 16 heads a KV head
+])
+def test_lengths_far_below_the_capacity(B, Hq, Hkv, cap, top, wide):
+    """A pool smaller than every sequence at full length: the sequences are cut by the lengths on the device."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, top + 1, B)
+    lens[rng.random(B) < 0.2] = 0
+    lens[rng.integers(0, B)] = wide
+    need = (lens + 63) // 64
+    c = Cache(1, Hkv, 64 * int(need.sum()), "e4m3", True, seed=B)
+    pages, at = c.table[0].cpu().numpy(), offsets_of(need)
+    table = np.full((B, (cap + 63) // 64), -7, np.int32)
+    for b in range(B):
+        table[b, :need[b]] = pages[at[b]:at[b + 1]]
+    c.B, c.cap, c.table = B, cap, i32(table)
+    q = rows_of(3, B, Hq)
+    out, err = token(c, q, lens, Hq)
+    ref, mag = attend(c, q, lens, Hq)
+    near(out, ref, mag)
+    assert err == 0
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
