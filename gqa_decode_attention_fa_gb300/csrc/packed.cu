@@ -822,6 +822,7 @@ extern "C" gqa_status_t gqa_packed_attn(const gqa_packed_desc_t *desc, const voi
   if (static_cast<long long>(d.num_queries) * d.num_q_heads > 0x7fffffffLL ||
       static_cast<long long>(d.num_keys) * d.num_kv_heads > 0x7fffffffLL || dense_q > 0x7fffffffLL)
     return GQA_ERR_UNSUPPORTED;
+  if (d.num_keys > 1 << 26) return GQA_ERR_UNSUPPORTED;  // a unit stays well within the limit of a wait (2 s)
   if (!q || !k || !v || !q_offsets || !out) return GQA_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) || !aligned_to(q_offsets, 4) ||
       !aligned_to(k_offsets, 4) || !aligned_to(device_errors, 4))

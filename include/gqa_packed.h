@@ -31,7 +31,7 @@ typedef struct gqa_packed_desc {
     int num_kv_heads; /* H_kv; H_q % H_kv == 0 and G = H_q / H_kv <= 16 */
     int head_dim;     /* d; must be 128 */
     int num_queries;  /* N_q >= 1 */
-    int num_keys;     /* N_k >= 1 */
+    int num_keys;     /* N_k, 1..2^26 */
     int causal;       /* non-zero: the mask above; 0: every query sees all its sequence's keys */
     int device;       /* CUDA device ordinal the call runs on */
     int q_stride;     /* elements between the rows of consecutive tokens of q, k and v: */
@@ -57,7 +57,8 @@ typedef struct gqa_packed_desc {
  * small its weight.  The rounding of the result does not depend on timing or on the other sequences of
  * the batch: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, bad sizes or strides), GQA_ERR_UNSUPPORTED
- * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, more than 2^31 - 1 rows N_q H_q or N_k H_kv), GQA_ERR_CUDA.
+ * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, more than 2^31 - 1 rows N_q H_q or N_k H_kv, more than 2^26
+ * keys), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_packed_attn(const gqa_packed_desc_t *desc, const void *q, const void *k, const void *v,
                              const int32_t *q_offsets, const int32_t *k_offsets, void *out, uint32_t *device_errors,

@@ -107,7 +107,7 @@ def _packed(args=None, **over):
     (dict(batch=0), INV), (dict(batch=1025), INV), (dict(num_q_heads=0), INV), (dict(num_kv_heads=0), INV), (dict(head_dim=64), UNS),
     (dict(num_q_heads=9), UNS), (dict(num_q_heads=34), UNS), (dict(num_queries=0), INV), (dict(num_keys=0), INV), (dict(num_keys=-1), INV),
     (dict(q_stride=1020), INV), (dict(q_stride=1016), INV), (dict(k_stride=128), INV), (dict(v_stride=-256), INV), (dict(v_stride=260), INV),
-    (dict(num_queries=1 << 29), UNS), (dict(num_keys=1 << 30), UNS),
+    (dict(num_queries=1 << 29), UNS), (dict(num_keys=1 << 30), UNS), (dict(num_q_heads=1, num_kv_heads=1, num_keys=(1 << 26) + 1), UNS),
 ])
 def test_packed_attn_refuses_bad_geometry(over, status):
     assert _packed(**over) == status
