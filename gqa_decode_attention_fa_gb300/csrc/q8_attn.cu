@@ -17,10 +17,18 @@
 // of its four tokens.
 //   q is scaled to binary16's range by a power of two a row (exact but for elements 2^-29 below the
 // largest).  The scale of K multiplies the score, that of V the weight: x = p vs 2^(m - E), rounded to
-// binary16 (2^-12 of each weight, where the output's own rounding is 2^-9) under a power of two 2^E of its own
+// binary16 (at most 2^-11 of each weight, where the output's own rounding is 2^-8) under a power of two 2^E of its own
 // that follows the largest weight seen, so that neither p nor the scale can pass binary16's range: weights down
 // to 2^-22 of the largest keep 11 bits, those below 2^-32 are lost.  The maximum m is raised lazily, where a score
 // passes it by 8; sums are binary32.
+//
+// Bounds and figures (a GB300 that copies 6.77 TB/s; 40 query over 8 KV heads where nothing else is said).  A token's K and V
+// of a head are 264 bytes, so the cache bounds long calls: 8 sequences of 32768 take 89 us, 6.2 TB/s, 0.92 of the copy rate;
+// one of 131072 with 64 query heads over int8 codes 50 us, 5.5 TB/s, where the fixed costs show: 5.5 us from the launch to the first products
+// (1.7 of them the cut, the rest the first copies' way), 3 us from a range's last products to its partials, 6 us for the
+// join of 38 parts a head.  32 sequences of 512 to 8192 in pages take 52 us, 5.4 TB/s.  One sequence of 256 takes 5.3 us on the
+// device and 8.6 from one call to the next, which is the host's.  At the long calls neither the
+// instruction issue (42 % used) nor the MMAs (16 %) is near a limit.
 #include <math.h>
 #include <string.h>
 
@@ -543,33 +551,48 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
 
 // ------------------------------------------------------------------------------------ merge
 // out = sum_k 2^(s_k - M) o_k / sum_k 2^(s_k - M) over the parts k of a cut sequence (s_k: log-sum, o_k: its normalised
-// output), in the order of the ranges.  A CTA joins one (sequence, query head): warp x takes the parts x, x + 8, ...,
-// a lane four dims; the warps' sums are added in order.
-constexpr int kQaMergeWarps = 8;
-__global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
+// output), in the order of the ranges.  A CTA joins one (sequence, query head): warp x of kWarps takes the parts x, x +
+// kWarps, ..., a lane four dims; the warps' sums are added in order.  One warp finds what to join: with all of them
+// looking, the 32 ragged sequences above took 56.5 us.
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
   __shared__ float s_w[kQaMaxRanges];
-  __shared__ float4 s_o[kQaMergeWarps][32];
+  __shared__ float4 s_o[kWarps][32];
+  __shared__ float s_sum[kWarps];
+  __shared__ int s_what[3];  // sequence, first range, parts
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hq = static_cast<int>(blockIdx.x) % p.Hq, index = static_cast<int>(blockIdx.x) / p.Hq;
   const int kv = hq / p.G, head = hq - kv * p.G;
   // What to join follows from the lengths, which the attention kernel has waited for before it let this one start.
-  const Q8Cut all = q8_cut(p, lane);
-  if (all.whole || all.ranges < 2) return;
-  int b = 0, first = 0;
-  if (p.merge_by_sequence) {
-    b = index;
-    const int per = (p.B + 31) / 32;
-    first = __shfl_sync(0xffffffffu, all.lane_first, b / per);
-    for (int x = b / per * per; x < b; ++x) first += q8_span(p, all, x);
-  } else {
-    if (index + 1 >= all.ranges) return;
-    q8_find(p, all, all.begin(index + 1), &b, &first);
+  if (warp == 0) {
+    const Q8Cut all = q8_cut(p, lane);
+    int b = 0, first = 0, w0 = 0, w1 = 0;
+    if (!all.whole && all.ranges > 1 && (p.merge_by_sequence || index + 1 < all.ranges)) {
+      if (p.merge_by_sequence) {
+        b = index;
+        const int per = (p.B + 31) / 32;
+        first = __shfl_sync(0xffffffffu, all.lane_first, b / per);
+        for (int x = b / per * per; x < b; ++x) first += q8_span(p, all, x);
+      } else {
+        q8_find(p, all, all.begin(index + 1), &b, &first);
+      }
+      const int nu = q8_units(p, b);
+      if (nu > 0) {
+        w0 = all.range_of(first);
+        w1 = all.range_of(first + nu - 1);
+        if (!p.merge_by_sequence && w0 != index) w1 = w0;  // another boundary is its first
+      }
+    }
+    if (lane == 0) {
+      s_what[0] = b;
+      s_what[1] = w0;
+      s_what[2] = w1 - w0 + 1;
+    }
   }
-  const int nu = q8_units(p, b);
-  if (nu == 0) return;
-  const int w0 = all.range_of(first), w1 = all.range_of(first + nu - 1);
-  if (w0 == w1 || (!p.merge_by_sequence && w0 != index)) return;  // not cut, or another boundary is its first
-  const int parts = w1 - w0 + 1;
+  __syncthreads();
+  const int b = s_what[0], w0 = s_what[1], parts = s_what[2];
+  griddep_wait();  // the attention kernel's partials; without any, too, or this kernel could end before that one
+  if (parts < 2) return;  // not cut, or joined by another CTA
   const long long each = static_cast<long long>(p.G) * (kHeadDim + 4);
   auto part = [&](int k) { return p.part + ((static_cast<long long>(w0 + k) * p.Hkv + kv) * 2 + (k == 0 ? 1 : 0)) * each; };
   constexpr int kAhead = 8;
@@ -577,12 +600,11 @@ __global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __gr
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int k = k0 + i * kQaMergeWarps;
+      const int k = k0 + i * kWarps;
       y[i] = k < parts ? __ldcg(reinterpret_cast<const float4 *>(part(k) + head * kHeadDim + 4 * lane))
                        : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
-  griddep_wait();  // the attention kernel's partials
   fetch(warp);
   // every warp finds M by itself
   float M = -INFINITY;
@@ -597,11 +619,11 @@ __global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __gr
   __syncthreads();
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  for (int k0 = warp; k0 < parts; k0 += kAhead * kQaMergeWarps) {
+  for (int k0 = warp; k0 < parts; k0 += kAhead * kWarps) {
     if (k0 > warp) fetch(k0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int k = k0 + i * kQaMergeWarps;
+      const int k = k0 + i * kWarps;
       if (k >= parts) break;
       const float f = fast_exp2(s_w[k] - M);
       sum += f;
@@ -611,12 +633,11 @@ __global__ void __launch_bounds__(32 * kQaMergeWarps) q8_merge_kernel(const __gr
       a.w = fmaf(f, y[i].w, a.w);
     }
   }
-  __shared__ float s_sum[kQaMergeWarps];
   s_o[warp][lane] = a;
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
   if (warp != 0) return;
-  for (int x = 1; x < kQaMergeWarps; ++x) {
+  for (int x = 1; x < kWarps; ++x) {
     const float4 y = s_o[x][lane];
     a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
     sum += s_sum[x];
@@ -784,7 +805,8 @@ extern "C" gqa_status_t gqa_q8_attn(const gqa_q8_desc_t *desc, const void *q, co
   if (launch_pdl(kernel, dim3(static_cast<unsigned>(p.W * (p.Hkv / p.hg))), dim3(kQaThreads),
                  static_cast<size_t>(wide ? Q8Smem<2>::kBytes : Q8Smem<1>::kBytes), s, p) != cudaSuccess ||
       (!y.whole && p.W > 1 &&
-       launch_pdl(q8_merge_kernel, dim3(static_cast<unsigned>(joins)), dim3(32 * kQaMergeWarps), 0, s, p) != cudaSuccess)) {
+       (p.W <= 4LL * p.B ? launch_pdl(q8_merge_kernel<2>, dim3(static_cast<unsigned>(joins)), dim3(64), 0, s, p)
+                         : launch_pdl(q8_merge_kernel<8>, dim3(static_cast<unsigned>(joins)), dim3(256), 0, s, p)) != cudaSuccess)) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
