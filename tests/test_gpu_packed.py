@@ -224,3 +224,37 @@ def test_long_sequences_and_rows_beyond_four_gib():
     ref, mag = attend(w)
     near(out, ref, mag)
     assert err == 0
+
+
+def test_padding_and_replay():
+    """Many packed rows, all of them prompts (a prompt's bits do not depend on the others) or nearly all padding; and a captured
+    call replayed with other lengths."""
+    n = [900, 1300, 40, 2000, 1, 700] * 4
+    w = make(4, 4, n, seed=11)                       # one head a KV head: units of 256 tokens
+    alone = {b: run({**w, "qa": w["qa"][b:b + 2], "ka": w["ka"][b:b + 2]})[0][w["qa"][b]:w["qa"][b + 1]] for b in (3, 4, 21)}
+    out, err = run(w)
+    ref, mag = attend(w)
+    near(out, ref, mag)
+    assert err == 0
+    for b, x in alone.items():
+        assert torch.equal(out[w["qa"][b]:w["qa"][b + 1]], x)
+    big = make(32, 32, [40, 333], seed=12, spare=40000)
+    out, err = run(big)
+    small = {x: big[x][:400] for x in "qkv"} | dict(qa=big["qa"], ka=big["ka"], out=big["out"][:400], given=False)
+    ref, mag = attend(small)
+    near(out[:400], ref, mag)
+    assert err == 0 and torch.equal(out[373:], big["out"][373:])
+    # captured with these lengths, replayed with others
+    w = make(40, 8, [150, 0, 300, 77], seed=13, spare=700)
+    at, out = i32(w["qa"]), w["out"].clone()
+    graph = torch.cuda.CUDAGraph()
+    binding.packed_attn(w["q"], w["k"], w["v"], at, None, out)
+    with torch.cuda.graph(graph):
+        binding.packed_attn(w["q"], w["k"], w["v"], at, None, out)
+    for lengths in ([150, 0, 300, 77], [1, 1, 1, 1], [0, 0, 0, 0], [600, 500, 100, 20]):
+        w["qa"] = w["ka"] = offsets(lengths)
+        at.copy_(i32(w["qa"]))
+        out.copy_(w["out"])
+        graph.replay()
+        ref, mag = attend(w)
+        near(out, ref, mag, norm=False)
