@@ -11,15 +11,34 @@
 // q = x (1 / scale) in two terms, multiplied by 1 - 2^-21 sign(d), falls on the right side, or on
 // the border itself (checked for all significands of x and max |x|).  Rows below 2^-60, whose scale may have lost bits, are
 // divided exactly: q cut to binary32 with its last bit set where anything was cut.
-//   Bounds.  HBM, and the append its arithmetic too (20 instructions a value when each was divided: 32 us where this
-// takes 25): 19k tokens of 8 KV heads appended 25 us = 4.8 TB/s, 0.71 of the measured copy rate, 28k rows read back
-// 29 us = 5.9 TB/s, 0.87.  With 16 rows a warp 25.4 and 29.3, with 32 35 and 30; small calls 2.3 to 2.9 us.
+//   Bounds.  HBM, and the append its arithmetic too (20 instructions a value when each was divided: 32 us where this takes
+// 23): 19k tokens of 8 KV heads appended 23 us = 5.2 TB/s, 0.77 of the measured copy rate, 28k rows read back 28.6 us =
+// 6.0 TB/s, 0.88; small calls 2.2 to 2.8 us.  What counts is that many warps are on their way: an SM's 64 take 32
+// registers each (with 40 and 48 warps 26.8 us), a CTA has four (8: 23.1 us and 28.7, 16: 23.7 and 29.0), and one
+// of its warps looks for the places of all its rows (each warp for its own: 24.6 us).  Warps that stay and load ahead took 30 to
+// 45 us, 16 rows a warp 2 % more than 8, 32 a third more.
 #include <string.h>
 
 #include "pairmath.cuh"
 #include "q8.cuh"
 
 namespace gqa {
+
+// Division by a divisor known beforehand, 2 .. 2^31 (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct Divisor {
+  uint32_t factor, shift;
+  void set(uint32_t d) {
+    int l = 1;
+    while (l < 31 && (1u << l) < d) ++l;
+    factor = static_cast<uint32_t>((((1ull << l) - d) << 32) / d + 1);
+    shift = l - 1;
+  }
+  __host__ __device__ uint32_t divide(uint32_t a) const {
+    const uint32_t t = static_cast<uint32_t>((static_cast<uint64_t>(factor) * a) >> 32);
+    return (t + ((a - t) >> 1)) >> shift;
+  }
+};
 
 struct Q8RowsParams {
   const uint16_t *k, *v;  // append: the packed rows
@@ -31,11 +50,12 @@ struct Q8RowsParams {
   long long k_stride, v_stride;
   int B, N, Hkv;
   int paged, max_seq, max_blocks, num_blocks;
+  Divisor by_rows;  // 2 Hkv
 };
 
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 4;
 
 // Where packed row n lives in the cache: its row, -1 if nothing is to be done, -2 if its page id is
 // outside the pool.
@@ -63,10 +83,10 @@ template <int R>
 struct Q8Rows {
   int n, r;  // token and row of the token; n = -1 behind the last one
 
-  __device__ __forceinline__ Q8Rows(const Q8RowsParams &p, int lane) {
+  __device__ __forceinline__ Q8Rows(const Q8RowsParams &p, int warp, int lane) {
     const uint32_t rows = 2u * p.Hkv;  // N rows < 2^32
-    const uint64_t all = static_cast<uint64_t>(blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * R + (lane % R);
-    const uint32_t at = static_cast<uint32_t>(all), t = at / rows;
+    const uint64_t all = static_cast<uint64_t>(blockIdx.x * kRowWarps + warp) * R + (lane % R);
+    const uint32_t at = static_cast<uint32_t>(all), t = p.by_rows.divide(at);
     n = all < static_cast<uint64_t>(rows) * p.N ? static_cast<int>(t) : -1;
     r = static_cast<int>(at - t * rows);
   }
@@ -95,6 +115,13 @@ __device__ __forceinline__ float quotient(float a, float s, float inv) {
   int bits = __float_as_int(q) + (__float_as_int(r) >> 31);
   if (r != 0.f) bits |= 1;
   return __int_as_float(bits);
+}
+
+// The larger sizes of two bf16 pairs, NaN where either is one; the signs mean nothing.
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
 }
 
 // The codes of a lane's 16 values (bf16 pairs); `largest` is max |x| of the row as bits.
@@ -155,11 +182,12 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&raw)[2], uint32_t larg
 
 // U groups of four rows a warp.
 template <int FMT, int U>
-__global__ void __launch_bounds__(32 * kRowWarps) q8_append_kernel(const Q8RowsParams p) {
+__global__ void __launch_bounds__(32 * kRowWarps, 64 / kRowWarps) q8_append_kernel(const Q8RowsParams p) {
   griddep_wait();
   q8_check_offsets(p);
-  const int lane = threadIdx.x & 31, sub = lane >> 3, ql = lane & 7;
-  const Q8Rows<4 * U> mine(p, lane);
+  __shared__ long long place[kRowWarps * 4 * U];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> 3, ql = lane & 7;
+  const Q8Rows<4 * U> mine(p, warp, lane);
   uint4 x[U][2];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -172,23 +200,28 @@ __global__ void __launch_bounds__(32 * kRowWarps) q8_append_kernel(const Q8RowsP
       x[u][1] = reinterpret_cast<const uint4 *>(src + 16 * ql)[1];
     }
   }
-  const long long found = mine.find(p);
+  // a lane to a row looks for its place, for the whole CTA, while the rows are on their way
+  if (threadIdx.x < kRowWarps * 4 * U)
+    place[threadIdx.x] = Q8Rows<4 * U>(p, threadIdx.x / (4 * U), threadIdx.x).find(p);
+  uint4 c[U];
+  float scale[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long to = __shfl_sync(0xffffffffu, found, 4 * u + sub);
+    uint32_t m = max_abs(max_abs(max_abs(x[u][0].x, x[u][0].y), max_abs(x[u][0].z, x[u][0].w)),
+                         max_abs(max_abs(x[u][1].x, x[u][1].y), max_abs(x[u][1].z, x[u][1].w)));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m &= 0x7fff7fffu;
+    c[u] = quantise16<FMT>(x[u], max(m & 0xffffu, m >> 16), &scale[u]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long to = place[4 * (U * warp + u) + sub];
     const bool is_k = __shfl_sync(0xffffffffu, mine.r, 4 * u + sub) < p.Hkv;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[u][i].x & 0x7fff7fffu, x[u][i].y & 0x7fff7fffu),
-                               __vmaxu2(x[u][i].z & 0x7fff7fffu, x[u][i].w & 0x7fff7fffu)));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float scale;
-    const uint4 c = quantise16<FMT>(x[u], max(m & 0xffffu, m >> 16), &scale);
     if (to >= 0) {
-      *reinterpret_cast<uint4 *>((is_k ? p.k_codes : p.v_codes) + to * kHeadDim + 16 * ql) = c;
-      if (ql == 0) (is_k ? p.k_scale : p.v_scale)[to] = scale;
+      *reinterpret_cast<uint4 *>((is_k ? p.k_codes : p.v_codes) + to * kHeadDim + 16 * ql) = c[u];
+      if (ql == 0) (is_k ? p.k_scale : p.v_scale)[to] = scale[u];
     }
   }
 }
@@ -198,7 +231,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) q8_read_kernel(const Q8RowsPar
   griddep_wait();
   q8_check_offsets(p);
   const int lane = threadIdx.x & 31, sub = lane >> 3, ql = lane & 7;
-  const Q8Rows<4 * U> mine(p, lane);
+  const Q8Rows<4 * U> mine(p, threadIdx.x >> 5, lane);
   const long long found = mine.find(p);
   uint4 x[U];
   float s[U];
@@ -284,6 +317,7 @@ gqa_status_t q8_rows_params(const gqa_q8_desc_t &d, const void *k, const void *v
   p->B = d.batch;
   p->N = d.num_tokens;
   p->Hkv = d.num_kv_heads;
+  p->by_rows.set(2u * d.num_kv_heads);
   p->paged = d.block_size > 0 ? 1 : 0;
   p->max_seq = d.max_seq_len;
   p->max_blocks = capacity_tiles(d.max_seq_len);
