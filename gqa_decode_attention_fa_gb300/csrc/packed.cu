@@ -18,6 +18,18 @@
 // the one before, so a thread that sees S finds O at rest.
 //   P is rounded to bf16 (at most 2^-8 of a weight): over the keys that adds about as much to a row as the
 // output's own rounding; a second term for what is cut would add half to the products.
+//
+// Bounds and figures (a GB300 whose bf16 library products run at 1908 TFLOP/s in bursts, 1719 for seconds).  Two chunks
+// of 6000 tokens over prefixes of 1500 to 2000, 64 query over 8 KV heads: 1030 us in short bursts, 1.74 PFLOP/s of
+// products that a row needs (ncu: tensor pipe active 74 % of the time, issue 43 %); in long trains the card's power
+// limit lowers the clock from 1.9 to 1.72 GHz and a call takes 1145 us, 0.91 of the rate for seconds.  16 prompts of 64 to
+// 2000, 40 over 8 heads: 240 us, where the needed products alone are 139 and tiles on the diagonal, multiplied up to the last
+// sixteen keys seen, make them 155; a unit's last tile and output wait for each other (about 4 us of the 12 that
+// a unit takes here), and the dealing leaves the slowest CTA 10 % behind the middle one.  One prompt of 150 tokens takes 8.9 us,
+// latency.
+//   Tried and slower or no faster: units taken as CTAs come free (16 prompts -0.5 %, 64 short ones +14 %, one of 3000 tokens
+// +4 %), warps of their own for the output (16 prompts 267 us), P from the maximum of the tile before (longer code),
+// stores turned through shuffles, V in two stages.
 #include <math.h>
 #include <string.h>
 
@@ -484,7 +496,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       // For each key tile, of stream 0 and then of stream 1: P V of the tile before, in two halves, and S, which
       // overwrites P; the tensor pipe runs what a thread issues in order.  One thread for both streams
       // keeps them half a tile apart: with an issuer each they fell into step, the tensor core idle while both
-      // made their P (two chunks of 6000 tokens over prefixes 1616 us).  A commit holds the pipe up, so
+      // made their P (the two chunks took 1616 us then, 1328 with one).  A commit holds the pipe up, so
       // there is one to a stream and tile, and the softmax warps that see it give the tiles back.
       //   The whole warp walks, on values that are known to be alike in its lanes, so that descriptors are made in
       // uniform registers; one lane issues.
