@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
       }
     }
 
-    float o[8][NT][4], m[NT][2], top[NT][2], l[NT][2], ex[NT][2], lim[NT][2], wt[NT][2];
+    float o[8][NT][4], m[NT][2], top[NT][2], l[NT][2], up[NT][2], lim[NT][2], wt[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -349,15 +349,15 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[x][e] = 0.f;                         // 0 until a score is finite
-        top[x][e] = ex[x][e] = -INFINITY;      // m + 8; E
-        l[x][e] = lim[x][e] = wt[x][e] = 0.f;  // lim: 2^(14 + E - m), wt: 2^((m - E) / 2)
+        top[x][e] = -INFINITY;                 // m + 8
+        up[x][e] = INFINITY;                   // m - E, kept for E: beside a large m, E would be too coarse
+        l[x][e] = lim[x][e] = wt[x][e] = 0.f;  // lim: 2^(14 + E - m), wt: 2^((m - E) / 2), at most 2^100
       }
     }
-    auto follow = [&](int x, int e) {  // lim and wt after m or E has changed
-      const float d = m[x][e] - ex[x][e];
-      const bool none = ex[x][e] == -INFINITY;
-      lim[x][e] = none ? 0.f : fast_exp2(kQaMostLog2 - d);
-      wt[x][e] = none ? 0.f : fast_exp2(0.5f * d);
+    auto follow = [&](int x, int e, float d) {  // m or E has changed
+      up[x][e] = d;
+      lim[x][e] = fast_exp2(kQaMostLog2 - d);
+      wt[x][e] = fast_exp2(fminf(0.5f * d, 100.f));  // (beyond, lim is 0: every x is, or E follows)
     };
 
     int stage = 0;
@@ -415,9 +415,9 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
             const float mx = max_over_g(fmaxf(acc[x][e], acc[x][e + 2]));
             if (mx > top[x][e]) {  // (a head's result does not depend on the others)
               l[x][e] *= top[x][e] == -INFINITY ? 0.f : fast_exp2(m[x][e] - mx);
+              follow(x, e, up[x][e] + (mx - m[x][e]));
               m[x][e] = mx;
               top[x][e] = mx + kQaRaise;
-              follow(x, e);
             }
           }
       }
@@ -440,12 +440,10 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
           for (int e = 0; e < 2; ++e) {
             const float most = max_over_g(fmaxf(fabsf(y[x][e]), fabsf(y[x][e + 2])));
             if (most > lim[x][e] && most < INFINITY) {
-              // E to the nearest power of two at which the largest x is about 2^8
-              const float fresh = floorf(m[x][e] + log2f(most) - kQaFreshLog2);
-              if (fresh > ex[x][e]) {
-                const float f = fast_exp2(ex[x][e] - fresh);
-                ex[x][e] = fresh;
-                follow(x, e);
+              const float fresh = kQaFreshLog2 - log2f(most);  // the largest x is about 2^8 then
+              if (fresh < up[x][e]) {
+                const float f = fast_exp2(fresh - up[x][e]);
+                follow(x, e, fresh);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   o[i][x][e] *= f;
@@ -460,8 +458,8 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          pb[x][r] = movmatrix_t(pack_f16((acc[x][2 * r] * wt[x][0]) * (vs[r] * wt[x][0]),
-                                          (acc[x][2 * r + 1] * wt[x][1]) * (vs[r] * wt[x][1])));
+          pb[x][r] = movmatrix_t(pack_f16(acc[x][2 * r] * wt[x][0] * vs[r] * wt[x][0],
+                                          acc[x][2 * r + 1] * wt[x][1] * vs[r] * wt[x][1]));
       const uint32_t vb = st + kQaUnit * 128 + 2 * t * 128;
       const uint4 v0 = lds128(vb + ((g ^ (2 * t)) << 4)), v1 = lds128(vb + 128 + ((g ^ (2 * t + 1)) << 4)),
                   v2 = lds128(vb + 1024 + ((g ^ (2 * t)) << 4)), v3 = lds128(vb + 1152 + ((g ^ (2 * t + 1)) << 4));
@@ -493,7 +491,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(co
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int head = 8 * x + 2 * t + e;
-        const float f = ex[x][e] == -INFINITY ? 0.f : fast_exp2(0.5f * (ex[x][e] - m[x][e]));
+        const float f = fast_exp2(-0.5f * up[x][e]);
         const float fl = sum != 0.f ? f / sum : 0.f;
         float *row = rows + (warp * kHeads + head) * Smem::kRow + 16 * g;
 #pragma unroll

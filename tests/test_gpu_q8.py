@@ -408,6 +408,25 @@ def test_extreme_scales(power):
     assert err == 0 and bool((out != 0).any()) == bool((np.abs(ref) >= 2.0 ** -133).any())
 
 
+@pytest.mark.parametrize("power", [8, 26])
+@pytest.mark.parametrize("cap", [300, 2500])
+def test_a_key_far_above_the_others(cap, power):
+    """One slot's score is 2^(power + 3) and more above all others, which weigh nothing beside it: the output is its value, be that
+    zeros (nothing else may then be scaled up in its place) or far smaller or larger than the values before it."""
+    B, Hq, Hkv = 4, 12, 4
+    c = Cache(B, Hkv, cap, "int8", False)
+    q = rows_of(9, B, Hq).abs()
+    at = torch.arange(B, device="cuda") * cap + torch.tensor([200, 0, 76, 55], device="cuda")
+    c.k[at] = 127
+    c.ks[at] = 2.0 ** (power - 7)
+    c.vs[at[:, None], torch.arange(4, device="cuda")] *= torch.tensor([0.0, 1.0, 2.0 ** -40, 2.0 ** 40], device="cuda")
+    lens = [cap, cap - 1, 77, 60]
+    out, err = token(c, q, lens, Hq)
+    ref, mag = attend(c, q, lens, Hq)
+    near(out, ref, mag)
+    assert err == 0 and bool((out[:, :3] == 0).all())
+
+
 @pytest.mark.parametrize("cap", [300, 2500])
 def test_values_that_are_not_finite_reach_what_sees_them(cap):
     B, Hq, Hkv = 3, 8, 4
