@@ -54,7 +54,8 @@ typedef struct gqa_packed_desc {
  *              do (GQA_DEVERR_SEQLEN) counts as one without keys.
  * Keys and values that a query does not see have no effect on it whatever they hold (NaN and infinities
  * included).  A value that is not finite makes that dim of every query that sees it infinite or NaN, however
- * small its weight.  The rounding of the result does not depend on timing or on the other sequences of
+ * small its weight.  Scores are meant to be at most 2^29 in size (beyond, 2^ the rounding of the row's
+ * maximum leaves the range of the weights).  The rounding of the result does not depend on timing or on the other sequences of
  * the batch: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, bad sizes or strides), GQA_ERR_UNSUPPORTED
  * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, more than 2^31 - 1 rows N_q H_q or N_k H_kv, more than 2^26

@@ -258,3 +258,15 @@ def test_padding_and_replay():
         graph.replay()
         ref, mag = attend(w)
         near(out, ref, mag, norm=False)
+
+
+@pytest.mark.parametrize("power", [8, 12])
+def test_scores_far_apart(power):
+    """Scores of about 2^(2 power): most of the next lie so far below the largest that its value alone counts."""
+    w = make(20, 4, [300, 1, 77], [500, 1, 130], seed=21)
+    w["q"], w["k"] = w["q"] * 2.0 ** power, w["k"] * 2.0 ** power
+    for causal in (True, False):
+        out, err = run(w, causal)
+        ref, mag = attend(w, causal)
+        near(out, ref, mag)
+        assert err == 0
