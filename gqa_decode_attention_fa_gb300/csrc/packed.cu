@@ -665,7 +665,12 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         if ((j + 1) * kPkKeys > all_see) {
           const int left = sees - j * kPkKeys;
 #pragma unroll
-          for (int c = 0; c < kPkKeys; ++c) sv[c >> 5][c & 31] = c < left ? sv[c >> 5][c & 31] : -INFINITY;
+          for (int c = 0; c < kPkKeys; c += 32) {
+            const int here = min(max(left - c, 0), 32);
+            const uint32_t seen = here == 32 ? 0xffffffffu : (1u << here) - 1;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[c >> 5][e] = seen & (1u << e) ? sv[c >> 5][e] : -INFINITY;
+          }
         }
         float m4[4];
 #pragma unroll
