@@ -192,9 +192,11 @@ __device__ __forceinline__ float max_over_g(float x) {
 
 }  // namespace
 
-// NT: the heads of a KV head in eights.
+// NT: the heads of a KV head in eights.  Two CTAs an SM leave 128 threads' registers, so that CTAs of the merge start
+// beside them and have found their parts by their end (one sequence of 4000 tokens 10.1 us; with 128 registers 10.8, with 96
+// and three CTAs' room 10.6, and 8 sequences of 32k 99).
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kQaThreads, NT == 1 ? 2 : 1) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
+__global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
   using Smem = Q8Smem<NT>;
   constexpr int kStages = Smem::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -804,7 +806,7 @@ extern "C" gqa_status_t gqa_q8_attn(const gqa_q8_desc_t *desc, const void *q, co
                  static_cast<size_t>(wide ? Q8Smem<2>::kBytes : Q8Smem<1>::kBytes), s, p) != cudaSuccess ||
       (!y.whole && p.W > 1 &&
        (p.W <= 4LL * p.B ? launch_pdl(q8_merge_kernel<2>, dim3(static_cast<unsigned>(joins)), dim3(64), 0, s, p)
-                         : launch_pdl(q8_merge_kernel<8>, dim3(static_cast<unsigned>(joins)), dim3(256), 0, s, p)) != cudaSuccess)) {
+                         : launch_pdl(q8_merge_kernel<4>, dim3(static_cast<unsigned>(joins)), dim3(128), 0, s, p)) != cudaSuccess)) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
