@@ -23,8 +23,8 @@
 // of 6000 tokens over prefixes of 1500 to 2000, 64 query over 8 KV heads: 1030 us in short bursts, 1.74 PFLOP/s of
 // products that a row needs (ncu: tensor pipe active 74 % of the time, issue 43 %); in long trains the card's power
 // limit lowers the clock from 1.9 to 1.72 GHz and a call takes 1145 us, 0.91 of the rate for seconds.  16 prompts of 64 to
-// 2000, 40 over 8 heads: 240 us, where the needed products alone are 139 and tiles on the diagonal, multiplied up to the last
-// sixteen keys seen, make them 155; a unit's last tile and output wait for each other (about 4 us of the 12 that
+// 2000, 40 over 8 heads: 236 us, where the needed products alone are 139 and tiles on the diagonal, multiplied up to the last
+// sixteen keys seen, make them 155; a unit's last tile and output wait for each other (about 3 us of the 11.5 that
 // a unit takes here), and the dealing leaves the slowest CTA 10 % behind the middle one.  One prompt of 150 tokens takes 8.9 us,
 // latency.
 //   Tried and slower or no faster: units taken as CTAs come free (16 prompts -0.5 %, 64 short ones +14 %, one of 3000 tokens
