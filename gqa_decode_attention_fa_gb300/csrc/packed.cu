@@ -134,6 +134,13 @@ __device__ __forceinline__ void store_32b(uint16_t *dst, const uint32_t (&x)[8],
   }
 }
 
+// The larger sizes of two bf16 pairs, NaN where either is one; the signs mean nothing.
+__device__ __forceinline__ uint32_t max_abs_bf16(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
 // Queries and keys of sequence b; n = 0 where the offsets of the queries, m = 0 where those of the keys are
 // not in order.
 struct PackedSeq {
@@ -360,22 +367,19 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         const int later = x.nt[1] > 0 ? 1 : 0;
         const int first = max(x.see0, 0);
         const int last = min(x.nt[later] > 0 ? (x.nt[later] - 1) * kPkKeys + 16 * x.steps[later] : 0, p.Nk - x.k0);
-        bool bad = false;
         constexpr int kAhead = 8;
-        for (int r = first + (lane >> 4); r < last; r += 2 * kAhead) {
+        uint32_t most = 0;  // the largest sizes in its halves
+        const uint16_t *row = p.v + (x.k0 + first + (lane >> 4)) * p.v_stride + x.kv * kHeadDim + 8 * (lane & 15);
+        for (int left = last - first - (lane >> 4); left > 0; left -= 2 * kAhead) {
           uint4 y[kAhead];
-          uint32_t most = 0;
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i)
-            y[i] = r + 2 * i < last ? __ldg(reinterpret_cast<const uint4 *>(p.v + (x.k0 + r + 2 * i) * p.v_stride +
-                                                                            x.kv * kHeadDim + 8 * (lane & 15)))
-                                    : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < kAhead; ++i, row += 2 * p.v_stride)
+            y[i] = 2 * i < left ? __ldg(reinterpret_cast<const uint4 *>(row)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i)
-            most = __vmaxu2(most, __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
-                                           __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)));
-          bad |= max(most & 0xffffu, most >> 16) >= 0x7f80u;
+          for (int i = 0; i < kAhead; ++i) most = max_abs_bf16(most, max_abs_bf16(max_abs_bf16(y[i].x, y[i].y), max_abs_bf16(y[i].z, y[i].w)));
         }
+        most &= 0x7fff7fffu;
+        bool bad = max(most & 0xffffu, most >> 16) >= 0x7f80u;
         bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) {
           if (bad) sh.unit[slot.at].bad = 1;
