@@ -37,6 +37,7 @@
 #include <atomic>
 
 #include "../../include/gqa_packed.h"
+#include "divisor.cuh"
 #include "op_args.h"
 #include "pairmath.cuh"
 #include "tc05.cuh"
@@ -50,6 +51,7 @@ struct PackedParams {
   uint32_t *err;
   long long v_stride;
   int B, Nq, Nk, Hq, Hkv, G, Tt;
+  Divisor by_heads, by_unit;  // Hkv, 2 Tt
   int causal;
   int out_wide;  // `out` is 32-byte aligned
   float scale_log2;
@@ -158,7 +160,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const PackedParams &p, int b) {
   return s;
 }
 __device__ __forceinline__ int units_of(const PackedParams &p, const PackedSeq &s) {
-  return static_cast<int>(static_cast<unsigned>(s.n + 2 * p.Tt - 1) / static_cast<unsigned>(2 * p.Tt));
+  return static_cast<int>(p.by_unit.divide(static_cast<uint32_t>(s.n) + 2u * p.Tt - 1u));
 }
 // Units a KV head of a sequence of `all` units whose key tiles are at least D.
 __device__ __forceinline__ int units_of_depth(const PackedParams &p, const PackedSeq &s, int all, int D) {
@@ -168,7 +170,7 @@ __device__ __forceinline__ int units_of_depth(const PackedParams &p, const Packe
   if (!p.causal) return all;
   const int last = need - (s.m - s.n);  // queries, counted from the sequence's first, up to the unit's last
   if (last <= 0) return all;
-  return last > s.n ? 0 : all - static_cast<int>(static_cast<unsigned>(last - 1) / static_cast<unsigned>(2 * p.Tt));
+  return last > s.n ? 0 : all - static_cast<int>(p.by_unit.divide(static_cast<uint32_t>(last - 1)));
 }
 
 // Finds units by their number, which grows from call to call.  Every lane of a warp alike; the lanes keep
@@ -337,14 +339,15 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         PackedUnit x = {};
         PackedSeq s;
         int index = 0;
-        if (number < 0x7fffffffLL && walk.find(p, static_cast<int>(number / p.Hkv), lane, &s, &index)) {
+        const uint32_t at = p.by_heads.divide(static_cast<uint32_t>(number));
+        if (number < 0x7fffffffLL && walk.find(p, static_cast<int>(at), lane, &s, &index)) {
           const int t0 = index * 2 * p.Tt;
           x.q0 = s.q0 + t0;
           x.k0 = s.k0;
           x.tokens = min(2 * p.Tt, s.n - t0);
           x.see0 = p.causal ? t0 + 1 + s.m - s.n : s.m;
           x.keys = s.m;
-          x.kv = static_cast<int>(number % p.Hkv);
+          x.kv = static_cast<int>(static_cast<uint32_t>(number) - at * p.Hkv);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int rows = min(p.Tt, x.tokens - i * p.Tt);  // tokens of the tile
@@ -872,6 +875,8 @@ extern "C" gqa_status_t gqa_packed_attn(const gqa_packed_desc_t *desc, const voi
   p.Hkv = d.num_kv_heads;
   p.G = d.num_q_heads / d.num_kv_heads;
   p.Tt = kPkRows / p.G;
+  p.by_heads.set(p.Hkv);
+  p.by_unit.set(2 * p.Tt);
   p.causal = d.causal ? 1 : 0;
   p.out_wide = aligned_to(out, 32) ? 1 : 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(kHeadDim)));

@@ -19,26 +19,11 @@
 // 45 us, 16 rows a warp 2 % more than 8, 32 a third more.
 #include <string.h>
 
+#include "divisor.cuh"
 #include "pairmath.cuh"
 #include "q8.cuh"
 
 namespace gqa {
-
-// Division by a divisor known beforehand, 2 .. 2^31 (Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994).
-struct Divisor {
-  uint32_t factor, shift;
-  void set(uint32_t d) {
-    int l = 1;
-    while (l < 31 && (1u << l) < d) ++l;
-    factor = static_cast<uint32_t>((((1ull << l) - d) << 32) / d + 1);
-    shift = l - 1;
-  }
-  __host__ __device__ uint32_t divide(uint32_t a) const {
-    const uint32_t t = static_cast<uint32_t>((static_cast<uint64_t>(factor) * a) >> 32);
-    return (t + ((a - t) >> 1)) >> shift;
-  }
-};
 
 struct Q8RowsParams {
   const uint16_t *k, *v;  // append: the packed rows
