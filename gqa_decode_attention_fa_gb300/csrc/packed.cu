@@ -367,9 +367,9 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         // Behind the first query's last key a row of V is seen by some rows of the unit or, from the sequence's end to the last
         // sixteen that is multiplied, by none: P is 0 there, but 0 x inf is not.  Looked at here, ahead of time and in global
         // memory: shared memory is the MMAs' (a warp that looked at the tiles there took up to 5900 cycles a unit).
-        const int later = x.nt[1] > 0 ? 1 : 0;
+        const int nt = x.nt[1] > 0 ? x.nt[1] : x.nt[0], steps = x.nt[1] > 0 ? x.steps[1] : x.steps[0];
         const int first = max(x.see0, 0);
-        const int last = min(x.nt[later] > 0 ? (x.nt[later] - 1) * kPkKeys + 16 * x.steps[later] : 0, p.Nk - x.k0);
+        const int last = min(nt > 0 ? (nt - 1) * kPkKeys + 16 * steps : 0, p.Nk - x.k0);
         constexpr int kAhead = 8;
         uint32_t most = 0;  // the largest sizes in its halves
         const uint16_t *row = p.v + (x.k0 + first + (lane >> 4)) * p.v_stride + x.kv * kHeadDim + 8 * (lane & 15);
