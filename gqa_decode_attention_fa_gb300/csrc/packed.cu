@@ -66,7 +66,7 @@ constexpr int kPkUnitWarp = 9;
 constexpr int kPkProducerWarp = 10;
 constexpr int kPkCheckWarp = 11;
 constexpr int kPkThreads = 32 * 12;
-constexpr int kPkKStages = 2, kPkVStages = 3;
+constexpr int kPkKStages = 2, kPkVStages = 2;
 constexpr int kPkPanelBytes = kPkRows * kHalfRowBytes;  // 64 dims of 128 rows: 16 KiB
 constexpr int kPkTileBytes = 2 * kPkPanelBytes;
 constexpr int kPkSlots = 4;  // units told ahead
@@ -750,24 +750,22 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         uint16_t *dst = p.out + (static_cast<long long>(x.q0 + token) * p.Hq + x.kv * p.G + g) * kHeadDim;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 64) {
-          float o[2][32];
-          tmem_ld32(tm + kPkTmemO + c, o[0]);  // (not used where there was no tile)
-          tmem_ld32(tm + kPkTmemO + c + 32, o[1]);
+        for (int c = 0; c < kHeadDim; c += 32) {
+          float o[32];
+          tmem_ld32(tm + kPkTmemO + c, o);  // (not used where there was no tile)
           tmem_wait_ld();
-          if (c > 0 && nt > 0) {  // the next unit's P V may come
+          if (c == kHeadDim - 32 && nt > 0) {  // the next unit's P V may come
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.o_free[st]));
           }
           if (valid) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                y[e] = l_run != 0.f ? pack_bf16(o[i >> 1][16 * (i & 1) + 2 * e] * inv, o[i >> 1][16 * (i & 1) + 2 * e + 1] * inv)
-                                    : 0u;
+                y[e] = l_run != 0.f ? pack_bf16(o[16 * i + 2 * e] * inv, o[16 * i + 2 * e + 1] * inv) : 0u;
               store_32b(dst + c + 16 * i, y, p.out_wide);
             }
           }
