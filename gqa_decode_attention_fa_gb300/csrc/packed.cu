@@ -25,12 +25,13 @@
 // limit lowers the clock from 1.9 to 1.72 GHz and a call takes 1145 us, 0.91 of the rate for seconds.  16 prompts of 64 to
 // 2000, 40 over 8 heads: 233 us, where the needed products alone are 139 and tiles on the diagonal, multiplied up to the last
 // sixteen keys seen, make them 155; a unit's first scores, last products and output wait for each other (0.9, 0.5 and 1.1 us
-// of the 11 that a unit takes here), and the dealing leaves the slowest CTA 10 % behind the middle one.  One prompt of 150 tokens takes 8.4 us,
-// latency.
+// of the 11 that a unit takes here), and the dealing leaves the slowest CTA 10 % behind the middle one.  One prompt of 150 tokens
+// takes 8.4 us, latency.
 //   Tried and slower or no faster: units taken as CTAs come free (16 prompts -0.5 %, 64 short ones +14 %, one of 3000 tokens
 // +4 %), warps of their own for the output (16 prompts 267 us), P from the maximum of the tile before (longer code),
 // output rows turned through shuffles (no gain), through shared memory (16 prompts 2 % slower) or copied from there by TMA
-// (4 %), V in three stages; scores rounded before m is taken off them where m is beyond 2^26, so that
+// (4 %), V in three stages, the issue of MMAs rolled over the streams (64 short prompts -4 %, the two chunks +6 %), S of the
+// next unit before the other stream's last P V (no change); scores rounded before m is taken off them where m is beyond 2^26, so that
 // scores of any size keep their largest (8 % on the 16 prompts, the code again).
 #include <math.h>
 #include <string.h>
