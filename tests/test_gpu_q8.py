@@ -427,6 +427,34 @@ def test_a_key_far_above_the_others(cap, power):
     assert err == 0 and bool((out[:, :3] == 0).all())
 
 
+@pytest.mark.parametrize("fmt,Hq,Hkv,cap,lens", [
+    ("int8", 20, 4, 300, [300, 1, 150, 0, 47]),
+    ("e4m3", 40, 8, 300, [299, 64]),
+    ("int8", 8, 1, 2600, [2600, 900, 17]),
+    ("e4m3", 32, 2, 5000, [4100, 33]),
+])
+def test_scales_of_many_sizes(fmt, Hq, Hkv, cap, lens):
+    """V scales over 60 binades.  A product x of a weight and a scale is a binary16 number under a power of two by which the
+    largest is at least 2^8: half a step below 2^-14 is 2^-25, 2^-33 of the largest.  n of them, times codes of at most Q, may be off by
+    n Q 2^-33 of it, beside what `near` allows (twice that is: a warp's largest is its own)."""
+    c = Cache(len(lens), Hkv, cap, fmt, True, seed=5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    c.vs *= torch.exp2(torch.randint(-30, 30, c.vs.shape, generator=g, device="cuda").float())
+    q = rows_of(7, len(lens), Hq)
+    out, err = token(c, q, lens, Hq)
+    ref, mag = attend(c, q, lens, Hq)
+    K, _ = c.dense()
+    floor = np.zeros((len(lens), Hq, 1))
+    for b, n in enumerate(lens):
+        rows = c.slots(b, 0, n)
+        for h in range(Hq if n else 0):
+            s = (K[rows, h // (Hq // Hkv)] @ q[b, h].double().cpu().numpy()) / np.sqrt(D)
+            p = np.exp(s - s.max())
+            floor[b, h] = n * MOST[fmt] * 2.0 ** -32 * (p / p.sum() * c.vs[:, h // (Hq // Hkv)].double().cpu().numpy()[rows]).max()
+    near(out, ref, mag, floor)
+    assert err == 0
+
+
 @pytest.mark.parametrize("cap", [300, 2500])
 def test_values_that_are_not_finite_reach_what_sees_them(cap):
     B, Hq, Hkv = 3, 8, 4
