@@ -80,7 +80,7 @@ gqa_status_t gqa_q8_append(const gqa_q8_desc_t *desc, const void *k, const void 
                            const int32_t *slot_start, uint32_t *device_errors, void *stream);
 
 /*
- * gqa_q8_read -- rows of the cache as bf16 (code * scale, rounded), packed.
+ * gqa_q8_read -- rows of the cache as bf16 (code * scale, rounded to binary32 and then to bf16), packed.
  *   k_codes, v_codes, k_scale, v_scale, page_table   the cache; read only
  *   offsets, slot_start   as in gqa_q8_append: row offsets[b] + i receives slot slot_start[b] + i of
  *              sequence b; slot_start NULL for 0
