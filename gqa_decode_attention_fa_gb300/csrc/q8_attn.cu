@@ -680,9 +680,10 @@ struct QaLayout {
   bool whole;
 };
 // A CTA to a sequence and KV head, its eight warps sharing the tokens, and nothing to join, where no sequence can be
-// long: 5 ns a token against 4 to 8 us for cuts, their ends and the merge.  (8 KV heads, us whole / cut: one sequence of
-// 700 tokens 8.4 / 9.3, of 1500 13.0 / 9.3; 16 sequences of up to 1500 12.6 / 17.6, of up to 2500 18.3 / 21.3, of up to 4500
-// 29.5 / 30.3; 200 of up to 2500 108 / 115.)
+// long: 5 ns a token against 3 to 8 us for cuts, their ends and the merge.  (8 KV heads, us whole / cut: one sequence of
+// 500 tokens 7.0 / 8.7, of 700 8.2 / 9.0, of 850 9.0 / 8.8, of 1015 9.8 / 8.4; 4 of up to 1015 8.9 / 11.8; 16 of up to 1015
+// 9.6 / 15.0, of up to 1500 12.2 / 15.5, of up to 2500 18.7 / 19.5; 64 of up to 2500 42.8 / 40.6; 200 of up to 2500 96.9 / 97.7.)
+constexpr int kQaWholeTokensOne = 768;  // of a single sequence
 constexpr int kQaWholeTokens = 1024;
 constexpr int kQaWholeTokensMany = 2560, kQaMany = 128;  // where there are as many sequences and heads
 // KV heads of a CTA where sequences are cut: one, so that few parts are to be joined, but in wide caches, whose rows are
@@ -691,7 +692,7 @@ constexpr int kQaWholeTokensMany = 2560, kQaMany = 128;  // where there are as m
 QaLayout qa_layout(const gqa_q8_desc_t &d, int sms) {
   QaLayout y;
   const int G = d.num_q_heads / d.num_kv_heads;
-  y.whole = d.max_seq_len <= kQaWholeTokens ||
+  y.whole = d.max_seq_len <= (d.batch == 1 ? kQaWholeTokensOne : kQaWholeTokens) ||
             (d.max_seq_len <= kQaWholeTokensMany && static_cast<long long>(d.batch) * d.num_kv_heads >= kQaMany);
   y.hg = 1;
   if (!y.whole)
