@@ -65,6 +65,8 @@ constexpr int kQaMaxRanges = 640;
 constexpr float kQaRaise = 8.f;     // log2: how far a score may pass m
 constexpr float kQaMostLog2 = 14.f; // of x (binary16 holds 65504)
 constexpr float kQaFreshLog2 = 8.f; // of the largest x when E is set
+// Of 2^(m - E): a product p vs below 2^-150, which is 0 in binary32 and cannot be seen by E, is an x below 2^7 then.
+constexpr float kQaUpMost = 157.f;
 
 template <int NT>
 struct Q8Smem {
@@ -352,14 +354,14 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
       for (int e = 0; e < 2; ++e) {
         m[x][e] = 0.f;                         // 0 until a score is finite
         top[x][e] = -INFINITY;                 // m + 8
-        up[x][e] = INFINITY;                   // m - E, kept for E: beside a large m, E would be too coarse
-        l[x][e] = lim[x][e] = wt[x][e] = 0.f;  // lim: 2^(14 + E - m), wt: 2^((m - E) / 2), at most 2^100
+        up[x][e] = kQaUpMost;                  // m - E, kept for E: beside a large m, E would be too coarse
+        l[x][e] = lim[x][e] = wt[x][e] = 0.f;  // lim: 2^(14 + E - m), wt: 2^((m - E) / 2)
       }
     }
     auto follow = [&](int x, int e, float d) {  // m or E has changed
       up[x][e] = d;
       lim[x][e] = fast_exp2(kQaMostLog2 - d);
-      wt[x][e] = fast_exp2(fminf(0.5f * d, 100.f));  // (beyond, lim is 0: every x is, or E follows)
+      wt[x][e] = fast_exp2(0.5f * d);
     };
 
     int stage = 0;
@@ -416,8 +418,9 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
           for (int e = 0; e < 2; ++e) {
             const float mx = max_over_g(fmaxf(acc[x][e], acc[x][e + 2]));
             if (mx > top[x][e]) {  // (a head's result does not depend on the others)
-              l[x][e] *= top[x][e] == -INFINITY ? 0.f : fast_exp2(m[x][e] - mx);
-              follow(x, e, up[x][e] + (mx - m[x][e]));
+              const bool first = top[x][e] == -INFINITY;  // nothing has been summed
+              l[x][e] *= first ? 0.f : fast_exp2(m[x][e] - mx);
+              follow(x, e, first ? kQaUpMost : up[x][e] + (mx - m[x][e]));
               m[x][e] = mx;
               top[x][e] = mx + kQaRaise;
             }
@@ -425,6 +428,10 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
       }
       float y[NT][4];
       raise = false;
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) raise |= up[x][e] > kQaUpMost;  // (m has risen far)
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -441,16 +448,16 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float most = max_over_g(fmaxf(fabsf(y[x][e]), fabsf(y[x][e + 2])));
-            if (most > lim[x][e] && most < INFINITY) {
-              const float fresh = kQaFreshLog2 - log2f(most);  // the largest x is about 2^8 then
-              if (fresh < up[x][e]) {
-                const float f = fast_exp2(fresh - up[x][e]);
-                follow(x, e, fresh);
+            float fresh = kQaUpMost;
+            if (most > lim[x][e] && most < INFINITY)
+              fresh = fminf(fresh, kQaFreshLog2 - log2f(most));  // the largest x is about 2^8 then
+            if (fresh < up[x][e]) {
+              const float f = fast_exp2(fresh - up[x][e]);
+              follow(x, e, fresh);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  o[i][x][e] *= f;
-                  o[i][x][e + 2] *= f;
-                }
+              for (int i = 0; i < 8; ++i) {
+                o[i][x][e] *= f;
+                o[i][x][e + 2] *= f;
               }
             }
           }

@@ -117,8 +117,9 @@ gqa_status_t gqa_q8_workspace_bytes(const gqa_q8_desc_t *desc, size_t *bytes);
  *              that page as zeros.
  * Slots from seq_lens[b] on have no effect whatever they hold.  A scale that is not finite, or an e4m3
  * code that is no number, makes what depends on it infinite or NaN.  A weight times its V scale is kept
- * to 2^-11 of itself or 2^-33 of the head's largest such product, whichever is more.  The rounding of the
- * result does not depend on timing: the same inputs give the same bits.
+ * to 2^-11 of itself, 2^-33 of the head's largest such product or 2^-182, whichever is most; a weight below 2^-118
+ * of the head's largest may count as 0.  The rounding of the result does not depend on timing: the same
+ * inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (as gqa_q8_append; also H_q % H_kv != 0, H_q / H_kv >
  * 16, B (ceil(max_seq_len / 16) + 8) or max(B, 640) H_q above 2^31 - 1), GQA_ERR_CUDA.
  */
