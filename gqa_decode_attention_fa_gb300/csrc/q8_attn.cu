@@ -29,6 +29,7 @@
 // join of 38 parts a head.  32 sequences of 512 to 8192 in pages take 52 us, 5.4 TB/s.  One sequence of 256 takes 5.3 us on the
 // device and 8.6 from one call to the next, which is the host's.  At the long calls neither the
 // instruction issue (42 % used) nor the MMAs (16 %) is near a limit.
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
     }
     auto follow = [&](int x, int e, float d) {  // m or E has changed
       up[x][e] = d;
-      lim[x][e] = fast_exp2(kQaMostLog2 - d);
+      lim[x][e] = fminf(fast_exp2(kQaMostLog2 - d), FLT_MAX);  // (a p vs that is infinite passes it)
       wt[x][e] = fast_exp2(0.5f * d);
     };
 
@@ -447,10 +448,10 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float most = max_over_g(fmaxf(fabsf(y[x][e]), fabsf(y[x][e + 2])));
-            float fresh = kQaUpMost;
-            if (most > lim[x][e] && most < INFINITY)
-              fresh = fminf(fresh, kQaFreshLog2 - log2f(most));  // the largest x is about 2^8 then
+            // the largest p vs, by its logarithm: it may pass binary32's range where the result does not
+            const float most = max_over_g(fmaxf(log2f(acc[x][e]) + log2f(fabsf(vs[0])), log2f(acc[x][e + 2]) + log2f(fabsf(vs[1]))));
+            float fresh = fminf(up[x][e], kQaUpMost);
+            if (most + fresh > kQaMostLog2 && most < INFINITY) fresh = kQaFreshLog2 - most;  // the largest x is about 2^8 then
             if (fresh < up[x][e]) {
               const float f = fast_exp2(fresh - up[x][e]);
               follow(x, e, fresh);

@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_q8 import Cache, MOST, D, near, rows_of, token, values
+from test_gpu_q8 import Cache, MOST, D, near, token, values
 
 pytestmark = pytest.mark.gpu
 CODE = 64.0  # of a key's one dim: a level of both formats
@@ -108,3 +108,21 @@ def test_weights_and_scales_of_many_sizes(fmt, cap):
     zero = draw(0, 3) == 0
     vs[zero] = 0
     check(c, scored(c, scores, Hq), [cap, 77, cap - 1] * 2, 210)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("cap", [300, 2500])
+def test_a_weight_times_a_large_scale(fmt, cap):
+    """V rows of 3e38: a weight of up to 2^8, which a key has whose score passes the maximum held by less than 8 (log2), times
+    their scales is beyond binary32, their mean is not."""
+    B, Hq, Hkv = 2, 4, 2
+    c = Cache(B, Hkv, cap, fmt, False)
+    slot = torch.arange(cap, device="cuda")
+    scores = torch.zeros(B, cap, Hkv, device="cuda", dtype=torch.float64)
+    top = slot == 16 * 8 + 5                    # in the second unit of a warp
+    scores[:, top] = 7.9 * np.log(2.0)
+    c.vs = torch.full_like(c.vs, 1e20)
+    c.vs.view(B, cap, Hkv)[:, top] = 3e38 / MOST[fmt]
+    c.v.view(B, cap, Hkv, D)[:, top, :, ::2] = torch.tensor(MOST[fmt], device="cuda").to(c.v.dtype)
+    out = check(c, scored(c, scores, Hq), [cap, 200], 6)
+    assert bool((out[1, :, ::2] > 1e38).all())
