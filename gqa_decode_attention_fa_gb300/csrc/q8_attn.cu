@@ -523,18 +523,17 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
       }
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       const float mm = M == -INFINITY ? 0.f : M;
-      for (int s = 0; s < wph; ++s) {
+      for (int s = 0; s < wph; ++s) sum += fast_exp2(ml[(s * p.hg + hq) * kHeads + head] - mm);
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      for (int s = 0; s < wph; ++s) {  // (weights of 1 in all: values near the largest number stay below it)
         const int from = (s * p.hg + hq) * kHeads + head;
-        const float f = fast_exp2(ml[from] - mm);
+        const float f = fast_exp2(ml[from] - mm) * inv;
         const float4 y = *reinterpret_cast<const float4 *>(rows + from * Smem::kRow + d);
-        sum += f;
         a.x = fmaf(f, y.x, a.x);
         a.y = fmaf(f, y.y, a.y);
         a.z = fmaf(f, y.z, a.z);
         a.w = fmaf(f, y.w, a.w);
       }
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
-      a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
       const int h = h0 + hq;
       if (whole) {
         *reinterpret_cast<uint2 *>(p.out + (static_cast<long long>(b) * p.Hq + h * p.G + head) * kHeadDim + d) =
@@ -566,7 +565,6 @@ template <int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
   __shared__ float s_w[kQaMaxRanges];
   __shared__ float4 s_o[kWarps][32];
-  __shared__ float s_sum[kWarps];
   __shared__ int s_what[3];  // sequence, first range, parts
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hq = static_cast<int>(blockIdx.x) % p.Hq, index = static_cast<int>(blockIdx.x) / p.Hq;
@@ -614,27 +612,38 @@ __global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const __grid_cons
     }
   };
   fetch(warp);
-  // every warp finds M by itself
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) {
-    const float x = __ldcg(part(k) + p.G * kHeadDim + head);
-    if (warp == 0) s_w[k] = x;
-    M = fmaxf(M, x);
-  }
+  if (warp == 0) {  // the weights, 1 in all, so that values near the largest number stay below it
+    constexpr int kHeld = 2;  // of a lane's parts in registers
+    float x[kHeld];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (M == -INFINITY) M = 0.f;
+    for (int i = 0; i < kHeld; ++i)
+      x[i] = lane + 32 * i < parts ? __ldcg(part(lane + 32 * i) + p.G * kHeadDim + head) : -INFINITY;
+    float M = fmaxf(x[0], x[1]);
+    for (int k = lane + 32 * kHeld; k < parts; k += 32) M = fmaxf(M, s_w[k] = __ldcg(part(k) + p.G * kHeadDim + head));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) sum += x[i] = fast_exp2(x[i] - M);
+    for (int k = lane + 32 * kHeld; k < parts; k += 32) sum += s_w[k] = fast_exp2(s_w[k] - M);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (lane + 32 * i < parts) s_w[lane + 32 * i] = x[i] * inv;
+    for (int k = lane + 32 * kHeld; k < parts; k += 32) s_w[k] *= inv;
+  }
   __syncthreads();
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
   for (int k0 = warp; k0 < parts; k0 += kAhead * kWarps) {
     if (k0 > warp) fetch(k0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int k = k0 + i * kWarps;
       if (k >= parts) break;
-      const float f = fast_exp2(s_w[k] - M);
-      sum += f;
+      const float f = s_w[k];
       a.x = fmaf(f, y[i].x, a.x);
       a.y = fmaf(f, y[i].y, a.y);
       a.z = fmaf(f, y[i].z, a.z);
@@ -642,17 +651,14 @@ __global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const __grid_cons
     }
   }
   s_o[warp][lane] = a;
-  if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
   if (warp != 0) return;
   for (int x = 1; x < kWarps; ++x) {
     const float4 y = s_o[x][lane];
     a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
-    sum += s_sum[x];
   }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   *reinterpret_cast<uint2 *>(p.out + (static_cast<long long>(b) * p.Hq + hq) * kHeadDim + 4 * lane) =
-      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
 }
 
 // --------------------------------------------------------------------------------- host side

@@ -126,3 +126,17 @@ def test_a_weight_times_a_large_scale(fmt, cap):
     c.v.view(B, cap, Hkv, D)[:, top, :, ::2] = torch.tensor(MOST[fmt], device="cuda").to(c.v.dtype)
     out = check(c, scored(c, scores, Hq), [cap, 200], 6)
     assert bool((out[1, :, ::2] > 1e38).all())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hkv,cap", [(2, 300), (2, 2500), (1, 40000)])
+def test_means_near_the_largest_number(fmt, Hkv, cap):
+    """All V rows alike, of 3e38: so is their mean, whatever the warps and ranges (a hundred in the longest) it is joined from."""
+    B, Hq = 3, 4
+    c = Cache(B, Hkv, cap, fmt, False)
+    c.vs = torch.full_like(c.vs, 3e38 / MOST[fmt])
+    sign = 1 - 2 * (torch.arange(D, device="cuda") % 2).float()
+    c.v.view(B, cap, Hkv, D)[:] = (MOST[fmt] * sign).to(c.v.dtype)
+    scores = torch.randn(B, cap, Hkv, device="cuda", dtype=torch.float64, generator=torch.Generator(device="cuda").manual_seed(2))
+    out = check(c, scored(c, scores, Hq), [cap, 33, cap - 17], 6)
+    assert bool((out.abs() > 2.9e38).all())
