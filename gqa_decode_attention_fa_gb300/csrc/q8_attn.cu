@@ -6,7 +6,8 @@
 // cost whatever the sequence boundaries; the lengths are read on the device.  A CTA streams a range for
 // `hg` neighbouring KV heads: its eight warps take a head each, or share a head's units in turn.  A piece
 // of a range that is a whole sequence writes its output rows, one that is cut leaves its normalised
-// output and log-sum in the workspace for q8_merge_kernel.
+// output, its maximum and its sum in the workspace for q8_merge_kernel.  (The two apart: beside a large maximum the
+// logarithm of a sum has no bits left.)
 //
 // A warp works alone between the ends of its pieces: a ring of stages of its own in shared memory, filled by
 // asynchronous 16-byte copies (16 tokens of K, of V and their scales a stage; rows in 16-byte chunks permuted by
@@ -45,7 +46,7 @@ struct Q8AttnParams {
   const float *k_scale, *v_scale;
   const int32_t *page_table, *seq_lens;
   uint16_t *out;
-  float *part;  // [W][Hkv][2] (G x 128 outputs, G log-sums) of cut pieces
+  float *part;  // [W][Hkv][2] (G x 128 outputs, G maxima, G sums, 2 G unused) of cut pieces
   uint32_t *err;
   int B, Hq, Hkv, G;
   int hg;       // KV heads of a CTA
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
     __syncthreads();
     float *const rows = reinterpret_cast<float *>(smem_raw);
     constexpr int kHeads = 8 * NT;
-    float *const ml = rows + kQaWarps * kHeads * Smem::kRow;
+    float *const ml = rows + kQaWarps * kHeads * Smem::kRow, *const sl = ml + kQaWarps * kHeads;  // maxima and sums
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -509,25 +510,27 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
           const float y0 = o[i][x][e] * f * fl, y1 = o[i][x][e + 2] * f * fl;
           *reinterpret_cast<float2 *>(row + 2 * i) = sum != 0.f ? make_float2(y0, y1) : make_float2(0.f, 0.f);
         }
-        // log2 of the sum; -infinity where nothing counts
-        if (g == 0) ml[warp * kHeads + head] = sum != 0.f ? m[x][e] + log2f(sum) : -INFINITY;
+        if (g == 0) {
+          ml[warp * kHeads + head] = sum != 0.f ? m[x][e] : -INFINITY;  // nothing counts
+          sl[warp * kHeads + head] = sum;
+        }
       }
     __syncthreads();
     const bool whole = j0 == 0 && j1 == nu;
     for (int c = tid; c < p.hg * p.G * (kHeadDim / 4); c += kQaThreads) {
       const int d = 4 * (c & 31), hh = c >> 5, hq = hh / p.G, head = hh - hq * p.G;
       float M = -INFINITY, sum = 0.f;
-      for (int s = 0; s < wph; ++s) {
-        const float x = ml[(s * p.hg + hq) * kHeads + head];
-        M = x > M || x != x ? x : M;
-      }
+      for (int s = 0; s < wph; ++s) M = fmaxf(M, ml[(s * p.hg + hq) * kHeads + head]);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       const float mm = M == -INFINITY ? 0.f : M;
-      for (int s = 0; s < wph; ++s) sum += fast_exp2(ml[(s * p.hg + hq) * kHeads + head] - mm);
+      for (int s = 0; s < wph; ++s) {
+        const int from = (s * p.hg + hq) * kHeads + head;
+        sum = fmaf(fast_exp2(ml[from] - mm), sl[from], sum);
+      }
       const float inv = sum != 0.f ? 1.f / sum : 0.f;
       for (int s = 0; s < wph; ++s) {  // (weights of 1 in all: values near the largest number stay below it)
         const int from = (s * p.hg + hq) * kHeads + head;
-        const float f = fast_exp2(ml[from] - mm) * inv;
+        const float f = fast_exp2(ml[from] - mm) * sl[from] * inv;
         const float4 y = *reinterpret_cast<const float4 *>(rows + from * Smem::kRow + d);
         a.x = fmaf(f, y.x, a.x);
         a.y = fmaf(f, y.y, a.y);
@@ -541,7 +544,10 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
       } else {
         float *mine = p.part + ((static_cast<long long>(w) * p.Hkv + h) * 2 + (j0 > 0 ? 0 : 1)) * p.G * (kHeadDim + 4);
         *reinterpret_cast<float4 *>(mine + head * kHeadDim + d) = a;
-        if (d == 0) mine[p.G * kHeadDim + head] = sum != 0.f ? mm + log2f(sum) : -INFINITY;
+        if (d == 0) {
+          mine[p.G * kHeadDim + head] = M;
+          mine[p.G * (kHeadDim + 1) + head] = sum;
+        }
       }
     }
     __syncthreads();  // the ring is filled anew
@@ -557,8 +563,8 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
 }
 
 // ------------------------------------------------------------------------------------ merge
-// out = sum_k 2^(s_k - M) o_k / sum_k 2^(s_k - M) over the parts k of a cut sequence (s_k: log-sum, o_k: its normalised
-// output), in the order of the ranges.  A CTA joins one (sequence, query head): warp x of kWarps takes the parts x, x +
+// out = sum_k 2^(m_k - M) l_k o_k / sum_k 2^(m_k - M) l_k over the parts k of a cut sequence (m_k: maximum, l_k: sum, o_k: its
+// normalised output), in the order of the ranges.  A CTA joins one (sequence, query head): warp x of kWarps takes the parts x, x +
 // kWarps, ..., a lane four dims; the warps' sums are added in order.  One warp finds what to join: with all of them
 // looking, the 32 ragged sequences above took 56.5 us.
 template <int kWarps>
@@ -614,19 +620,23 @@ __global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const __grid_cons
   fetch(warp);
   if (warp == 0) {  // the weights, 1 in all, so that values near the largest number stay below it
     constexpr int kHeld = 2;  // of a lane's parts in registers
-    float x[kHeld];
+    float x[kHeld], l[kHeld];
+    auto max_of = [&](int k) { return __ldcg(part(k) + p.G * kHeadDim + head); };
+    auto sum_of = [&](int k) { return __ldcg(part(k) + p.G * (kHeadDim + 1) + head); };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      x[i] = lane + 32 * i < parts ? __ldcg(part(lane + 32 * i) + p.G * kHeadDim + head) : -INFINITY;
+    for (int i = 0; i < kHeld; ++i) {
+      x[i] = lane + 32 * i < parts ? max_of(lane + 32 * i) : -INFINITY;
+      l[i] = lane + 32 * i < parts ? sum_of(lane + 32 * i) : 0.f;
+    }
     float M = fmaxf(x[0], x[1]);
-    for (int k = lane + 32 * kHeld; k < parts; k += 32) M = fmaxf(M, s_w[k] = __ldcg(part(k) + p.G * kHeadDim + head));
+    for (int k = lane + 32 * kHeld; k < parts; k += 32) M = fmaxf(M, s_w[k] = max_of(k));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M == -INFINITY) M = 0.f;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) sum += x[i] = fast_exp2(x[i] - M);
-    for (int k = lane + 32 * kHeld; k < parts; k += 32) sum += s_w[k] = fast_exp2(s_w[k] - M);
+    for (int i = 0; i < kHeld; ++i) sum += x[i] = fast_exp2(x[i] - M) * l[i];
+    for (int k = lane + 32 * kHeld; k < parts; k += 32) sum += s_w[k] = fast_exp2(s_w[k] - M) * sum_of(k);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = sum != 0.f ? 1.f / sum : 0.f;

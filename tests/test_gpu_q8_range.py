@@ -140,3 +140,18 @@ def test_means_near_the_largest_number(fmt, Hkv, cap):
     scores = torch.randn(B, cap, Hkv, device="cuda", dtype=torch.float64, generator=torch.Generator(device="cuda").manual_seed(2))
     out = check(c, scored(c, scores, Hq), [cap, 33, cap - 17], 6)
     assert bool((out.abs() > 2.9e38).all())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hkv,cap", [(3, 300), (3, 2500), (1, 40000)])
+@pytest.mark.parametrize("power", [0, 12, 20, 26, 30, 100])
+def test_tied_keys_with_large_scores(fmt, Hkv, cap, power):
+    """Keys with one score of 2^power (log2), spread unevenly over warps and ranges, all others 0: the mean of their values.  (At
+    2^0 the others have weights too.)"""
+    B, Hq = 3, 6
+    c = Cache(B, Hkv, cap, fmt, False)
+    scores = torch.zeros(B, cap, Hkv, device="cuda", dtype=torch.float64)
+    at = [4, 5, 7, 30, cap // 2, cap // 2 + 1, cap - 90, cap - 89, cap - 88, cap - 87, cap - 86, cap - 40, cap - 11]
+    scores[:, at] = 2.0 ** power * np.log(2.0)
+    # (bit-equal scores: the others lie 2^power below, beyond every weight but at 2^0, so their size is no source of error)
+    check(c, scored(c, scores, Hq), [cap, cap - 20, cap - 87], 2)
