@@ -64,6 +64,7 @@ constexpr int kQaThreads = 32 * kQaWarps;
 constexpr int kQaUnit = 16;                              // tokens of a stage
 constexpr int kQaStageBytes = 2 * kQaUnit * 128 + 2 * kQaUnit * 4;  // K, V, scales of K, of V
 constexpr int kQaMaxRanges = 640;
+constexpr int kQaPieceCost = 3;     // of a piece's end, in units of a warp
 constexpr float kQaRaise = 8.f;     // log2: how far a score may pass m
 constexpr float kQaMostLog2 = 14.f; // of x (binary16 holds 65504)
 constexpr float kQaFreshLog2 = 8.f; // of the largest x when E is set
@@ -118,7 +119,7 @@ __device__ __forceinline__ Q8Cut q8_cut(const Q8AttnParams &p, int lane) {
   Q8Cut c;
   c.ranges = all < 1 ? 0 : max(1, min(p.W, all / (2 * wph)));
   const int quarter = c.ranges > 0 ? all / c.ranges / 4 : 0;
-  c.gap = min(quarter, 3 * wph);
+  c.gap = min(quarter, kQaPieceCost * wph);
   c.whole = c.ranges > 0 && all_seqs <= p.W && longest <= all / c.ranges + c.gap * all_seqs / c.ranges + 2 * wph;
   if (c.whole) c.ranges = all_seqs;
   const int total = c.whole ? all_seqs : all + c.gap * max(0, all_seqs - 1);
@@ -743,7 +744,7 @@ gqa_status_t qa_check(const gqa_q8_desc_t &d) {
   const gqa_status_t st = q8_check(d, true);
   if (st != GQA_OK) return st;
   // grid sizes, and the numbers of the batch's units with their gaps, are int32
-  const long long units = static_cast<long long>(d.batch) * ((d.max_seq_len - 1) / kQaUnit + 1 + kQaWarps);
+  const long long units = static_cast<long long>(d.batch) * ((d.max_seq_len - 1) / kQaUnit + 1 + kQaPieceCost * kQaWarps);
   return units > 0x7fffffffLL || static_cast<long long>(d.batch > kQaMaxRanges ? d.batch : kQaMaxRanges) * d.num_q_heads > 0x7fffffffLL
              ? GQA_ERR_UNSUPPORTED
              : GQA_OK;

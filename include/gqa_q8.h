@@ -121,7 +121,7 @@ gqa_status_t gqa_q8_workspace_bytes(const gqa_q8_desc_t *desc, size_t *bytes);
  * of the head's largest may count as 0.  The rounding of the result does not depend on timing: the same
  * inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG, GQA_ERR_UNSUPPORTED (as gqa_q8_append; also H_q % H_kv != 0, H_q / H_kv >
- * 16, B (ceil(max_seq_len / 16) + 8) or max(B, 640) H_q above 2^31 - 1), GQA_ERR_CUDA.
+ * 16, B (ceil(max_seq_len / 16) + 24) or max(B, 640) H_q above 2^31 - 1), GQA_ERR_CUDA.
  */
 gqa_status_t gqa_q8_attn(const gqa_q8_desc_t *desc, const void *q, const void *k_codes, const void *v_codes,
                          const float *k_scale, const float *v_scale, const int32_t *page_table,

@@ -79,6 +79,20 @@ def test_attn_refuses_bad_geometry(over, status):
     assert _attn(**over) == (status, status)
 
 
+@pytest.mark.parametrize("num_kv_heads", [1, 2, 64])
+@pytest.mark.parametrize("batch", [300, 1023, 1024])
+def test_attn_counts_the_numbers_of_a_batch(batch, num_kv_heads):
+    """The batch's units of 16 tokens, with 24 numbers behind each sequence (the end of a piece that eight warps share, 3 units of each
+    warp), are fewer than 2^31: the last capacity that keeps to it, and the next."""
+    units = (2 ** 31 - 1) // batch - 24
+    geometry = dict(batch=batch, num_q_heads=num_kv_heads, num_kv_heads=num_kv_heads, block_size=64, num_cache_blocks=1)
+    n = ctypes.c_size_t()
+    sized = lambda cap: binding.load().gqa_q8_workspace_bytes(_desc(dict(geometry, max_seq_len=cap))[1], ctypes.byref(n))  # noqa: E731
+    assert sized(16 * units) != UNS  # (not called: on a device it would run)
+    assert sized(16 * units + 1) == UNS
+    assert _attn(max_seq_len=16 * units + 1, **geometry) == (UNS, UNS)
+
+
 def test_attn_refuses_bad_arguments():
     for name in ("q", "kc", "vc", "ks", "vs", "lens", "out", "ws"):
         assert _attn(args={name: None})[1] == INV
