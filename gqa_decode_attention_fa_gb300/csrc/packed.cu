@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         }
         ok = mbar_wait(smem_addr(&sh.unit_checked[slot.at][st]), slot.phase);
         const bool bad = *reinterpret_cast<volatile uint32_t *>(&sh.unit[slot.at].bad) != 0;
-        if (bad && valid && ok) packed_add_nonfinite(p, x.k0, x.kv, max(0, x.see0), sees, dst, inv);
+        if (bad && valid && ok && l_run != 0.f) packed_add_nonfinite(p, x.k0, x.kv, max(0, x.see0), sees, dst, inv);
       } else if (nt > 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.o_free[st]));

@@ -54,7 +54,7 @@ typedef struct gqa_packed_desc {
  *              do (GQA_DEVERR_SEQLEN) counts as one without keys.
  * Keys and values that a query does not see have no effect on it whatever they hold (NaN and infinities
  * included).  A value that is not finite makes that dim of every query that sees it infinite or NaN, however
- * small its weight.  Scores are meant to be at most 2^29 in size (beyond, 2^ the rounding of the row's
+ * small its weight, unless the query's every score is -infinity.  Scores are meant to be at most 2^29 in size (beyond, 2^ the rounding of the row's
  * maximum leaves the range of the weights).  The rounding of the result does not depend on timing or on the other sequences of
  * the batch: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, bad sizes or strides), GQA_ERR_UNSUPPORTED
