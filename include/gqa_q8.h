@@ -68,7 +68,8 @@ typedef struct gqa_q8_desc {
  *              sequence whose offsets descend or pass N, or whose last slot is beyond max_seq_len
  *              (GQA_DEVERR_SEQLEN), or with a negative slot_start (GQA_DEVERR_POSITION), stores
  *              nothing; a page id outside the pool (GQA_DEVERR_PAGE) stores nothing for the tokens
- *              there.
+ *              there.  Where offsets descend anywhere, rows of other sequences may be left out too (a row's
+ *              sequence is found by bisection); a row that is stored is stored where it belongs.
  * Every slot written must belong to its sequence alone (no shared page: gqa_pages.h).
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, page_table given for a contiguous cache
  * or missing for a paged one, bad sizes, strides or format, NULL offsets with N != B),

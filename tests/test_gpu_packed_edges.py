@@ -29,3 +29,35 @@ def test_rows_whose_every_score_is_minus_infinity(Hq, Hkv, causal):
     rest = torch.ones(int(at[-1]), dtype=torch.bool, device="cuda")
     rest[lone] = False
     assert err == 0 and bool((out[:at[-1]][rest] == 0).all()) and bool(torch.isnan(out[lone]).all())
+
+
+@pytest.mark.parametrize("qa,ka", [
+    ([0, 40, 20, 130, 180], None),
+    ([-5, 40, 100, 130, 180], None),
+    ([0, 40, 100, 130, 200], None),
+    ([10, 5, 60, 60, 170], None),
+    ([0, 40, 100, 130, 170], [0, 50, 30, 150, 181]),     # the keys' alone: a sequence without keys
+    ([0, 40, 30, 130, 170], [-1, 50, 60, 150, 999]),
+])
+def test_offsets_out_of_order(qa, ka):
+    """Each sequence by its own offsets: one with bad ones is left out, its rows and those of none as they were, the others as ever
+    (but in rows that two of them hold)."""
+    w = make(8, 2, [180], [180], seed=33)
+    N = len(w["out"])
+    w["qa"], w["ka"], w["given"] = np.array(qa), np.array(qa if ka is None else ka), ka is not None
+    out, err = run(w)
+    assert err == binding.DEVERR_SEQLEN
+    ref, mag, owners = w["out"].double().clone(), torch.zeros(w["out"].shape, dtype=torch.float64, device="cuda"), np.zeros(N, int)
+    for b in range(4):
+        (x, y), (j, k) = w["qa"][b:b + 2], w["ka"][b:b + 2]
+        if not 0 <= x <= y <= N:
+            continue
+        if not 0 <= j <= k <= N:
+            j = k = 0
+        owners[x:y] += 1
+        o, m = attend({**w, "qa": np.array([x, y]), "ka": np.array([j, k])})
+        ref[x:y], mag[x:y] = o[x:y], m[x:y]
+    one = torch.as_tensor(owners == 1, device="cuda")
+    near(out[one], ref[one], mag[one], norm=False)
+    none = torch.as_tensor(owners == 0, device="cuda")
+    assert bool(none.any()) and torch.equal(out[none], w["out"][none])
