@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) raise |= acc[x][e] > top[x][e & 1];
+      bool far = false;  // m has risen so that 2^(m - E) is beyond what it may be
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -426,15 +427,12 @@ __global__ void __launch_bounds__(kQaThreads) __maxnreg__(NT == 1 ? 112 : 255) q
               follow(x, e, first ? kQaUpMost : up[x][e] + (mx - m[x][e]));
               m[x][e] = mx;
               top[x][e] = mx + kQaRaise;
+              far |= up[x][e] > kQaUpMost;
             }
           }
       }
       float y[NT][4];
-      raise = false;
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) raise |= up[x][e] > kQaUpMost;  // (m has risen far)
+      raise = far;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -708,6 +706,8 @@ struct QaLayout {
 // long: 5 ns a token against 3 to 8 us for cuts, their ends and the merge.  (8 KV heads, us whole / cut: one sequence of
 // 500 tokens 7.0 / 8.7, of 700 8.2 / 9.0, of 850 9.0 / 8.8, of 1015 9.8 / 8.4; 4 of up to 1015 8.9 / 11.8; 16 of up to 1015
 // 9.6 / 15.0, of up to 1500 12.2 / 15.5, of up to 2500 18.7 / 19.5; 64 of up to 2500 42.8 / 40.6; 200 of up to 2500 96.9 / 97.7.)
+// The host knows the capacity alone, so short sequences in a cache for long ones are cut (unless the lengths let the device
+// take them whole): 16 of 1000 tokens take 12.3 us in a cache for 2048 tokens and 18.8 in one for 32768.
 constexpr int kQaWholeTokensOne = 768;  // of a single sequence
 constexpr int kQaWholeTokens = 1024;
 constexpr int kQaWholeTokensMany = 2560, kQaMany = 128;  // where there are as many sequences and heads
