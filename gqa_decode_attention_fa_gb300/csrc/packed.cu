@@ -16,15 +16,16 @@
 // memory, P over S as bf16 pairs in two halves, the first multiplied while the second is made.  A softmax thread holds a
 // row.  The maximum is raised lazily (by more than 2^8), so most tiles rescale nothing; S of a tile is issued behind P V of
 // the one before, so a thread that sees S finds O at rest.
-//   P is rounded to bf16 (at most 2^-8 of a weight): over the keys that adds about as much to a row as the
-// output's own rounding; a second term for what is cut would add half to the products.
+//   P is rounded to bf16 (at most 2^-8 of a weight) and the row divided by the sum of the weights as they were: over the
+// keys that adds about as much to a row as the output's own rounding; a second term for what is cut, as the chunked
+// prefill and the draft trees have, would add half to the products.
 //
 // Bounds and figures (a GB300 whose bf16 library products run at 1908 TFLOP/s in bursts, 1719 for seconds).  Two chunks
 // of 6000 tokens over prefixes of 1500 to 2000, 64 query over 8 KV heads: 1030 us in short bursts, 1.74 PFLOP/s of
 // products that a row needs (ncu: tensor pipe active 74 % of the time, issue 43 %); in long trains the card's power
 // limit lowers the clock from 1.9 to 1.72 GHz and a call takes 1145 us, 0.91 of the rate for seconds.  16 prompts of 64 to
-// 2000, 40 over 8 heads: 233 us, where the needed products alone are 139 and tiles on the diagonal, multiplied up to the last
-// sixteen keys seen, make them 155; a unit's first scores, last products and output wait for each other (0.9, 0.5 and 1.1 us
+// 2000, 40 over 8 heads: 233 us, where the needed products alone are 139 and tiles on the diagonal make them 155 (S over all
+// 128 keys, P V up to the last sixteen seen); a unit's first scores, last products and output wait for each other (0.9, 0.5 and 1.1 us
 // of the 11 that a unit takes here), and the dealing leaves the slowest CTA 10 % behind the middle one.  One prompt of 150 tokens
 // takes 8.4 us, latency.
 //   Tried and slower or no faster: units taken as CTAs come free (16 prompts -0.5 %, 64 short ones +14 %, one of 3000 tokens
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       constexpr uint32_t kIdO = idesc_bf16_f32(kPkRows, kHeadDim, false, true);
       const uint64_t qd0 = sdesc_sw128(smem_addr(smem), 16, 1024), kd0 = sdesc_sw128(k_ptr(0), 16, 1024),
                      vd0 = sdesc_sw128(v_ptr(0), kPkPanelBytes, 1024);
-      //   The walk runs on across the units: a unit's first S comes before the last P V of the unit before.
+      //   The walk runs on across the units: a unit's last P V come right before the next unit's first S.
       Ring<kPkKStages> ks;                                 // of the tile at hand
       Ring<kPkVStages> vs;                                 // of the tile before
       Ring<kPkSlots> slot;
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
   }
 
   // ------------------------------------------------------------------ teardown
-  __syncwarp();  // the MMA warps ran their loops on lane 0 alone
+  __syncwarp();  // the producer ran its loop on lane 0 alone
   tc_fence_before();
   __syncthreads();
   if (warp == kPkMmaWarp) {

@@ -27,9 +27,9 @@
 // of a head are 264 bytes, so the cache bounds long calls: 8 sequences of 32768 take 90 us (88 to 92 on different GPUs), 6.2 TB/s, 0.91 of the copy rate;
 // one of 131072 with 64 query heads over int8 codes 50 us, 5.5 TB/s, where the fixed costs show: 5.5 us from the launch to the first products
 // (1.7 of them the cut, the rest the first copies' way), 3 us from a range's last products to its partials, 6 us for the
-// join of 38 parts a head.  32 sequences of 512 to 8192 in pages take 52 us, 5.4 TB/s.  One sequence of 256 takes 5.3 us on the
-// device and 8.6 from one call to the next, which is the host's.  At the long calls neither the
-// instruction issue (42 % used) nor the MMAs (16 %) is near a limit.
+// join of 38 parts a head.  32 sequences of 512 to 8192 in pages take 52 us, 5.4 TB/s.  One sequence of 256 takes 5.0 us on the
+// device and 8.2 from one call to the next, which is the host's.  At the long calls neither the
+// instruction issue (45 % used) nor the MMAs (16 %) is near a limit.
 #include <float.h>
 #include <math.h>
 #include <string.h>

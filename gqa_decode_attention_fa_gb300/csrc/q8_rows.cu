@@ -14,9 +14,10 @@
 //   Bounds.  HBM, and the append its arithmetic too (20 instructions a value when each was divided: 32 us where this takes
 // 23): 19k tokens of 8 KV heads appended 23 us = 5.2 TB/s, 0.77 of the measured copy rate, 28k rows read back 28.6 us =
 // 6.0 TB/s, 0.88; small calls 2.2 to 2.8 us.  What counts is that many warps are on their way: an SM's 64 take 32
-// registers each (with 40 and 48 warps 26.8 us), a CTA has four (8: 23.1 us and 28.7, 16: 23.7 and 29.0), and one
-// of its warps looks for the places of all its rows (each warp for its own: 24.6 us).  Warps that stay and load ahead took 30 to
-// 45 us, 16 rows a warp 2 % more than 8, 32 a third more.
+// registers each (with 40 and 48 warps 26.8 us; held to 32 the append of 8 rows a warp stores seven words in local memory and
+// loads two), a CTA has four (8: 23.1 us and 28.7, 16: 23.7 and 29.0), and one of its warps looks for the places of all its
+// rows (each warp for its own: 24.6 us).  Warps that stay and load ahead took 30 to 45 us, 16 rows a warp 2 % more than 8, 32 a
+// third more.
 #include <string.h>
 
 #include "divisor.cuh"

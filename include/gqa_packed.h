@@ -54,9 +54,12 @@ typedef struct gqa_packed_desc {
  *              do (GQA_DEVERR_SEQLEN) counts as one without keys.
  * Keys and values that a query does not see have no effect on it whatever they hold (NaN and infinities
  * included).  A value that is not finite makes that dim of every query that sees it infinite or NaN, however
- * small its weight, unless the query's every score is -infinity.  Scores are meant to be at most 2^29 in size (beyond, 2^ the rounding of the row's
- * maximum leaves the range of the weights).  The rounding of the result does not depend on timing or on the other sequences of
- * the batch: the same inputs give the same bits.
+ * small its weight, unless the query's every score is -infinity.  The weights are rounded to bf16 (by at most 2^-8 of
+ * each) before V is multiplied, where gqa_prefill_attn and gqa_tree_attn keep 16 bits of them: with N(0, 1) inputs the
+ * result is off by 1.9e-3 to 2.3e-3 of itself in the 2-norm, 1.65e-3 there (the rounding of the output alone).
+ * Scores are meant to be at most 2^29 in size (beyond, 2^ the rounding of the row's maximum leaves the range of the
+ * weights), values at most 2^119 / m_b (they are added in binary32 under weights of up to 2^8).  The rounding of the
+ * result does not depend on timing or on the other sequences of the batch: the same inputs give the same bits.
  * Errors: GQA_ERR_INVALID_ARG (NULL or misaligned tensors, bad sizes or strides), GQA_ERR_UNSUPPORTED
  * (head_dim != 128, H_q % H_kv != 0, H_q / H_kv > 16, more than 2^31 - 1 rows N_q H_q or N_k H_kv, more than 2^26
  * keys), GQA_ERR_CUDA.
